@@ -17,3 +17,14 @@ from .ring_attn import (  # noqa: F401
     ring_attention,
     workspace_status,
 )
+from .kv_cache import (  # noqa: F401
+    Kv4Cache,
+    Kv4Tables,
+    kv4_attention,
+    kv4_attention_workspace,
+    kv4_load,
+    kv4_status,
+    kv4_store,
+    kv4_tables,
+    kv4_tables_out,
+)

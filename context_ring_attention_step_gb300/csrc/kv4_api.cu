@@ -1,0 +1,253 @@
+// kv4_api.cu -- C entry points of the 4-bit key/value cache: argument checks
+// and launches.  Nothing here allocates or synchronises (ra_kv4_status does).
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "../../include/ring_attn.h"
+#include "kv4.h"
+#include "ring_attn_internal.h"
+
+namespace {
+
+ra_status fail(ra_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return ra::set_last_error(st, buf);
+}
+ra_status cuda_fail(cudaError_t e, const char* what) { return fail(RA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr size_t kHeader = 256;
+constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int page_shift(int32_t page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+ra_status check_geometry(int64_t num_pages, int32_t page_size, int32_t Hkv, int32_t D) {
+  if (D != 64 && D != 128 && D != 256) return fail(RA_ERR_UNSUPPORTED, "head_dim %d: 64, 128 or 256", D);
+  if (page_shift(page_size) < 0) return fail(RA_ERR_UNSUPPORTED, "page_size %d: 16, 32, 64, 128 or 256", page_size);
+  if (Hkv < 1 || Hkv > 4096) return fail(RA_ERR_INVALID_ARG, "num_kv_heads %d outside [1, 4096]", Hkv);
+  if (num_pages < 1 || num_pages > (int64_t(1) << 30))
+    return fail(RA_ERR_INVALID_ARG, "num_pages %lld outside [1, 2^30]", (long long)num_pages);
+  return RA_OK;
+}
+
+ra_status check_cache(const ra_kv4_cache* c, ra::Kv4Cache* out) {
+  if (!c) return fail(RA_ERR_INVALID_ARG, "cache is NULL");
+  ra_status rs = check_geometry(c->num_pages, c->page_size, c->num_kv_heads, c->head_dim);
+  if (rs != RA_OK) return rs;
+  if (!c->pages || !aligned(c->pages, 16)) return fail(RA_ERR_INVALID_ARG, "pages must be a 16-byte aligned device pointer");
+  *out = ra::Kv4Cache{reinterpret_cast<uint8_t*>(c->pages), c->num_pages, page_shift(c->page_size), c->num_kv_heads};
+  return RA_OK;
+}
+
+size_t page_bytes(int32_t page_size, int32_t Hkv, int32_t D) {
+  return (size_t)(page_size / ra::kKv4Tile) * ra::kv4_tile_bytes(D) * Hkv;
+}
+
+struct AttnLayout {
+  size_t parts, partials, total;
+};
+AttnLayout attn_layout(int32_t D, int32_t G, int32_t max_q_len) {
+  const ra::Kv4AttnShape s = ra::kv4_attn_shape(D, G, max_q_len, ra::kKv4MaxSms);
+  AttnLayout l;
+  l.parts = kHeader;
+  l.partials = align256(l.parts + (size_t)s.ctas * sizeof(ra::Kv4Part));
+  l.total = align256(l.partials + (size_t)s.ctas * 2 * s.slot_floats * sizeof(float));
+  return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+ra_status ra_kv4_cache_bytes(int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                             size_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "NULL output");
+  ra_status rs = check_geometry(num_pages, page_size, num_kv_heads, head_dim);
+  if (rs != RA_OK) return rs;
+  *bytes = (size_t)num_pages * page_bytes(page_size, num_kv_heads, head_dim);
+  return RA_OK;
+}
+
+ra_status ra_kv4_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t num_requests, int32_t* block_table,
+                        int32_t table_width, int64_t table_stride, int32_t page_size, int32_t* free_pages,
+                        int32_t num_pages, const int32_t* free_count, int64_t num_slots, int32_t* kv_lens_out,
+                        int32_t* cu_new, int64_t* slot_map, int32_t* positions, int32_t* free_count_out,
+                        int32_t* status, void* stream) {
+  if (num_requests < 1 || num_requests > ra::kKv4MaxRequests)
+    return fail(RA_ERR_INVALID_ARG, "num_requests %d outside [1, %d]", num_requests, ra::kKv4MaxRequests);
+  if (page_shift(page_size) < 0) return fail(RA_ERR_UNSUPPORTED, "page_size %d: 16, 32, 64, 128 or 256", page_size);
+  if (table_width < 1 || table_stride < table_width)
+    return fail(RA_ERR_INVALID_ARG, "table_width %d, table_stride %lld: need 1 <= width <= stride", table_width,
+                (long long)table_stride);
+  if (num_slots < 0 || num_slots > (int64_t(1) << 30))
+    return fail(RA_ERR_INVALID_ARG, "num_slots %lld outside [0, 2^30]", (long long)num_slots);
+  if (!kv_lens || !new_lens || !block_table || !kv_lens_out || !cu_new || !status ||
+      (num_slots > 0 && (!slot_map || !positions)))
+    return fail(RA_ERR_INVALID_ARG, "NULL pointer");
+  if (free_pages && (!free_count || !free_count_out || num_pages < 1 || num_pages > (1 << 30)))
+    return fail(RA_ERR_INVALID_ARG, "a free list needs free_count, free_count_out and num_pages in [1, 2^30]");
+  const void* words[] = {kv_lens, new_lens, block_table, kv_lens_out, cu_new, status, positions, free_pages,
+                         free_count, free_count_out};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return fail(RA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  if (!aligned(slot_map, 8)) return fail(RA_ERR_INVALID_ARG, "slot_map must be 8-byte aligned");
+  if (kv_lens_out == new_lens) return fail(RA_ERR_INVALID_ARG, "kv_lens_out may replace kv_lens, not new_lens");
+  ra::Kv4TablesParams p{kv_lens, new_lens, block_table, table_stride, table_width, num_requests,
+                        page_shift(page_size), free_pages, num_pages, free_count, num_slots, kv_lens_out, cu_new,
+                        slot_map, positions, free_count_out, status};
+  const cudaError_t e = ra::launch_kv4_tables(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache tables launch");
+}
+
+static ra_status check_rows(const ra_kv4_cache* cache, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int64_t* slot_map, int64_t T, ra::Kv4RowsParams* p) {
+  ra_status rs = check_cache(cache, &p->cache);
+  if (rs != RA_OK) return rs;
+  if (T < 0 || T > (int64_t(1) << 31)) return fail(RA_ERR_INVALID_ARG, "num_tokens %lld outside [0, 2^31]", (long long)T);
+  if (T > 0 && (!k || !v || !slot_map)) return fail(RA_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(RA_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
+  if (!aligned(slot_map, 8)) return fail(RA_ERR_INVALID_ARG, "slot_map must be 8-byte aligned");
+  const int64_t row = (int64_t)cache->num_kv_heads * cache->head_dim;
+  if (T > 1 && (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8))
+    return fail(RA_ERR_INVALID_ARG, "row strides %lld, %lld: multiples of 8 elements, at least %lld",
+                (long long)k_stride, (long long)v_stride, (long long)row);
+  p->slots = slot_map;
+  p->T = T;
+  return RA_OK;
+}
+
+ra_status ra_kv4_store(const ra_kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       const int64_t* slot_map, int64_t num_tokens, void* stream) {
+  ra::Kv4RowsParams p{};
+  ra_status rs = check_rows(cache, k, k_stride, v, v_stride, slot_map, num_tokens, &p);
+  if (rs != RA_OK || num_tokens == 0) return rs;
+  p.k = k;
+  p.v = v;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  const cudaError_t e = ra::launch_kv4_store(cache->head_dim, p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache store launch");
+}
+
+ra_status ra_kv4_load(const ra_kv4_cache* cache, const int64_t* slot_map, int64_t num_tokens, void* k, void* v,
+                      void* stream) {
+  ra::Kv4RowsParams p{};
+  const int64_t row = cache ? (int64_t)cache->num_kv_heads * cache->head_dim : 0;
+  ra_status rs = check_rows(cache, k, row, v, row, slot_map, num_tokens, &p);
+  if (rs != RA_OK || num_tokens == 0) return rs;
+  p.k_out = k;
+  p.v_out = v;
+  const cudaError_t e = ra::launch_kv4_load(cache->head_dim, p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache load launch");
+}
+
+static ra_status check_heads(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q_len) {
+  if (D != 64 && D != 128 && D != 256) return fail(RA_ERR_UNSUPPORTED, "head_dim %d: 64, 128 or 256", D);
+  if (Hkv < 1 || Hq < 1 || Hq > 65536 || Hq % Hkv)
+    return fail(RA_ERR_INVALID_ARG, "num_q_heads %d must be a multiple of num_kv_heads %d", Hq, Hkv);
+  if (max_q_len < 1) return fail(RA_ERR_INVALID_ARG, "max_q_len %d must be at least 1", max_q_len);
+  return RA_OK;
+}
+
+ra_status ra_kv4_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                           int32_t max_q_len, size_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "NULL output");
+  ra_status rs = check_heads(num_q_heads, num_kv_heads, head_dim, max_q_len);
+  if (rs != RA_OK) return rs;
+  *bytes = attn_layout(head_dim, num_q_heads / num_kv_heads, max_q_len).total;
+  return RA_OK;
+}
+
+ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_stride, int32_t num_q_tokens,
+                           int32_t num_q_heads, const int32_t* block_table, int32_t table_width, int64_t table_stride,
+                           const int32_t* kv_lens, const int32_t* cu_q, int32_t num_requests, int32_t max_q_len,
+                           int32_t causal, float softmax_scale, void* o, int32_t o_is_fp32, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  ra::Kv4AttnParams p{};
+  ra_status rs = check_cache(cache, &p.cache);
+  if (rs != RA_OK) return rs;
+  const int32_t D = cache->head_dim, Hkv = cache->num_kv_heads;
+  rs = check_heads(num_q_heads, Hkv, D, max_q_len);
+  if (rs != RA_OK) return rs;
+  if (num_q_tokens < 0 || num_requests < 0)
+    return fail(RA_ERR_INVALID_ARG, "num_q_tokens %d, num_requests %d must not be negative", num_q_tokens, num_requests);
+  if (table_width < 1 || table_stride < table_width)
+    return fail(RA_ERR_INVALID_ARG, "table_width %d, table_stride %lld: need 1 <= width <= stride", table_width,
+                (long long)table_stride);
+  const AttnLayout l = attn_layout(D, num_q_heads / Hkv, max_q_len);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total)
+    return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes: need %zu, 256-byte aligned", workspace ? workspace_bytes : 0,
+                l.total);
+  if (num_q_tokens == 0 || num_requests == 0) {  // no row to write; the status is still this call's
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, "status reset");
+  }
+  if (!q || !o || !lse || !block_table || !kv_lens || !cu_q) return fail(RA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
+      !aligned(cu_q, 4))
+    return fail(RA_ERR_INVALID_ARG, "q and o must be 16-byte aligned, the other arrays 4-byte aligned");
+  const int64_t row = (int64_t)num_q_heads * D;
+  if (num_q_tokens > 1 && (q_stride < row || q_stride % 8))
+    return fail(RA_ERR_INVALID_ARG, "q row stride %lld: a multiple of 8 elements, at least %lld", (long long)q_stride,
+                (long long)row);
+  if (!std::isfinite(softmax_scale)) return fail(RA_ERR_INVALID_ARG, "softmax_scale is not finite");
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  p.q = q;
+  p.q_stride = q_stride;
+  p.Tq = num_q_tokens;
+  p.Hq = num_q_heads;
+  p.R = num_requests;
+  p.causal = causal != 0;
+  p.block_table = block_table;
+  p.table_stride = table_stride;
+  p.table_width = table_width;
+  p.kv_lens = kv_lens;
+  p.cu_q = cu_q;
+  p.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D);
+  p.o = o;
+  p.o_is_fp32 = o_is_fp32 != 0;
+  p.lse = lse;
+  p.status = reinterpret_cast<int32_t*>(ws);
+  p.parts = reinterpret_cast<ra::Kv4Part*>(ws + l.parts);
+  p.partials = reinterpret_cast<float*>(ws + l.partials);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  e = ra::launch_kv4_attn(D, ra::kv4_attn_shape(D, num_q_heads / Hkv, max_q_len, sms), p, st);
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache attention launch");
+}
+
+ra_status ra_kv4_status(const void* status, void* stream_) {
+  if (!status) return fail(RA_ERR_INVALID_ARG, "status is NULL");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_);
+  int32_t word = 0;
+  cudaError_t e = cudaMemcpyAsync(&word, status, sizeof(word), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return cuda_fail(e, "status read");
+  switch (word) {
+    case 0: return RA_OK;
+    case RA_KV4_BAD_PAGE: return fail(RA_ERR_INVALID_ARG, "a block table entry is not a page of the cache");
+    case RA_KV4_BAD_LENGTH: return fail(RA_ERR_INVALID_ARG, "a length is negative or passes the block table's row");
+    case RA_KV4_BAD_OFFSET: return fail(RA_ERR_INVALID_ARG, "query offsets fall or pass the number of query tokens");
+    case RA_KV4_TOO_MANY_TOKENS: return fail(RA_ERR_INVALID_ARG, "more new tokens than slots");
+    case RA_KV4_NO_PAGES: return fail(RA_ERR_WORKSPACE, "not enough free pages");
+    case RA_KV4_BAD_FREE_COUNT: return fail(RA_ERR_INVALID_ARG, "the free count is negative or passes the number of pages");
+  }
+  return fail(RA_ERR_TIMEOUT, "a kernel gave up on a pipeline wait (site %d)", word);
+}
+
+}  // extern "C"

@@ -100,6 +100,17 @@ def load_library(path: str | None = None):
     lib.ra_selftest_wait_timeout.restype = i32
     lib.ra_workspace_status.argtypes = [P, P]
     lib.ra_workspace_status.restype = i32
+    lib.ra_kv4_cache_bytes.argtypes = [i64, i32, i32, i32, c.POINTER(sz)]
+    lib.ra_kv4_tables.argtypes = [P, P, i32, P, i32, i64, i32, P, i32, P, i64, P, P, P, P, P, P, P]
+    lib.ra_kv4_store.argtypes = [P, P, i64, P, i64, P, i64, P]
+    lib.ra_kv4_load.argtypes = [P, P, i64, P, P, P]
+    lib.ra_kv4_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, c.POINTER(sz)]
+    lib.ra_kv4_attention.argtypes = [P, P, i64, i32, i32, P, i32, i64, P, P, i32, i32, i32, c.c_float, P, i32, P, P,
+                                     sz, P]
+    lib.ra_kv4_status.argtypes = [P, P]
+    for name in ("ra_kv4_cache_bytes", "ra_kv4_tables", "ra_kv4_store", "ra_kv4_load",
+                 "ra_kv4_attention_workspace_bytes", "ra_kv4_attention", "ra_kv4_status"):
+        getattr(lib, name).restype = i32
     _lib = lib
     return lib
 

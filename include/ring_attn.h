@@ -395,6 +395,150 @@ ra_status ra_fwd_noalloc(const ra_plan* plan, const void* q, const void* k, cons
  */
 ra_status ra_noalloc_status(void* stream);
 
+/* ------------------------------------------------------------------------
+ * Key/value cache held in 4 bits, and attention over it
+ * ------------------------------------------------------------------------
+ * For generating tokens after a prompt: the prompt's keys and values (the
+ * inputs of ra_fwd) go into a paged cache of 4.5 bits an element, and later
+ * query rows attend to them.  No counterpart on the pages; a library
+ * convenience that shares ra_fwd's conventions (THD rows, grouped query heads,
+ * natural-log LSE, exact merge of partial results by their LSE).
+ *
+ * Format.  16 neighbouring elements of a row share a scale s of 8 bits: 5
+ * exponent bits (bias 15) and 3 mantissa bits, no sign; the byte shifted left
+ * by 7 is an fp16 number.  An element is a sign and one of 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 (codes 0..7, the sign is bit 3), times s.
+ *   s    = max|x| / 6, rounded to nearest even, at most 10240;
+ *   code = x / s, rounded to nearest even, at most 6.
+ * So |x| above 61440 reads as 61440, and a group with an infinity or a NaN
+ * reads as NaN (scale byte 255).
+ *
+ * Pages.  A page holds page_size tokens (16, 32, 64, 128 or 256) of every
+ * key/value head: [num_pages][num_kv_heads][page_size / 16] tiles of 16 tokens,
+ * 18 head_dim bytes each: key codes (8 head_dim bytes), key scales (head_dim),
+ * value codes (8 head_dim), value scales (head_dim).  The order inside a tile
+ * follows the attention kernel's operands and is the library's own; rows are
+ * written by ra_kv4_store and read by ra_kv4_load.
+ *
+ * Slots.  Token t of a request with block table row `row` lives in slot
+ * row[t / page_size] * page_size + t % page_size.
+ *
+ * All lengths, tables and maps are device memory and are read by the kernels,
+ * so a captured step replays with new contents; no call allocates or waits
+ * (ra_kv4_status does wait).  What a kernel finds wrong in them it refuses
+ * without reading or writing out of bounds, and says so in a status word.
+ */
+typedef struct ra_kv4_cache {
+  void* pages;          /* device, 16-byte aligned, ra_kv4_cache_bytes(..) */
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t reserved;     /* 0 */
+} ra_kv4_cache;
+
+/* Status words of the calls below. */
+typedef enum {
+  RA_KV4_BAD_PAGE = 1001,        /* a block table entry is not a page of the cache */
+  RA_KV4_BAD_LENGTH = 1002,      /* a length is negative or passes the block table's row */
+  RA_KV4_BAD_OFFSET = 1003,      /* query offsets fall or pass the number of query tokens */
+  RA_KV4_TOO_MANY_TOKENS = 1004, /* more new tokens than slots */
+  RA_KV4_NO_PAGES = 1005,        /* not enough free pages */
+  RA_KV4_BAD_FREE_COUNT = 1006   /* free count negative or, with the released pages, above num_pages */
+} ra_kv4_code;
+
+/* Bytes of a cache's pages. */
+ra_status ra_kv4_cache_bytes(int64_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                             size_t* bytes);
+
+/*
+ * One step's page bookkeeping, in one launch: give back the pages of requests
+ * that leave, take pages for the new tokens, extend the block table, and write
+ * the slot and position of every new token.
+ *   kv_lens [R], new_lens [R]: tokens cached before the step, and tokens it
+ *     adds (0 allowed); new_lens[r] = -1: the request leaves.  1 <= R <= 4096.
+ *   block_table: int32 [R, table_width], rows table_stride apart; the first
+ *     ceil(kv_lens[r] / page_size) entries of row r are its pages.  New entries
+ *     are written behind them; others stay as they are.
+ *   free_pages [num_pages], free_count [1]: a stack of free pages.  Released
+ *     pages are pushed first (in request order, then page order), then new
+ *     ones popped (likewise).  free_pages NULL: no pages are taken or given
+ *     back; the block table already holds every page that the new tokens use
+ *     (slots of a negative entry are -1).
+ *   kv_lens_out [R] (may be kv_lens): lengths after the step, 0 for a request
+ *     that left.  cu_new [R + 1]: prefix sums of the added tokens.
+ *   slot_map int64 [num_slots], positions int32 [num_slots]: of the new tokens,
+ *     request by request; -1 behind the last one.
+ *   free_count_out [1] (may be free_count).
+ *   status int32 [1]: 0, or why the step was refused.  A refused step changes
+ *     nothing: kv_lens_out = kv_lens, free_count_out = free_count, cu_new = 0,
+ *     slots and positions -1.  Read it with ra_kv4_status.
+ * A page must occur only once in the free list and the block table together.
+ */
+ra_status ra_kv4_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t num_requests, int32_t* block_table,
+                        int32_t table_width, int64_t table_stride, int32_t page_size, int32_t* free_pages,
+                        int32_t num_pages, const int32_t* free_count, int64_t num_slots, int32_t* kv_lens_out,
+                        int32_t* cu_new, int64_t* slot_map, int32_t* positions, int32_t* free_count_out,
+                        int32_t* status, void* stream);
+
+/*
+ * Round key and value rows to 4 bits into the cache.  k, v: bf16
+ * [num_tokens, num_kv_heads, head_dim], rows k_stride / v_stride elements
+ * apart (multiples of 8, so slices of a fused projection's output go in as they
+ * are).  Row t goes to slot_map[t]; rows with a negative slot, or one outside
+ * the cache, are left out.  A slot must not occur twice in one call: its
+ * content would be parts of either row.
+ */
+ra_status ra_kv4_store(const ra_kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       const int64_t* slot_map, int64_t num_tokens, void* stream);
+
+/*
+ * Read cached rows: k, v bf16 [num_tokens, num_kv_heads, head_dim] (dense)
+ * receive the values in slots slot_map[t], exactly (6 significant bits fit
+ * bf16); rows with a negative slot, or one outside the cache, become zero.
+ * Slots may repeat.
+ */
+ra_status ra_kv4_load(const ra_kv4_cache* cache, const int64_t* slot_map, int64_t num_tokens, void* k, void* v,
+                      void* stream);
+
+/* Workspace bytes of ra_kv4_attention for calls with up to max_q_len query tokens a request. */
+ra_status ra_kv4_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                           int32_t max_q_len, size_t* bytes);
+
+/*
+ * Attention of packed query rows over the cache.  Request r brings the query
+ * rows [cu_q[r], cu_q[r+1]) and has kv_lens[r] cached tokens, its newest
+ * (already stored) ones among them: with causal != 0, query i of n sees the
+ * keys j <= kv_lens[r] - n + i, else all of them.  Query head h reads
+ * key/value head h / (num_q_heads / num_kv_heads).
+ *   q bf16 [num_q_tokens, num_q_heads, head_dim], rows q_stride elements apart
+ *     (a multiple of 8).
+ *   block_table as in ra_kv4_tables; kv_lens int32 [R], cu_q int32 [R + 1].
+ *   max_q_len: query tokens of the request with the most; selects the kernel
+ *     variant (a wrong value costs time, not correctness).
+ *   softmax_scale <= 0 selects 1/sqrt(head_dim).
+ *   o [num_q_tokens, num_q_heads, head_dim]: bf16, or fp32 when o_is_fp32.
+ *   lse fp32 [num_q_heads, num_q_tokens], natural log.
+ * A row that sees no key gets o = 0 and lse = -inf.  Rows outside
+ * [cu_q[0], cu_q[R]) are left as they were.  The workspace (device, 256-byte
+ * aligned) must not be shared by calls that may overlap; its first word is the
+ * status of the last call (ra_kv4_status): a page id outside the cache, a length
+ * or an offset out of range is left out of the result and reported there.
+ */
+ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_stride, int32_t num_q_tokens,
+                           int32_t num_q_heads, const int32_t* block_table, int32_t table_width, int64_t table_stride,
+                           const int32_t* kv_lens, const int32_t* cu_q, int32_t num_requests, int32_t max_q_len,
+                           int32_t causal, float softmax_scale, void* o, int32_t o_is_fp32, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Synchronise `stream` and read a status word (ra_kv4_tables' status, or the
+ * start of ra_kv4_attention's workspace): RA_OK; RA_ERR_WORKSPACE for missing
+ * pages; RA_ERR_INVALID_ARG for the other refusals; RA_ERR_TIMEOUT if a kernel
+ * gave up on a pipeline wait.
+ */
+ra_status ra_kv4_status(const void* status, void* stream);
+
 /* Thread-local text for the last non-OK status returned on this thread. */
 const char* ra_last_error(void);
 

@@ -1,0 +1,502 @@
+"""4-bit key/value cache on the GPU against the fp64 oracle.
+
+Store, load and the tables are exact.  Attention's tolerance, derived for
+every case from its inputs (see ``bounds``):
+  * S is accumulated in fp32 from exact products: D terms, each sum off by at
+    most one unit in the last place (tensor cores may truncate: 2^-23) of the
+    sum of magnitudes; that is an absolute error e_s of the exponent, and a
+    relative one of every p (twice with the normaliser);
+  * p goes into P.V as fp16: 2^-11 relative at the most coarse reading of half a
+    step (finfo(fp16).eps / 2 = 2^-11), and 2^-25 / 2^6 absolute;
+  * 2^x and log2 approximations and the merge weights: 2^-20;
+  * O and l add at most L terms in fp32, 16 at a time in the products;
+  * bf16 outputs round by half a step: finfo(bf16).eps / 2 relative.
+"""
+
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4 as O
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ra(lib_path):
+    import context_ring_attention_step_gb300 as m
+    m.load_library(lib_path)
+    return m
+
+
+def bf16(rng, *shape, scale=1.0):
+    return torch.tensor(rng.standard_normal(shape) * scale, dtype=torch.float32).to(torch.bfloat16)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ store and load
+
+def hard_rows(rng, T, H, d):
+    """Rows with ties of both formats, tiny, huge, zero and non-finite groups."""
+    x = rng.standard_normal((T, H, d)) * np.exp2(rng.integers(-24, 20, (T, H, 1)))
+    g = x.reshape(T, H, d // 16, 16)
+    kind = rng.integers(0, 12, (T, H, d // 16))
+    ties = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5, 6, -.25, -.75, -1.25, -1.75, -2.5, -3.5, -5, -6])
+    for i, e in enumerate((-12, 0, 9)):
+        g[kind == i] = ties * 2.0 ** e                           # elements on the borders
+    g[kind == 4] = rng.integers(-255, 256, g[kind == 4].shape)   # amax / 6 on and off the scales' borders
+    g[kind == 5] = 0
+    g[kind == 6] *= 1e30
+    g[kind == 7] = rng.choice([0, 2.0 ** -17, 2.0 ** -18 * 3, -2.0 ** -20, 2.0 ** -15], g[kind == 7].shape)
+    g[kind == 8, 3] = np.inf
+    g[kind == 9, 15] = np.nan
+    return torch.tensor(x).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,page,T", [(1, 16, 1), (3, 32, 77), (8, 64, 333), (2, 256, 600)])
+def test_store_load_are_exact(ra, d, H, page, T):
+    rng = np.random.default_rng(100 * d + T)
+    pages = T // page + 3
+    k, v = hard_rows(rng, T, H, d), hard_rows(rng, T, H, d)
+    slots = torch.tensor(rng.permutation(pages * page)[:T])
+    skip = torch.tensor(rng.random(T) < 0.1)
+    given = torch.where(skip, torch.tensor(rng.choice([-1, -7, pages * page, 1 << 40], T)), slots)
+    cache = ra.Kv4Cache(pages, page, H, d)
+    # rows of a fused projection: q, k, v of a token one after the other
+    qkv = torch.cat([k, torch.zeros(T, 2, d, dtype=torch.bfloat16), v], dim=1).cuda()
+    ra.kv4_store(cache, qkv[:, :H], qkv[:, H + 2:], given.cuda(), check=False)
+    ko, vo = ra.kv4_load(cache, slots.cuda())
+    keep = (~skip).numpy()
+    for got, x in ((ko, k), (vo, v)):
+        want = O.rounded(f64(x))
+        want[~keep] = 0                                          # never written: the fresh cache's zeros
+        np.testing.assert_array_equal(f64(got), want)
+    # skipped rows of a load are zero, repeated ones repeat
+    again = torch.cat([slots[:5], slots[:5], torch.tensor([-1, pages * page, 1 << 62])]).cuda()
+    k2, _ = ra.kv4_load(cache, again)
+    n = min(5, T)
+    assert torch.equal(torch.nan_to_num(k2[:n]), torch.nan_to_num(k2[n:2 * n])) and k2[2 * n:].eq(0).all()
+
+
+def test_store_leaves_other_slots(ra):
+    rng = np.random.default_rng(5)
+    cache = ra.Kv4Cache(3, 32, 2, 128)
+    cache.pages.random_(0, 256, generator=torch.Generator("cuda").manual_seed(1))
+    others = torch.tensor([s for s in range(96) if s not in (17, 40)]).cuda()
+    before = [t.clone() for t in ra.kv4_load(cache, others)]
+    x = bf16(rng, 2, 2, 128).cuda()
+    ra.kv4_store(cache, x, x, torch.tensor([17, 40]).cuda())
+    for a, b in zip(before, ra.kv4_load(cache, others)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    np.testing.assert_array_equal(f64(ra.kv4_load(cache, torch.tensor([17, 40]).cuda())[0]), O.rounded(f64(x)))
+
+
+def test_store_checks_slots(ra):
+    cache = ra.Kv4Cache(2, 16, 1, 64)
+    x = torch.zeros(2, 1, 64, dtype=torch.bfloat16).cuda()
+    with pytest.raises(ValueError, match="twice"):
+        ra.kv4_store(cache, x, x, torch.tensor([3, 3]).cuda(), check=True)
+    with pytest.raises(ValueError, match="outside"):
+        ra.kv4_store(cache, x, x, torch.tensor([3, 32]).cuda(), check=True)
+    ra.kv4_store(cache, x, x, torch.tensor([-1, -1]).cuda(), check=True)
+    ra.kv4_store(cache, x[:0], x[:0], torch.zeros(0, dtype=torch.int64).cuda(), check=True)
+
+
+# ------------------------------------------------------------------ tables
+
+def draw_tables(rng, R, page, width, alloc=True):
+    lens = [rng.choice([0, rng.randrange(0, width * page + 1), rng.randrange(0, page + 1)]) for _ in range(R)]
+    new = [rng.choice([-1, 0, 1, 1, 1, rng.randrange(0, 200)]) for _ in range(R)]
+    new = [min(a, width * page - n) for n, a in zip(lens, new)]
+    held = [-(-n // page) for n in lens]
+    need = [-(-(n + max(a, 0)) // page) for n, a in zip(lens, new)]
+    ids = list(range(sum(need) + sum(held) + 5))
+    rng.shuffle(ids)
+    table, at = [], 0
+    for h, n in zip(held, need):
+        m = h if alloc else n
+        table.append(ids[at:at + m] + [-9] * (width - m))
+        at += m
+    free = ids[at:]
+    pad = [-5] * (sum(held) + 3)
+    return lens, new, table, free + pad, len(free)
+
+
+def run_tables(ra, lens, new, table, page, slots, free=None, count=0, in_place=False, stride=None):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+    tb = i32(table)
+    if stride:
+        wide = torch.full((len(table), stride), -77, dtype=torch.int32).cuda()
+        wide[:, :tb.shape[1]] = tb
+        tb = wide[:, :tb.shape[1]]
+    fr = None if free is None else i32(free)
+    ct = None if free is None else i32([count])
+    ln = i32(lens)
+    out = ra.kv4_tables_out(len(lens), slots)
+    if in_place:
+        out = out._replace(kv_lens=ln, free_count=ct if ct is not None else out.free_count)
+    step = ra.kv4_tables(ln, i32(new), tb, page, slots, fr, ct, out=out)
+    code = int(step.status)
+    return (code, step.kv_lens.tolist(), step.cu_new.tolist(), step.slot_map.tolist(), step.positions.tolist(),
+            None if ct is None else int(step.free_count), tb.tolist(), None if fr is None else fr.tolist())
+
+
+@pytest.mark.parametrize("R,page,width", [(1, 16, 4), (3, 64, 9), (64, 64, 40), (200, 16, 30), (1025, 32, 12), (4096, 128, 5)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_tables_match_the_lists(ra, R, page, width, in_place):
+    rng = random.Random(R + in_place)
+    for spare in (0, 1, 137):
+        lens, new, table, free, count = draw_tables(rng, R, page, width)
+        slots = sum(max(a, 0) for a in new) + spare
+        want = O.tables(lens, new, table, page, slots, free, count)
+        got = run_tables(ra, lens, new, table, page, slots, free, count, in_place, stride=width + 3 if spare else None)
+        assert got == (0,) + want
+
+
+@pytest.mark.parametrize("R", [1, 33, 300])
+def test_tables_map_only(ra, R):
+    rng = random.Random(R)
+    lens, new, table, _, _ = draw_tables(rng, R, 32, 20, alloc=False)
+    slots = sum(max(a, 0) for a in new) + 9
+    want = O.tables(lens, new, table, 32, slots)
+    got = run_tables(ra, lens, new, table, 32, slots)
+    assert got[:5] == (0,) + want[:4] and got[6] == table
+    lens, new = [0] * 2, [40, 40]
+    got = run_tables(ra, lens, new, [[3, -1], [7, 8]], 32, 80)
+    assert got[3] == list(range(96, 128)) + [-1] * 8 + list(range(224, 264))
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(slots=99), 1004), (dict(count=1), 1005), (dict(count=-1), 1006), (dict(count=12), 1006),
+    (dict(lens=[10, -1, 70]), 1002), (dict(lens=[10, 0, 129]), 1002), (dict(new=[30, -2, 3]), 1002),
+    (dict(new=[119, -1, 3]), 1002), (dict(new=[2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]), 1002)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_tables_refuse_whole_steps(ra, change, code, in_place):
+    a = dict(lens=[10, 20, 70], new=[97, -1, 3], table=[[0, 1, 2, 3, 4, 5, 6, 7]] * 3, slots=100, count=8)
+    a["free"] = list(range(10, 20))
+    a.update(change)
+    got = run_tables(ra, a["lens"], a["new"], a["table"], 16, a["slots"], a["free"], a["count"], in_place)
+    assert got[0] == code
+    assert got[1] == a["lens"] and got[2] == [0] * 4 and got[3] == [-1] * a["slots"] == got[4]
+    assert got[5] == a["count"] and got[6] == a["table"] and got[7] == a["free"]
+    step = ra.Kv4Tables(None, None, None, None, None, torch.tensor([code], dtype=torch.int32).cuda())
+    with pytest.raises(ra.RingAttnError) as e:
+        ra.kv4_status(step.status)
+    assert e.value.status == (4 if code == 1005 else 1)
+
+
+# ------------------------------------------------------------------ attention
+
+class Case:
+    """A cache with random pages, holding the keys and values of several requests."""
+
+    def __init__(self, ra, seed, lens, qlens, Hq, Hkv, d, page, kscale=1.0, vscale=1.0, garbage=True, keys=None, values=None):
+        rng = np.random.default_rng(seed)
+        self.lens, self.qlens, self.Hq, self.Hkv, self.d = lens, qlens, Hq, Hkv, d
+        held = [-(-n // page) for n in lens]
+        N = sum(held) + 2
+        ids = rng.permutation(N)
+        width = max(held + [0]) + 2
+        table = np.full((len(lens), width), -1, dtype=np.int32)
+        at = 0
+        for r, n in enumerate(held):
+            table[r, :n] = ids[at:at + n]
+            at += n
+        self.cache = ra.Kv4Cache(N, page, Hkv, d)
+        if garbage:   # what unused places hold must not matter: all bytes, NaN scales among them
+            self.cache.pages.random_(0, 256, generator=torch.Generator("cuda").manual_seed(seed))
+        self.keys, self.values = [], []
+        for r, n in enumerate(lens):
+            k = bf16(rng, n, Hkv, d, scale=kscale) if keys is None else keys[r]
+            v = bf16(rng, n, Hkv, d, scale=vscale) if values is None else values[r]
+            t = np.arange(n)
+            slots = table[r, t // page].astype(np.int64) * page + t % page
+            ra.kv4_store(self.cache, k.cuda(), v.cuda(), torch.tensor(slots).cuda())
+            self.keys.append(O.rounded(f64(k)))
+            self.values.append(O.rounded(f64(v)))
+        self.cu = np.concatenate([[0], np.cumsum(qlens)]).astype(int).tolist()
+        self.q = bf16(rng, self.cu[-1], Hq, d)
+        self.table = torch.tensor(table).cuda()
+        self.lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+        self.cu_t = torch.tensor(self.cu, dtype=torch.int32).cuda()
+
+    def bounds(self, scale, o_fp32, want):
+        """Absolute tolerances of o (array) and lse, as the module's docstring derives them."""
+        L = max(self.lens + [1])
+        qm = np.abs(f64(self.q)).max() if self.q.numel() else 0.0
+        ks = max([np.nan_to_num(np.abs(k)).sum(-1).max() for k in self.keys if k.size] + [0.0])
+        vm = max([np.nan_to_num(np.abs(v)).max() for v in self.values if v.size] + [0.0])
+        e_s = scale * self.d * 2.0 ** -23 * qm * ks
+        e = 2 * e_s + 2.0 ** -11 + 2.0 ** -20 + L * 2.0 ** -23
+        tol_o = e * vm + L * 2.0 ** -31 * vm
+        if not o_fp32:
+            tol_o = tol_o + np.nan_to_num(np.abs(want)) * 2.0 ** -8
+        return tol_o, e_s + 2.0 ** -20 + L * 2.0 ** -23 + 2.0 ** -22 * 20
+
+    def check(self, ra, causal=True, scale=None, o_fp32=True, max_q_len=None, q=None):
+        sc = scale or 1 / math.sqrt(self.d)
+        want, wl = O.attention(f64(self.q), self.keys, self.values, self.lens, self.cu, causal, sc)
+        o, lse = ra.kv4_attention((self.q.cuda() if q is None else q), self.cache, self.table, self.lens_t, self.cu_t,
+                                  causal=causal, scale=scale, o_fp32=o_fp32, max_q_len=max_q_len, check=True)
+        self.compare(f64(o), f64(lse), want, wl, sc, o_fp32)
+        return o, lse
+
+    def compare(self, o, lse, want, wl, sc, o_fp32):
+        tol_o, tol_l = self.bounds(sc, o_fp32, want)
+        assert np.array_equal(np.isnan(o), np.isnan(want))
+        assert np.all(np.nan_to_num(np.abs(o - want)) <= tol_o), np.nanmax(np.abs(o - want) - tol_o)
+        assert np.array_equal(np.isneginf(lse), np.isneginf(wl)) and np.array_equal(np.isnan(lse), np.isnan(wl))
+        f = np.isfinite(wl)
+        assert np.all(np.abs(lse[f] - wl[f]) <= tol_l), np.abs(lse[f] - wl[f]).max()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 4, 5, 8, 16])
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode(ra, d, G, page):
+    lens = [1, 2, 15, 16, 17, 31, 63, 64, 65, 0, 130, 1000]
+    c = Case(ra, 7 * d + G, lens, [1] * len(lens), 2 * G, 2, d, page)
+    c.check(ra, max_q_len=1)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 2, 2), (128, 8, 2), (128, 7, 1), (256, 6, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("qlens", [[2, 3, 1, 4, 0, 5, 8], [17, 0, 64, 1, 33, 5, 9]])
+def test_several_tokens(ra, d, Hq, Hkv, causal, qlens):
+    lens = [2, 40, 64, 100, 50, 333, 5]          # the last request brings more rows than it has keys
+    c = Case(ra, 11 + d + sum(qlens), lens, qlens, Hq, Hkv, d, 32)
+    c.check(ra, causal=causal, max_q_len=max(qlens))
+    c.check(ra, causal=causal, o_fp32=False)     # max_q_len: the number of rows
+    c.check(ra, causal=causal, max_q_len=1)      # a wrong bound costs time only
+    c.check(ra, causal=causal, scale=0.3)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,L", [(128, 4, 1, 4001), (64, 1, 1, 6000), (256, 2, 2, 2500), (128, 1, 1, 4096)])
+def test_one_long_request_is_split(ra, d, Hq, Hkv, L):
+    c = Case(ra, L, [L], [1], Hq, Hkv, d, 64)
+    c.check(ra, max_q_len=1)
+
+
+def test_prompt_part(ra):
+    c = Case(ra, 3, [700, 512], [300, 257], 4, 2, 128, 64)
+    c.check(ra, max_q_len=300)
+    c.check(ra, causal=False, o_fp32=False, max_q_len=300)
+
+
+def test_uneven_scores_move_the_reference(ra):
+    """Scores that grow along the keys by far more than the reference's headroom, and shrink again."""
+    rng = np.random.default_rng(9)
+    L, d = 900, 128
+    ramp = np.concatenate([np.linspace(0.01, 30, 450), np.linspace(30, 0.01, 450)])
+    k = torch.tensor(rng.standard_normal((1, 1, d)) * ramp[:, None, None]).to(torch.bfloat16)
+    c = Case(ra, 9, [L], [3], 2, 1, d, 16, keys=[k])
+    c.check(ra, max_q_len=3)
+
+
+def test_wide_ranges_of_q(ra):
+    rng = np.random.default_rng(10)
+    c = Case(ra, 10, [200], [8], 2, 1, 128, 16)
+    c.q = torch.tensor(rng.standard_normal((8, 2, 128)) * np.exp2([[-120], [-20], [-3], [0], [2], [3], [4], [5]])[:, :, None]).to(torch.bfloat16)
+    c.q[0, 1] = 0
+    c.check(ra, max_q_len=8)
+
+
+def test_nan_stays_in_its_rows(ra):
+    """A NaN value or key of a late token reaches the rows that see it, and no other."""
+    rng = np.random.default_rng(12)
+    for d, Hq in ((64, 2), (128, 4), (256, 2)):
+        L, n = 150, 40
+        k, v = bf16(rng, L, 1, d), bf16(rng, L, 1, d)
+        v[130, 0, 3] = float("nan")
+        v[131, 0, d - 1] = float("inf")
+        c = Case(ra, d, [L], [n], Hq, 1, d, 16, keys=[k], values=[v])
+        c.check(ra, max_q_len=n)
+        assert not np.isnan(f64(c.check(ra, max_q_len=n)[0])[:20]).any()
+        k[149, 0, 5] = float("nan")
+        c = Case(ra, d, [L], [n], Hq, 1, d, 16, keys=[k], values=[v])
+        c.check(ra, max_q_len=n)
+        c.check(ra, max_q_len=1)
+
+
+def test_strided_q_and_rows_behind_the_last(ra):
+    c = Case(ra, 21, [40, 90], [1, 2], 4, 2, 64, 16)
+    T = 6                                                        # three rows more than the requests bring
+    fused = torch.full((T, 8, 64), float("nan"), dtype=torch.bfloat16).cuda()
+    fused[:3, :4] = c.q.cuda()
+    o = torch.full((T, 4, 64), 7.0, device="cuda")
+    lse = torch.full((4, T), 5.0, device="cuda")
+    ra.kv4_attention(fused[:, :4], c.cache, c.table, c.lens_t, c.cu_t, o_fp32=True, max_q_len=2, out=(o, lse), check=True)
+    want, wl = O.attention(f64(c.q), c.keys, c.values, c.lens, c.cu, True, 1 / 8)
+    c.compare(f64(o[:3]), f64(lse[:, :3]), want, wl, 1 / 8, True)
+    assert o[3:].eq(7).all() and lse[:, 3:].eq(5).all()
+
+
+def test_refused_contents_are_reported_and_stay_in_bounds(ra):
+    c = Case(ra, 31, [40, 90, 33], [1, 1, 1], 4, 2, 64, 16)
+    q = c.q.cuda()
+    good = ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, max_q_len=1, check=True)[0]
+
+    def refused(match, table=c.table, lens=c.lens_t, cu=c.cu_t):
+        ws = ra.kv4_attention_workspace(c.cache, 3, 4, 1)
+        o, _ = ra.kv4_attention(q, c.cache, table, lens, cu, max_q_len=1, workspace=ws)
+        with pytest.raises(ra.RingAttnError, match=match):
+            ra.kv4_status(ws)
+        ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, max_q_len=1, workspace=ws, check=True)  # fresh status
+        return o
+    for bad in (-1, c.cache.num_pages, 2 ** 31 - 1, -2 ** 31):
+        t = c.table.clone()
+        t[1, 2] = bad
+        o = refused("page", table=t)
+        assert torch.equal(o[0], good[0]) and torch.equal(o[2], good[2]) and torch.isfinite(o).all()
+    for bad in (-1, c.table.shape[1] * 16 + 1, 2 ** 31 - 1):
+        x = c.lens_t.clone()
+        x[1] = bad
+        refused("length|page", lens=x)
+    for cu in ([0, 1, 2, 4], [0, 2, 1, 3], [-1, 1, 2, 3], [0, 1, 2, 2 ** 31 - 1]):
+        refused("offsets", cu=torch.tensor(cu, dtype=torch.int32).cuda())
+
+
+def test_empty_calls(ra):
+    c = Case(ra, 41, [0, 0], [1, 2], 4, 2, 64, 16)
+    o, lse = c.check(ra, max_q_len=2)
+    assert o.eq(0).all() and torch.isneginf(lse).all()
+    e = torch.zeros(0, 4, 64, dtype=torch.bfloat16).cuda()
+    z = torch.zeros(3, dtype=torch.int32).cuda()
+    o, lse = ra.kv4_attention(e, c.cache, c.table, c.lens_t, z, check=True)
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+
+
+def test_page_offsets_beyond_32_bits(ra):
+    """Pages that lie more than 2^32 bytes into the cache."""
+    page, H, d = 64, 8, 128
+    N = (5 << 30) // (page * H * d * 9 // 8)
+    cache = ra.Kv4Cache(N, page, H, d)
+    rng = np.random.default_rng(77)
+    L = 200
+    ids = [N - 1, 3, N - 5, N // 2]
+    k, v = bf16(rng, L, H, d), bf16(rng, L, H, d)
+    t = np.arange(L)
+    slots = torch.tensor(np.array(ids)[t // page] * page + t % page).cuda()
+    ra.kv4_store(cache, k.cuda(), v.cuda(), slots)
+    np.testing.assert_array_equal(f64(ra.kv4_load(cache, slots)[1]), O.rounded(f64(v)))
+    c = Case(ra, 77, [0], [1], 16, 8, d, page)
+    c.cache, c.lens, c.lens_t = cache, [L], torch.tensor([L], dtype=torch.int32).cuda()
+    c.table = torch.tensor([ids], dtype=torch.int32).cuda()
+    c.keys, c.values = [O.rounded(f64(k))], [O.rounded(f64(v))]
+    c.check(ra, max_q_len=1)
+
+
+# ------------------------------------------------------------------ use
+
+def test_other_streams_and_two_workspaces(ra):
+    a, b = (Case(ra, s, [900, 300], [1, 1], 8, 2, 128, 64) for s in (51, 52))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(5):
+        outs = []
+        for c, st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                q = c.q.cuda()
+                outs.append(ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, o_fp32=True, max_q_len=1))
+        torch.cuda.synchronize()
+    for c, (o, lse) in zip((a, b), outs):
+        want, wl = O.attention(f64(c.q), c.keys, c.values, c.lens, c.cu, True, 1 / math.sqrt(128))
+        c.compare(f64(o), f64(lse), want, wl, 1 / math.sqrt(128), True)
+
+
+def test_results_repeat(ra):
+    c = Case(ra, 61, [3000, 17, 500], [2, 1, 3], 8, 2, 128, 32)
+    q = c.q.cuda()
+    first = ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, o_fp32=True, max_q_len=3)
+    for _ in range(4):
+        again = ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, o_fp32=True, max_q_len=3)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_prompt_then_tokens_in_a_captured_step(ra):
+    """Prompts by ring attention, their keys and values into the cache, then decode steps replayed from a CUDA
+    graph; a request leaves and another takes its pages."""
+    rng = np.random.default_rng(71)
+    Hq, Hkv, d, page, R, W = 8, 2, 128, 16, 3, 12
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+    N = 20
+    cache = ra.Kv4Cache(N, page, Hkv, d)
+    table, free, count = torch.full((R, W), -1, dtype=torch.int32).cuda(), torch.arange(N, dtype=torch.int32).cuda(), i32([N])
+    lens = i32([0, 0, 0])
+    prompt = [37, 1, 64]
+    T = sum(prompt)
+    q, k, v = bf16(rng, T, Hq, d).cuda(), bf16(rng, T, Hkv, d).cuda(), bf16(rng, T, Hkv, d).cuda()
+    out = ra.kv4_tables_out(R, T)._replace(kv_lens=lens, free_count=count)
+    step = ra.kv4_tables(lens, i32(prompt), table, page, T, free, count, out=out, check=True)
+    cu = step.cu_new.tolist()
+    ra.kv4_store(cache, k, v, step.slot_map)
+    # the prompt's attention over what the cache holds, by ring attention and by the cache's own
+    kr, vr = ra.kv4_load(cache, step.slot_map)
+    o_ring, lse_ring = ra.ring_attn_fwd(q, kr, vr, cu, 1, o_fp32=True, check=True)
+    o_kv4, lse_kv4 = ra.kv4_attention(q, cache, table, lens, step.cu_new, o_fp32=True, max_q_len=max(prompt), check=True)
+    # the ring's P is bf16 (2^-8), the cache's fp16 (2^-11)
+    assert (o_ring - o_kv4).abs().max() <= vr.float().abs().max() * (2.0 ** -8 + 2.0 ** -10)
+    assert (lse_ring - lse_kv4).abs().max() <= 1e-3
+
+    hist_k = [O.rounded(f64(k[cu[r]:cu[r + 1]])) for r in range(R)]
+    hist_v = [O.rounded(f64(v[cu[r]:cu[r + 1]])) for r in range(R)]
+    new = i32([1, 1, 1])
+    q1, k1, v1 = (torch.zeros(R, h, d, dtype=torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv))
+    st = ra.kv4_tables_out(R, R)._replace(kv_lens=lens, free_count=count)
+    res = torch.zeros(R, Hq, d).cuda(), torch.zeros(Hq, R).cuda()
+    ws = ra.kv4_attention_workspace(cache, R, Hq, 1)
+
+    def one_step():
+        ra.kv4_tables(lens, new, table, page, R, free, count, out=st)
+        ra.kv4_store(cache, k1, v1, st.slot_map)
+        ra.kv4_attention(q1, cache, table, lens, st.cu_new, o_fp32=True, max_q_len=1, workspace=ws, out=res)
+
+    saved = [t.clone() for t in (lens, table, free, count, cache.pages)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        one_step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one_step()
+    for t, s in zip((lens, table, free, count, cache.pages), saved):
+        t.copy_(s)
+    for i in range(40):
+        adds = [1, 1, 1]
+        if i == 20:
+            adds[2] = -1                                         # the third request leaves ...
+        if i == 21:
+            adds[2] = 1                                          # ... and its row starts again with one token
+        new.copy_(i32(adds))
+        n = sum(a > 0 for a in adds)
+        qs, ks, vs = bf16(rng, R, Hq, d), bf16(rng, R, Hkv, d), bf16(rng, R, Hkv, d)
+        q1.copy_(qs), k1.copy_(ks), v1.copy_(vs)
+        graph.replay()
+        ra.kv4_status(st.status)
+        ra.kv4_status(ws)
+        row = 0
+        for r, a in enumerate(adds):
+            if a < 0:
+                hist_k[r], hist_v[r] = hist_k[r][:0], hist_v[r][:0]
+            else:
+                hist_k[r] = np.concatenate([hist_k[r], O.rounded(f64(ks[row:row + 1]))])
+                hist_v[r] = np.concatenate([hist_v[r], O.rounded(f64(vs[row:row + 1]))])
+                row += 1
+        assert lens.tolist() == [len(x) for x in hist_k]
+        if i % 5 == 0 or i in (20, 21, 22):
+            cuq = st.cu_new.tolist()
+            want, wl = O.attention(f64(qs[:n]), hist_k, hist_v, lens.tolist(), cuq, True, 1 / math.sqrt(d))
+            err = np.abs(f64(res[0][:n]) - want).max()
+            assert err <= 2.0 ** -10 * max(np.abs(x).max() for x in hist_v if x.size)
+            assert np.abs(f64(res[1][:, :n]) - wl).max() <= 1e-4
+    used = [p for r in range(R) for p in table[r, :-(-len(hist_k[r]) // page)].tolist()]
+    assert sorted(used + free[:int(count)].tolist()) == list(range(N))
