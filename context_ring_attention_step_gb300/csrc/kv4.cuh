@@ -64,13 +64,8 @@ __device__ __forceinline__ uint32_t kv4_round_group(const uint4* __restrict__ sr
   return byte;
 }
 
-// One byte of codes -> two fp16 numbers (low code in the low half).
-__device__ __forceinline__ uint32_t kv4_code_pair(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(byte));
-  return r;
-}
-// The four bytes of a word.
+// The four bytes of a word of codes -> eight fp16 numbers, the low code of a byte
+// in the low half.
 __device__ __forceinline__ void kv4_code_pairs(uint32_t w, uint32_t (&r)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"

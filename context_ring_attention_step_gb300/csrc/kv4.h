@@ -108,14 +108,6 @@ struct Kv4RowsParams {
   void* v_out;
 };
 
-// Work of one attention CTA that another one finishes: the unit it began.
-struct Kv4Part {
-  int32_t request, row_tile, head;
-  int32_t parts;   // partial results to merge, from this CTA's onward; 0: nothing to do
-  int32_t status;  // what this CTA found wrong (RA_KV4_BAD_...), 0 for nothing
-  int32_t pad[3];
-};
-
 struct Kv4AttnParams {
   Kv4Cache cache;
   const void* q;  // bf16 [Tq, Hq, D], rows q_stride elements apart
@@ -127,12 +119,15 @@ struct Kv4AttnParams {
   const int32_t* kv_lens;
   const int32_t* cu_q;
   float scale;
+  int64_t page_bytes;
   void* o;
   int32_t o_is_fp32;
   float* lse;  // [Hq, Tq]
   int32_t* status;
-  Kv4Part* parts;   // one per CTA
-  float* partials;  // two slots per CTA
+  // Zero between calls: what the CTAs found wrong (RA_KV4_BAD_...), how many of
+  // them have ended, and how many partial results the unit that a CTA began has.
+  int32_t *found, *ended, *tickets;
+  float* partials;  // two slots per CTA: [0] of a unit that an earlier CTA began, [1] of one that this CTA began
 };
 
 cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream);

@@ -56,13 +56,13 @@ size_t page_bytes(int32_t page_size, int32_t Hkv, int32_t D) {
 }
 
 struct AttnLayout {
-  size_t parts, partials, total;
+  size_t tickets, partials, total;
 };
 AttnLayout attn_layout(int32_t D, int32_t G, int32_t max_q_len) {
   const ra::Kv4AttnShape s = ra::kv4_attn_shape(D, G, max_q_len, ra::kKv4MaxSms);
   AttnLayout l;
-  l.parts = kHeader;
-  l.partials = align256(l.parts + (size_t)s.ctas * sizeof(ra::Kv4Part));
+  l.tickets = kHeader;
+  l.partials = align256(l.tickets + (size_t)s.ctas * sizeof(int32_t));
   l.total = align256(l.partials + (size_t)s.ctas * 2 * s.slot_floats * sizeof(float));
   return l;
 }
@@ -217,11 +217,14 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
   p.kv_lens = kv_lens;
   p.cu_q = cu_q;
   p.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D);
+  p.page_bytes = (int64_t)page_bytes(cache->page_size, Hkv, D);
   p.o = o;
   p.o_is_fp32 = o_is_fp32 != 0;
   p.lse = lse;
   p.status = reinterpret_cast<int32_t*>(ws);
-  p.parts = reinterpret_cast<ra::Kv4Part*>(ws + l.parts);
+  p.found = p.status + 1;
+  p.ended = p.status + 2;
+  p.tickets = reinterpret_cast<int32_t*>(ws + l.tickets);
   p.partials = reinterpret_cast<float*>(ws + l.partials);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -26,8 +26,9 @@
 //   * the work of all requests, 64 keys at a time, is one line that the grid's
 //     CTAs cut into equal parts (lengths are on the device: the grid is fixed,
 //     and each CTA finds its part from the lengths).  A unit (request, row
-//     tile, head) that spans CTAs leaves partial results in the workspace, which
-//     a second launch merges.
+//     tile, head) that spans CTAs leaves partial results in the workspace, and
+//     the CTA that brings the last one merges them (in the CTAs' order, so the
+//     result does not depend on which one that is).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -40,7 +41,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kBlockKeys = 16 * kWarps;  // keys of one block: a tile a warp
+constexpr int KB = 16 * kWarps;  // keys of one block: a tile a warp
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 // P's reference: a row's largest P is in (2^6, 2^7] when the reference moves,
@@ -81,32 +82,11 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t w, int i, int j) {
   return __byte_perm(w, 0, 0x0404 | (i << 4) | (j << 12)) >> 1;
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
-// Four columns of a finished row: O / l, and the row's log-sum-exp with the first.
-__device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, int token, int h, int D, int d4, float4 v,
-                                              float m, float l) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-  const size_t off = ((size_t)token * p.Hq + h) * D + 4 * d4;
-  if (p.o_is_fp32)
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + off) = v;
-  else
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.o) + off) =
-        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-  if (d4 == 0) p.lse[(size_t)h * p.Tq + token] = l == 0.f ? neg_inf() : (m + log2f(l)) * kLn2;
-}
-
 // What a CTA knows of a request.
 struct Request {
   int b, n, L;     // first query row, query tokens, keys
   int row_tiles;
-  int blocks;      // 64-key blocks of each of its units (at least one: empty rows are written too)
+  int blocks;      // blocks of keys of each of its units (at least one: empty rows are written too)
   int bad;
 };
 
@@ -131,12 +111,41 @@ __device__ __forceinline__ Request request(const Kv4AttnParams& p, int r) {
   q.L = L;
   const int G = p.Hq / p.cache.Hkv;
   q.row_tiles = (int)(((long long)q.n * G + RT - 1) / RT);
-  q.blocks = max(1, (L + kBlockKeys - 1) / kBlockKeys);
+  q.blocks = max(1, (int)(((long long)L + KB - 1) / KB));
   return q;
 }
 __device__ __forceinline__ long long request_work(const Request& q, int Hkv) {
   return (long long)q.row_tiles * Hkv * q.blocks;
 }
+
+__device__ __forceinline__ int key_limit(const Kv4AttnParams& p, const Request& q, int row) {
+  return p.causal ? max(0, min(q.L, q.L - q.n + row / (p.Hq / p.cache.Hkv) + 1)) : q.L;
+}
+
+// A place on the line of work: block `blk` of unit (r, rt, head).
+struct Walk {
+  long long pos;   // blocks before this place
+  long long base;  // blocks before request r
+  int r;
+  int rt = 0, head = 0, blk = 0, t_end = 0;  // t_end: keys that some row of the unit sees
+  Request rq;
+  // find the unit that holds pos (pos is inside the line)
+  template <int RT>
+  __device__ __forceinline__ void enter(const Kv4AttnParams& p) {
+    long long work;
+    for (;; ++r) {  // (requests without rows have no work)
+      rq = request<RT>(p, r);
+      work = request_work(rq, p.cache.Hkv);
+      if (pos < base + work || r + 1 >= p.R) break;
+      base += work;
+    }
+    const long long unit = (pos - base) / rq.blocks;
+    blk = (int)(pos - base - unit * rq.blocks);
+    rt = (int)(unit / p.cache.Hkv);
+    head = (int)(unit - (long long)rt * p.cache.Hkv);
+    t_end = key_limit(p, rq, min((rt + 1) * RT, rq.n * (p.Hq / p.cache.Hkv)) - 1);
+  }
+};
 
 // One warp's tile in registers.
 template <int D>
@@ -145,25 +154,51 @@ struct TileRegs {
   uint32_t ks[D == 256 ? 2 : 1], vs[D == 256 ? 2 : 1];
 };
 
+// Loads of a lane's share; `at` is the tile's address plus 16 x lane.
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg4(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
 template <int D>
-__device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* tile, int lane) {
+__device__ __forceinline__ void load_k(TileRegs<D>& t, const uint8_t* at, int lane) {
   using L = Kv4Layout<D>;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    t.k[i] = ldg_stream(tile + L::kKCodes + 512 * i + 16 * lane);
-    t.v[i] = ldg_stream(tile + L::kVCodes + 512 * i + 16 * lane);
-  }
+  for (int i = 0; i < D / 64; ++i) t.k[i] = ldg16(at + L::kKCodes + 512 * i);
+  const uint8_t* s = at - 16 * lane + L::kKScales;
   if (D == 64) {
-    t.ks[0] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + 2 * lane);
-    t.vs[0] = *reinterpret_cast<const uint32_t*>(tile + L::kVScales + 4 * ((lane >> 3) * 4 + (lane & 3)));
+    t.ks[0] = ldg4(s + (2 * lane & ~3)) >> (16 * (lane & 1));
   } else if (D == 128) {
-    t.ks[0] = *reinterpret_cast<const uint32_t*>(tile + L::kKScales + 4 * lane);
-    t.vs[0] = *reinterpret_cast<const uint32_t*>(tile + L::kVScales + 4 * lane);
+    t.ks[0] = ldg4(s + 4 * lane);
   } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(tile + L::kKScales + 8 * lane);
-    const uint2 b = *reinterpret_cast<const uint2*>(tile + L::kVScales + 8 * lane);
+    const uint2 a = ldg8(s + 8 * lane);
     t.ks[0] = a.x; t.ks[D == 256 ? 1 : 0] = a.y;
-    t.vs[0] = b.x; t.vs[D == 256 ? 1 : 0] = b.y;
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_v(TileRegs<D>& t, const uint8_t* at, int lane) {
+  using L = Kv4Layout<D>;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) t.v[i] = ldg16(at + L::kVCodes + 512 * i);
+  const uint8_t* s = at - 16 * lane + L::kVScales;
+  if (D == 64) {
+    t.vs[0] = ldg4(s + 4 * ((lane >> 3) * 4 + (lane & 3)));
+  } else if (D == 128) {
+    t.vs[0] = ldg4(s + 4 * lane);
+  } else {
+    const uint2 a = ldg8(s + 8 * lane);
+    t.vs[0] = a.x; t.vs[D == 256 ? 1 : 0] = a.y;
   }
 }
 
@@ -195,8 +230,137 @@ __device__ __forceinline__ uint32_t v_word(const TileRegs<D>& t, int h, int e, i
 template <int D, int NT>
 struct Acc {
   float o[NT][D / 16][4];
-  float m[NT][2], l[NT][2];
+  // the rows' reference (0 while a row has seen no key), the value of x - m that
+  // moves it (-inf while the row has seen no key), and the running sum
+  float m[NT][2], top[NT][2], l[NT][2];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = 0.f;
+      top[nt][0] = top[nt][1] = neg_inf();
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][d][i] = 0.f;
+    }
+  }
+  __device__ __forceinline__ float ref(int nt, int e) const { return top[nt][e] == neg_inf() ? neg_inf() : m[nt][e]; }
 };
+
+// Add the warps' accumulators up in warp 0: all take the rows' largest
+// reference, then half of those left hand theirs to the other half, until one is
+// left.  `sum_l`: l is still one sum per lane.  The buffers of the next call are
+// other ones (ml) or are written behind its first barrier (so).
+template <int D, int NT>
+__device__ __forceinline__ void merge_warps(Acc<D, NT>& acc, float4 (&ml)[kWarps][NT][4], float4* so, int warp, int lane,
+                                            bool sum_l = true) {
+  constexpr int F = NT * (D / 16);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (sum_l)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 4);
+        acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 8);
+        acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 16);
+      }
+    if (lane < 4) ml[warp][nt][lane] = make_float4(acc.ref(nt, 0), acc.ref(nt, 1), acc.l[nt][0], acc.l[nt][1]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float mm[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 x = ml[w][nt][lane & 3];
+      mm[0] = fmaxf(mm[0], x.x);
+      mm[1] = fmaxf(mm[1], x.y);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 x = ml[w][nt][lane & 3];
+      if (x.x != neg_inf()) l[0] += x.z * ex2_approx(x.x - mm[0]);
+      if (x.y != neg_inf()) l[1] += x.w * ex2_approx(x.y - mm[1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float a = acc.ref(nt, e) == neg_inf() ? 0.f : ex2_approx(acc.ref(nt, e) - mm[e]);
+      if (mm[e] != neg_inf()) {
+        acc.m[nt][e] = mm[e];
+        acc.top[nt][e] = kMaxExp;
+      }
+      acc.l[nt][e] = l[e];
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        acc.o[nt][d][e] *= a;
+        acc.o[nt][d][2 + e] *= a;
+      }
+    }
+  }
+#pragma unroll
+  for (int n = kWarps; n > 1; n = (n + 1) / 2) {
+    const int half = (n + 1) / 2;
+    if (n < kWarps) __syncthreads();
+    if (warp >= half && warp < n) {
+      float4* dst = so + (warp - half) * 32 * F + lane;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+          dst[32 * (nt * (D / 16) + d)] =
+              make_float4(acc.o[nt][d][0], acc.o[nt][d][1], acc.o[nt][d][2], acc.o[nt][d][3]);
+    }
+    __syncthreads();
+    if (warp < n - half) {
+      const float4* src = so + warp * 32 * F + lane;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          const float4 x = src[32 * (nt * (D / 16) + d)];
+          acc.o[nt][d][0] += x.x; acc.o[nt][d][1] += x.y; acc.o[nt][d][2] += x.z; acc.o[nt][d][3] += x.w;
+        }
+    }
+  }
+}
+
+// A finished unit's rows: O / l and the log-sum-exp, from warp 0's accumulators.
+template <int D, int NT>
+__device__ __forceinline__ void write_rows(const Kv4AttnParams& p, const Acc<D, NT>& acc, int b, int head, int row0,
+                                           int rows, int G, int lane) {
+  const int r8 = lane >> 2, c4 = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * nt + 2 * c4 + e;
+      if (row >= rows) continue;
+      const int token = b + (row0 + row) / G, h = head * G + (row0 + row) % G;
+      const float l = acc.l[nt][e], inv = l == 0.f ? 0.f : 1.f / l;
+      const size_t off = ((size_t)token * p.Hq + h) * D + r8 * (D / 8);
+#pragma unroll
+      for (int d = 0; d < D / 16; d += 4) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = acc.o[nt][d + i][e] * inv;
+          v[2 * i + 1] = acc.o[nt][d + i][2 + e] * inv;
+        }
+        if (p.o_is_fp32) {
+          float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + off + 2 * d);
+          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + off + 2 * d) =
+              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7]));
+        }
+      }
+      if (r8 == 0) p.lse[(size_t)h * p.Tq + token] = l == 0.f ? neg_inf() : (acc.m[nt][e] + log2f(l)) * kLn2;
+    }
+}
 
 // O^T rows of dims whose V is NaN for a token that a row sees (only reached
 // where a mask runs through the tile; elsewhere the product carries the NaN).
@@ -226,47 +390,55 @@ __device__ __forceinline__ void add_nan(Acc<D, NT>& acc, uint32_t nan0, uint32_t
   }
 }
 
-constexpr int ctas_per_sm(int D, int NT) { return D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2; }
+// CTAs of four warps per SM: as many as the registers of a variant allow
+// (accumulators and query operands 48 NT D / 128 a thread, two tiles 36 D / 128,
+// and about 40 more): 128 registers at four CTAs, 168 at three, 255 at two.
+__host__ __device__ constexpr int ctas_per_sm(int D, int NT) {
+  return D == 64 ? (NT < 3 ? 4 : 3) : D == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : 2;
+}
 
 template <int D, int NT>
 struct AttnCfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kPitch = D + 4;  // floats between rows of the merge buffer
-  static constexpr int kSmem = kWarps * kRows * (kPitch + 2) * 4;
-  static constexpr int kSlot = kRows * (D + 2);  // floats of a partial result: m, l, O
-  // CTAs per SM (registers: 32 NT (D / 128) accumulators and half as many query words)
   static constexpr int kPerSm = ctas_per_sm(D, NT);
+  static constexpr int kFrag = NT * (D / 16);       // float4 accumulators of a lane
+  static constexpr int kSmem = (kWarps / 2) * kFrag * 512;
+  static constexpr int kSlot = (kFrag + NT) * 128;  // floats of a partial result
 };
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_kernel(const Kv4AttnParams p) {
   using C = AttnCfg<D, NT>;
+  using L = Kv4Layout<D>;
   constexpr int RT = C::kRows;
-  extern __shared__ float s_dyn[];
-  float* s_o = s_dyn;                               // [kWarps][RT][kPitch]
-  float* s_m = s_dyn + kWarps * RT * C::kPitch;     // [kWarps][RT]
-  float* s_l = s_m + kWarps * RT;                   // [kWarps][RT]
+  extern __shared__ __align__(128) uint8_t s_dyn[];
+  __shared__ __align__(16) float4 s_ml[2][kWarps][NT][4];  // m and l of a warp's rows, for two units in turn
   __shared__ long long s_sum[kWarps];
   __shared__ long long s_found[2];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r8 = lane >> 2, c4 = lane & 3;
   const int G = p.Hq / p.cache.Hkv, Hkv = p.cache.Hkv;
-  if (tid == 0) s_bad = 0;
+  float4* s_o = reinterpret_cast<float4*>(s_dyn);  // [kWarps / 2][kFrag][32]
+  if (tid == 0) {
+    s_bad = 0;
+    s_found[0] = -1;
+  }
 
   // ---- this CTA's part of the line of work
-  long long total = 0;
   int bad = 0;
-  for (int r = tid; r < p.R; r += kThreads) {
-    const Request q = request<RT>(p, r);
-    total += request_work(q, Hkv);
+  long long mine = 0, total = 0;  // work of request `tid`; of all
+  for (int i = tid; i < p.R; i += kThreads) {
+    const Request q = request<RT>(p, i);
+    const long long w = request_work(q, Hkv);
+    if (i == tid) mine = w;
+    total += w;
     bad = max(bad, q.bad);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
   if (lane == 0) s_sum[warp] = total;
   __syncthreads();
-  if (bad) atomicMax(&s_bad, bad);
   total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += s_sum[w];
@@ -274,11 +446,16 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
   const long long cut = min((long long)gridDim.x, total);
   const bool idle = blockIdx.x >= cut;
   const long long begin = idle ? 0 : total * blockIdx.x / cut, end = idle ? 0 : total * (blockIdx.x + 1) / cut;
-  long long base = 0;  // work before request r
-  int r = 0;
-  if (begin < end) {
+  auto owner = [&](long long x) {  // the CTA whose part holds block x
+    int c = (int)(x * cut / total);
+    while (total * (c + 1) / cut <= x) ++c;
+    while (total * c / cut > x) --c;
+    return c;
+  };
+  Walk wk{begin, 0, 0};
+  if (!idle) {
     for (int r0 = 0; r0 < p.R; r0 += kThreads) {
-      long long w = r0 + tid < p.R ? request_work(request<RT>(p, r0 + tid), Hkv) : 0;
+      const long long w = r0 == 0 ? mine : r0 + tid < p.R ? request_work(request<RT>(p, r0 + tid), Hkv) : 0;
       long long x = w;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -287,9 +464,8 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
       }
       __syncthreads();
       if (lane == 31) s_sum[warp] = x;
-      if (tid == 0) s_found[0] = -1;
       __syncthreads();
-      long long before = base, chunk = 0;
+      long long before = wk.base, chunk = 0;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
         if (i < warp) before += s_sum[i];
@@ -301,37 +477,28 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
       }
       __syncthreads();
       if (s_found[0] >= 0) {
-        r = (int)s_found[0];
-        base = s_found[1];
+        wk.r = (int)s_found[0];
+        wk.base = s_found[1];
         break;
       }
-      base += chunk;
+      wk.base += chunk;
     }
   }
 
-  Kv4Part part{};
-  for (long long pos = begin; pos < end && r < p.R;) {
-    const Request rq = request<RT>(p, r);
-    const long long work = request_work(rq, Hkv);
-    if (pos >= base + work) {  // (requests without rows have no work)
-      base += work;
-      ++r;
-      continue;
-    }
-    const long long unit = (pos - base) / rq.blocks;
-    const int blk0 = (int)(pos - base - unit * rq.blocks);
-    const int nb = (int)min((long long)(rq.blocks - blk0), end - pos);
-    const int rt = (int)(unit / Hkv), head = (int)(unit - (long long)rt * Hkv);
-    const int row0 = rt * RT, rows = min(RT, rq.n * G - row0);
+  int units = 0;
+  while (wk.pos < end) {
+    wk.enter<RT>(p);
+    const Request& rq = wk.rq;
+    const int blk0 = wk.blk, head = wk.head;
+    const int nb = (int)min((long long)(rq.blocks - blk0), end - wk.pos);
+    const int row0 = wk.rt * RT, rows = min(RT, rq.n * G - row0);
+    const int lim_min = key_limit(p, rq, row0), lim_max = wk.t_end;
 
     // ---- query rows: fp16 operands, scales and key limits
     uint32_t qf[NT][D / 16][2];
     float sl2[NT][2];
     int lim[NT][2];
-    auto limit = [&](int row) {
-      return p.causal ? max(0, min(rq.L, rq.L - rq.n + row / G + 1)) : rq.L;
-    };
-    const int lim_min = limit(row0), lim_max = limit(row0 + rows - 1);
+    auto limit = [&](int row) { return key_limit(p, rq, row); };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = row0 + 8 * nt + r8;
@@ -376,38 +543,34 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
     }
 
     Acc<D, NT> acc;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      acc.m[nt][0] = acc.m[nt][1] = neg_inf();
-      acc.l[nt][0] = acc.l[nt][1] = 0.f;
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc.o[nt][d][i] = 0.f;
-    }
+    acc.clear();
 
-    // ---- this warp's tiles: keys t0, t0 + 64, ...
-    const int32_t* table = p.block_table + (size_t)r * p.table_stride;
-    int t0 = blk0 * kBlockKeys + 16 * warp;
-    const int t_end = min((blk0 + nb) * kBlockKeys, lim_max);
-    auto page_of = [&](int t) -> int { return t < t_end ? table[t >> p.cache.page_shift] : 0; };
+    // ---- this warp's tiles: keys t0, t0 + KB, ...  The next tile's words and the
+    // page id after that are under way while one is worked on.  For a page that is
+    // not one of the cache, page 0 is read instead, and masked.
+    const int t_stop = min((blk0 + nb) * KB, lim_max);
+    const int32_t* table = p.block_table + (size_t)wk.r * p.table_stride;
+    const int tiles_mask = (1 << (p.cache.page_shift - 4)) - 1;
+    const uint8_t* base = p.cache.pages + ((size_t)head << (p.cache.page_shift - 4)) * L::kBytes + 16 * lane;
+    auto page_of = [&](int t) -> int { return t < t_stop ? table[t >> p.cache.page_shift] : 0; };
     auto fetch = [&](TileRegs<D>& t, int page, int tok) {
-      // a page id outside the cache: read page 0, and mask the tile
-      const int64_t pg = (uint32_t)page < (uint64_t)p.cache.num_pages ? page : 0;
-      load_tile<D>(t, p.cache.pages + kv4_tile_offset<D>(p.cache, pg, head, tok & ((1 << p.cache.page_shift) - 1)),
-                   lane);
+      const uint32_t pg = (uint32_t)page < (uint64_t)p.cache.num_pages ? page : 0;
+      const uint8_t* at = base + (int64_t)pg * p.page_bytes + ((tok >> 4) & tiles_mask) * L::kBytes;
+      load_k<D>(t, at, lane);
+      load_v<D>(t, at, lane);
     };
+    int t0 = blk0 * KB + 16 * warp;
     TileRegs<D> next;
-    int page = page_of(t0), page_next = page_of(t0 + kBlockKeys);
-    if (t0 < t_end) fetch(next, page, t0);
-    for (; t0 < t_end; t0 += kBlockKeys) {
+    int page = page_of(t0), page_next = page_of(t0 + KB);
+    if (t0 < t_stop) fetch(next, page, t0);
+#pragma unroll 1
+    for (; t0 < t_stop; t0 += KB) {
       TileRegs<D> cur = next;
       const bool page_ok = (uint32_t)page < (uint64_t)p.cache.num_pages;
       if (!page_ok) bad = RA_KV4_BAD_PAGE;
       page = page_next;
-      if (t0 + kBlockKeys < t_end) fetch(next, page, t0 + kBlockKeys);
-      page_next = page_of(t0 + 2 * kBlockKeys);
-
+      if (t0 + KB < t_stop) fetch(next, page, t0 + KB);
+      page_next = page_of(t0 + 2 * KB);
       // S^T = K Q^T
       float s[NT][4];
 #pragma unroll
@@ -419,18 +582,18 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
         kv4_code_pairs(k_word<D>(cur, 1, i), hi);
         const uint32_t sa = k_scale2<D>(cur, 0, i >> 1), sb = k_scale2<D>(cur, 1, i >> 1);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t a[4] = {hmul2(lo[2 * j], sa), hmul2(hi[2 * j], sb), hmul2(lo[2 * j + 1], sa),
-                                 hmul2(hi[2 * j + 1], sb)};
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t a[4] = {hmul2(lo[2 * k], sa), hmul2(hi[2 * k], sb), hmul2(lo[2 * k + 1], sa),
+                                 hmul2(hi[2 * k + 1], sb)};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * i + j]);
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * i + k]);
         }
       }
-      // log2 units and the mask
+      // x - m in log2 units, and the mask
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] *= sl2[nt][i & 1];
+        for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(s[nt][i], sl2[nt][i & 1], -acc.m[nt][i & 1]);
       uint32_t nan0 = 0, nan1 = 0;
       const bool masked = t0 + 16 > lim_min || !page_ok;
       if (masked) {
@@ -458,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) over |= s[nt][i] - kMaxExp > acc.m[nt][i & 1];
+        for (int e = 0; e < 2; ++e) over |= fmaxf(s[nt][e], s[nt][2 + e]) > acc.top[nt][e];
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -468,11 +631,14 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-            if (mt - kMaxExp > acc.m[nt][e]) {
-              const float m_new = ceilf(mt) - kHeadroom;
-              const float alpha = ex2_approx(acc.m[nt][e] - m_new);
-              acc.m[nt][e] = m_new;
+            if (mt > acc.top[nt][e]) {
+              const float up = ceilf(mt) - kHeadroom;  // the reference moves by this much
+              const float alpha = acc.top[nt][e] == neg_inf() ? 0.f : ex2_approx(-up);
+              acc.m[nt][e] += up;
+              acc.top[nt][e] = kMaxExp;
               acc.l[nt][e] *= alpha;
+              s[nt][e] -= up;
+              s[nt][2 + e] -= up;
 #pragma unroll
               for (int d = 0; d < D / 16; ++d) {
                 acc.o[nt][d][e] *= alpha;
@@ -488,8 +654,7 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
         float x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float m = acc.m[nt][i & 1];
-          x[i] = ex2_approx(s[nt][i] - (m == neg_inf() ? 0.f : m));
+          x[i] = ex2_approx(s[nt][i]);
           acc.l[nt][i & 1] += x[i];
         }
         pf[nt][0] = transpose8x8(pack_f16x2(x[0], x[1]));
@@ -508,154 +673,112 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
         const uint32_t vs = cur.vs[D == 256 ? i >> 1 : 0];
         const uint32_t sa = scale_pair(vs, 0, 1), sb = scale_pair(vs, 2, 3);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a[4] = {hmul2(ev[0][j], sa), hmul2(od[0][j], sa), hmul2(ev[1][j], sb), hmul2(od[1][j], sb)};
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t a[4] = {hmul2(ev[0][k], sa), hmul2(od[0][k], sa), hmul2(ev[1][k], sb), hmul2(od[1][k], sb)};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(acc.o[nt][4 * i + j], a, pf[nt]);
+          for (int nt = 0; nt < NT; ++nt) mma16816(acc.o[nt][4 * i + k], a, pf[nt]);
         }
       }
       if (masked && __any_sync(0xffffffffu, (nan0 | nan1) != 0)) add_nan<D, NT>(acc, nan0, nan1, t0, lim, lane);
     }
 
-    // ---- merge the warps
+    // ---- merge the warps; warp 0 then holds the segment's result
+    merge_warps<D, NT>(acc, s_ml[units & 1], s_o, warp, lane);
+    ++units;
+    const bool direct = blk0 == 0 && nb == rq.blocks;
+    if (direct) {
+      if (warp == 0) write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
+    } else {
+      // a partial result; the CTA that brings a unit's last one merges them all
+      const long long first = wk.pos - blk0, last = first + rq.blocks - 1;
+      const int c0 = owner(first), parts = owner(last) - c0 + 1;
+      auto slot = [&](int c) {
+        return reinterpret_cast<float4*>(p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * C::kSlot);
+      };
+      if (warp == 0) {
+        float4* dst = slot(blockIdx.x);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          dst[32 * nt + lane] = make_float4(acc.ref(nt, 0), acc.ref(nt, 1), acc.l[nt][0], acc.l[nt][1]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = acc.l[nt][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (r8 == 0) {
-          s_m[warp * RT + 8 * nt + 2 * c4 + e] = acc.m[nt][e];
-          s_l[warp * RT + 8 * nt + 2 * c4 + e] = l;
+          for (int d = 0; d < D / 16; ++d)
+            dst[32 * (NT + nt * (D / 16) + d) + lane] =
+                make_float4(acc.o[nt][d][0], acc.o[nt][d][1], acc.o[nt][d][2], acc.o[nt][d][3]);
         }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) s_last = atomicAdd(&p.tickets[c0], 1) == parts - 1;
       }
-    __syncthreads();
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        acc.clear();
+        // the rows' largest reference first: the weights, and with them all loads
+        // of the partial results, then depend on nothing
+        float mm[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) mm[nt][0] = mm[nt][1] = neg_inf();
+#pragma unroll 4
+        for (int i = r8; i < parts; i += 8)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 8 * nt + 2 * c4 + e;
-        float mm = neg_inf();
+          for (int nt = 0; nt < NT; ++nt) {
+            const float4 ml = __ldcg(slot(c0 + i) + 32 * nt + lane);
+            mm[nt][0] = fmaxf(mm[nt][0], ml.x);
+            mm[nt][1] = fmaxf(mm[nt][1], ml.y);
+          }
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * RT + row]);
-        const float a = acc.m[nt][e] == neg_inf() ? 0.f : ex2_approx(acc.m[nt][e] - mm);
-        float* dst = s_o + (warp * RT + row) * C::kPitch + r8 * (D / 8);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-          *reinterpret_cast<float2*>(dst + 2 * d) = make_float2(acc.o[nt][d][e] * a, acc.o[nt][d][2 + e] * a);
-      }
-    __syncthreads();
-    const bool starts = blk0 == 0, ends = blk0 + nb == rq.blocks;
-    const bool direct = starts && ends;
-    float* slot = p.partials + ((size_t)blockIdx.x * 2 + (starts ? 1 : 0)) * C::kSlot;
-    for (int i = tid; i < rows * (D / 4); i += kThreads) {
-      const int row = i / (D / 4), d4 = i % (D / 4);
-      float mm = neg_inf(), l = 0.f;
+          for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * RT + row]);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int d = 4; d < 32; d <<= 1) mm[nt][e] = fmaxf(mm[nt][e], __shfl_xor_sync(0xffffffffu, mm[nt][e], d));
+            if (mm[nt][e] != neg_inf()) {
+              acc.m[nt][e] = mm[nt][e];
+              acc.top[nt][e] = kMaxExp;
+            }
+          }
+#pragma unroll 4
+        for (int i = warp; i < parts; i += kWarps) {
+          const float4* src = slot(c0 + i);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = s_m[w * RT + row];
-        l += mw == neg_inf() ? 0.f : s_l[w * RT + row] * ex2_approx(mw - mm);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * RT + row) * C::kPitch + 4 * d4);
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-      }
-      if (direct) {
-        kv4_write_row(p, rq.b + (row0 + row) / G, head * G + (row0 + row) % G, D, d4, v, mm, l);
-      } else {
-        *reinterpret_cast<float4*>(slot + 2 * RT + row * D + 4 * d4) = v;
-        if (d4 == 0) {
-          slot[row] = mm;
-          slot[RT + row] = l;
+          for (int nt = 0; nt < NT; ++nt) {
+            if (8 * nt + 2 * c4 >= rows) continue;  // rows that nobody asks for
+            const float4 ml = __ldcg(src + 32 * nt + lane);
+            const float w0 = ml.x == neg_inf() ? 0.f : ex2_approx(ml.x - mm[nt][0]);
+            const float w1 = ml.y == neg_inf() ? 0.f : ex2_approx(ml.y - mm[nt][1]);
+            acc.l[nt][0] = fmaf(ml.z, w0, acc.l[nt][0]);
+            acc.l[nt][1] = fmaf(ml.w, w1, acc.l[nt][1]);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              const float4 x = __ldcg(src + 32 * (NT + nt * (D / 16) + d) + lane);
+              acc.o[nt][d][0] = fmaf(x.x, w0, acc.o[nt][d][0]);
+              acc.o[nt][d][1] = fmaf(x.y, w1, acc.o[nt][d][1]);
+              acc.o[nt][d][2] = fmaf(x.z, w0, acc.o[nt][d][2]);
+              acc.o[nt][d][3] = fmaf(x.w, w1, acc.o[nt][d][3]);
+            }
+          }
+        }
+        merge_warps<D, NT>(acc, s_ml[units & 1], s_o, warp, lane, false);
+        ++units;
+        if (warp == 0) {
+          write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
+          if (lane == 0) p.tickets[c0] = 0;  // as the next call expects it
         }
       }
     }
-    if (starts && !ends) {
-      part.request = r;
-      part.row_tile = rt;
-      part.head = head;
-      // the CTA that holds the unit's last block
-      const long long last = base + (unit + 1) * rq.blocks - 1;
-      int c = (int)(last * cut / total);
-      while (total * (c + 1) / cut <= last) ++c;
-      while (total * c / cut > last) --c;
-      part.parts = c - (int)blockIdx.x + 1;
-    }
-    __syncthreads();  // the merge buffers are free again
-    pos += nb;
+    wk.pos += nb;
   }
   if (bad) atomicMax(&s_bad, bad);
   __syncthreads();
   if (tid == 0) {
-    part.status = s_bad;
-    p.parts[blockIdx.x] = part;
-  }
-}
-
-// Merge the partial results of the units that span CTAs: block (c, row) the
-// unit that CTA c began.  Block (0, 0) also gathers the CTAs' status.
-template <int D>
-__global__ void __launch_bounds__(256) kv4_merge_kernel(const Kv4AttnParams p, int rt_rows, int ctas) {
-  constexpr int V = D / 32;
-  __shared__ float s_o[8][D];
-  __shared__ float s_l[8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    int st = 0;
-    for (int c = tid; c < ctas; c += 256) st = max(st, p.parts[c].status);
-    st = __reduce_max_sync(0xffffffffu, st);
-    __shared__ int s_st[8];
-    if (lane == 0) s_st[warp] = st;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < 8; ++w) st = max(st, s_st[w]);
-      *p.status = st;
+    // the last CTA to end turns what was found into the call's status
+    if (s_bad) atomicMax(p.found, s_bad);
+    __threadfence();
+    if (atomicAdd(p.ended, 1) == (int)gridDim.x - 1) {
+      __threadfence();
+      *p.status = atomicExch(p.found, 0);
+      *p.ended = 0;
     }
-  }
-  const Kv4Part part = p.parts[blockIdx.x];
-  if (part.parts == 0) return;
-  const int G = p.Hq / p.cache.Hkv;
-  int b = p.cu_q[part.request], e = p.cu_q[part.request + 1];
-  b = min(max(b, 0), p.Tq);
-  e = min(max(e, b), p.Tq);
-  const int row = blockIdx.y, grow = part.row_tile * rt_rows + row;
-  if (grow >= (e - b) * G) return;
-  const size_t slot_floats = (size_t)rt_rows * (D + 2);
-  auto slot = [&](int i) {
-    return p.partials + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * slot_floats;
-  };
-  float mm = neg_inf();
-  for (int i = lane; i < part.parts; i += 32) mm = fmaxf(mm, slot(i)[row]);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-  float o[V], l = 0.f;
-#pragma unroll
-  for (int j = 0; j < V; ++j) o[j] = 0.f;
-  for (int i = warp; i < part.parts; i += 8) {
-    const float* s = slot(i);
-    const float m = s[row];
-    const float a = m == neg_inf() ? 0.f : ex2_approx(m - mm);
-    l += m == neg_inf() ? 0.f : s[rt_rows + row] * a;
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] += s[2 * rt_rows + row * D + 32 * j + lane] * a;
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j) s_o[warp][32 * j + lane] = o[j];
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  if (tid < D / 4) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float4 x = *reinterpret_cast<const float4*>(&s_o[w][4 * tid]);
-      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-      l += s_l[w];
-    }
-    kv4_write_row(p, b + grow / G, part.head * G + grow % G, D, tid, v, mm, l);
   }
 }
 
@@ -666,8 +789,6 @@ cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, C::kSmem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kv4_merge_kernel<D><<<dim3(ctas, C::kRows), 256, 0, stream>>>(p, C::kRows, ctas);
   return cudaGetLastError();
 }
 
@@ -677,7 +798,7 @@ Kv4AttnShape kv4_attn_shape(int D, int G, int max_q_len, int sms) {
   const long long rows = (long long)G * max_q_len;
   int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 3;
   if (D == 256) nt = nt > 2 ? 2 : nt;
-  return Kv4AttnShape{8 * nt, ctas_per_sm(D, nt) * (sms < kKv4MaxSms ? sms : kKv4MaxSms), (size_t)8 * nt * (D + 2)};
+  return Kv4AttnShape{8 * nt, ctas_per_sm(D, nt) * (sms < kKv4MaxSms ? sms : kKv4MaxSms), (size_t)8 * nt * (D + 16)};
 }
 
 cudaError_t launch_kv4_attn(int D, const Kv4AttnShape& s, const Kv4AttnParams& p, cudaStream_t stream) {

@@ -205,7 +205,7 @@ def kv4_attention_workspace(cache, num_q_tokens, num_q_heads, max_q_len=None):
     longest = max(1, int(num_q_tokens if max_q_len is None else max_q_len))
     _ra._check(lib.ra_kv4_attention_workspace_bytes(int(num_q_heads), cache.num_kv_heads, cache.head_dim, longest,
                                                     ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
+    return torch.zeros(n.value, dtype=torch.uint8, device=cache.device)
 
 
 def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None, o_fp32=False, max_q_len=None,

@@ -521,7 +521,8 @@ ra_status ra_kv4_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_h
  *   lse fp32 [num_q_heads, num_q_tokens], natural log.
  * A row that sees no key gets o = 0 and lse = -inf.  Rows outside
  * [cu_q[0], cu_q[R]) are left as they were.  The workspace (device, 256-byte
- * aligned) must not be shared by calls that may overlap; its first word is the
+ * aligned) must be zero before its first use (a call leaves it ready for the
+ * next) and must not be shared by calls that may overlap; its first word is the
  * status of the last call (ra_kv4_status): a page id outside the cache, a length
  * or an offset out of range is left out of the result and reported there.
  */
