@@ -127,6 +127,8 @@ struct Kv4AttnParams {
   // Zero between calls: what the CTAs found wrong (RA_KV4_BAD_...), how many of
   // them have ended, and how many partial results the unit that a CTA began has.
   int32_t *found, *ended, *tickets;
+  int32_t status_kept;  // the status holds what the other kernel of this call found
+  int32_t split_rows;   // rows (query tokens x heads of a group) from which a request is the tile kernel's; 0: see kv4_walk.cuh
   float* partials;  // two slots per CTA: [0] of a unit that an earlier CTA began, [1] of one that this CTA began
 };
 
@@ -134,15 +136,18 @@ cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_store(int D, const Kv4RowsParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_load(int D, const Kv4RowsParams& p, cudaStream_t stream);
 
-// The attention kernel's variant for a call: query rows (tokens x query heads of
-// a group) of one CTA, CTAs on a GPU with `sms` SMs, and the floats of one
-// partial-result slot (two slots a CTA).
+// Variant of the kernel for few rows (kv4_attn.cu): query rows of one CTA, CTAs
+// on a GPU with `sms` SMs, and the floats of one partial-result slot (two slots a
+// CTA).  `rows`: the rows (tokens x heads of a group) that most requests bring.
 struct Kv4AttnShape {
   int rows, ctas;
   size_t slot_floats;
 };
 constexpr int kKv4MaxSms = 160;  // workspaces are sized for this many SMs
-Kv4AttnShape kv4_attn_shape(int D, int G, int max_q_len, int sms);
+Kv4AttnShape kv4_attn_shape(int D, long long rows, int sms);
+// The tile kernel (kv4_tile.cu): one CTA an SM, head_dim 64 and 128.
+constexpr size_t kv4_tile_slot_floats(int D) { return 256 * ((size_t)D + 2); }
+cudaError_t launch_kv4_tile(int D, int ctas, const Kv4AttnParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_attn(int D, const Kv4AttnShape& shape, const Kv4AttnParams& p, cudaStream_t stream);
 
 }  // namespace ra

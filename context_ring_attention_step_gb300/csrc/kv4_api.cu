@@ -2,6 +2,7 @@
 // and launches.  Nothing here allocates or synchronises (ra_kv4_status does).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -55,15 +56,32 @@ size_t page_bytes(int32_t page_size, int32_t Hkv, int32_t D) {
   return (size_t)(page_size / ra::kKv4Tile) * ra::kv4_tile_bytes(D) * Hkv;
 }
 
+// Requests with at least this many rows (tokens x heads of a group) go to the
+// tile kernel, where a call can have them.
+constexpr int kTileMinRows = 64;
+bool has_tiles(int32_t D, int32_t G, int32_t max_q_len) {
+  return D <= 128 && (int64_t)G * max_q_len >= kTileMinRows;
+}
+// Rows that the other kernel's CTAs take: those of the longest request, or of
+// one token where the tile kernel takes the long ones.
+int64_t few_rows(int32_t D, int32_t G, int32_t max_q_len) {
+  return has_tiles(D, G, max_q_len) ? G : (int64_t)G * max_q_len;
+}
+
 struct AttnLayout {
   size_t tickets, partials, total;
 };
 AttnLayout attn_layout(int32_t D, int32_t G, int32_t max_q_len) {
-  const ra::Kv4AttnShape s = ra::kv4_attn_shape(D, G, max_q_len, ra::kKv4MaxSms);
+  const ra::Kv4AttnShape s = ra::kv4_attn_shape(D, few_rows(D, G, max_q_len), ra::kKv4MaxSms);
+  size_t ctas = s.ctas, floats = (size_t)s.ctas * 2 * s.slot_floats;
+  if (has_tiles(D, G, max_q_len)) {
+    ctas = std::max(ctas, (size_t)ra::kKv4MaxSms);
+    floats = std::max(floats, (size_t)ra::kKv4MaxSms * 2 * ra::kv4_tile_slot_floats(D));
+  }
   AttnLayout l;
   l.tickets = kHeader;
-  l.partials = align256(l.tickets + (size_t)s.ctas * sizeof(int32_t));
-  l.total = align256(l.partials + (size_t)s.ctas * 2 * s.slot_floats * sizeof(float));
+  l.partials = align256(l.tickets + ctas * sizeof(int32_t));
+  l.total = align256(l.partials + floats * sizeof(float));
   return l;
 }
 
@@ -230,8 +248,19 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  e = ra::launch_kv4_attn(D, ra::kv4_attn_shape(D, num_q_heads / Hkv, max_q_len, sms), p, st);
-  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache attention launch");
+  const int32_t G = num_q_heads / Hkv;
+  const bool tiles = has_tiles(D, G, max_q_len);
+  if (!tiles || num_requests > 1) {  // (a single long request is the tile kernel's, whatever its real length)
+    p.split_rows = tiles ? kTileMinRows : 0;
+    e = ra::launch_kv4_attn(D, ra::kv4_attn_shape(D, few_rows(D, G, max_q_len), sms), p, st);
+    if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
+    p.status_kept = 1;
+  }
+  if (tiles) {
+    e = ra::launch_kv4_tile(D, std::min(sms, ra::kKv4MaxSms), p, st);
+    if (e != cudaSuccess) return cuda_fail(e, "cache attention launch (row tiles)");
+  }
+  return RA_OK;
 }
 
 ra_status ra_kv4_status(const void* status, void* stream_) {

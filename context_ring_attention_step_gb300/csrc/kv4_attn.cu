@@ -34,6 +34,7 @@
 
 #include "kv4.cuh"
 #include "kv4.h"
+#include "kv4_walk.cuh"
 #include "tc.cuh"
 
 namespace ra {
@@ -42,15 +43,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int KB = 16 * kWarps;  // keys of one block: a tile a warp
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kLog2e = 1.4426950408889634f;
 // P's reference: a row's largest P is in (2^6, 2^7] when the reference moves,
 // and it moves when a P would pass 2^15.
 constexpr float kHeadroom = 7.f;
 constexpr float kMaxExp = 15.f;
-
-__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -64,89 +60,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// Scale byte `i` of a word as fp16 in both halves; bytes i and j in low and high half.
-__device__ __forceinline__ uint32_t scale_both(uint32_t w, int i) {
-  return __byte_perm(w, 0, 0x0404 | (i << 4) | (i << 12)) >> 1;
-}
-__device__ __forceinline__ uint32_t scale_pair(uint32_t w, int i, int j) {
-  return __byte_perm(w, 0, 0x0404 | (i << 4) | (j << 12)) >> 1;
-}
-
-// What a CTA knows of a request.
-struct Request {
-  int b, n, L;     // first query row, query tokens, keys
-  int row_tiles;
-  int blocks;      // blocks of keys of each of its units (at least one: empty rows are written too)
-  int bad;
-};
-
-template <int RT>
-__device__ __forceinline__ Request request(const Kv4AttnParams& p, int r) {
-  Request q;
-  int b = p.cu_q[r], e = p.cu_q[r + 1];
-  int L = p.kv_lens[r];
-  q.bad = 0;
-  if (b < 0 || e < b || e > p.Tq) {
-    q.bad = RA_KV4_BAD_OFFSET;
-    b = min(max(b, 0), p.Tq);
-    e = min(max(e, b), p.Tq);
-  }
-  const long long cap = (long long)p.table_width << p.cache.page_shift;
-  if (L < 0 || L > cap) {
-    q.bad = RA_KV4_BAD_LENGTH;
-    L = L < 0 ? 0 : (int)cap;
-  }
-  q.b = b;
-  q.n = e - b;
-  q.L = L;
-  const int G = p.Hq / p.cache.Hkv;
-  q.row_tiles = (int)(((long long)q.n * G + RT - 1) / RT);
-  q.blocks = max(1, (int)(((long long)L + KB - 1) / KB));
-  return q;
-}
-__device__ __forceinline__ long long request_work(const Request& q, int Hkv) {
-  return (long long)q.row_tiles * Hkv * q.blocks;
-}
-
-__device__ __forceinline__ int key_limit(const Kv4AttnParams& p, const Request& q, int row) {
-  return p.causal ? max(0, min(q.L, q.L - q.n + row / (p.Hq / p.cache.Hkv) + 1)) : q.L;
-}
-
-// A place on the line of work: block `blk` of unit (r, rt, head).
-struct Walk {
-  long long pos;   // blocks before this place
-  long long base;  // blocks before request r
-  int r;
-  int rt = 0, head = 0, blk = 0, t_end = 0;  // t_end: keys that some row of the unit sees
-  Request rq;
-  // find the unit that holds pos (pos is inside the line)
-  template <int RT>
-  __device__ __forceinline__ void enter(const Kv4AttnParams& p) {
-    long long work;
-    for (;; ++r) {  // (requests without rows have no work)
-      rq = request<RT>(p, r);
-      work = request_work(rq, p.cache.Hkv);
-      if (pos < base + work || r + 1 >= p.R) break;
-      base += work;
-    }
-    const long long unit = (pos - base) / rq.blocks;
-    blk = (int)(pos - base - unit * rq.blocks);
-    rt = (int)(unit / p.cache.Hkv);
-    head = (int)(unit - (long long)rt * p.cache.Hkv);
-    t_end = key_limit(p, rq, min((rt + 1) * RT, rq.n * (p.Hq / p.cache.Hkv)) - 1);
-  }
-};
-
 // One warp's tile in registers.
 template <int D>
 struct TileRegs {
@@ -420,85 +333,26 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
   const int r8 = lane >> 2, c4 = lane & 3;
   const int G = p.Hq / p.cache.Hkv, Hkv = p.cache.Hkv;
   float4* s_o = reinterpret_cast<float4*>(s_dyn);  // [kWarps / 2][kFrag][32]
-  if (tid == 0) {
-    s_bad = 0;
-    s_found[0] = -1;
-  }
+  if (tid == 0) s_bad = 0;
 
-  // ---- this CTA's part of the line of work
   int bad = 0;
-  long long mine = 0, total = 0;  // work of request `tid`; of all
-  for (int i = tid; i < p.R; i += kThreads) {
-    const Request q = request<RT>(p, i);
-    const long long w = request_work(q, Hkv);
-    if (i == tid) mine = w;
-    total += w;
-    bad = max(bad, q.bad);
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  if (lane == 0) s_sum[warp] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s_sum[w];
-  // no part is empty: a unit's partial results then lie in consecutive CTAs
-  const long long cut = min((long long)gridDim.x, total);
-  const bool idle = blockIdx.x >= cut;
-  const long long begin = idle ? 0 : total * blockIdx.x / cut, end = idle ? 0 : total * (blockIdx.x + 1) / cut;
-  auto owner = [&](long long x) {  // the CTA whose part holds block x
-    int c = (int)(x * cut / total);
-    while (total * (c + 1) / cut <= x) ++c;
-    while (total * c / cut > x) --c;
-    return c;
-  };
-  Walk wk{begin, 0, 0};
-  if (!idle) {
-    for (int r0 = 0; r0 < p.R; r0 += kThreads) {
-      const long long w = r0 == 0 ? mine : r0 + tid < p.R ? request_work(request<RT>(p, r0 + tid), Hkv) : 0;
-      long long x = w;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_sum[warp] = x;
-      __syncthreads();
-      long long before = wk.base, chunk = 0;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += s_sum[i];
-        chunk += s_sum[i];
-      }
-      if (begin >= before + x - w && begin < before + x) {
-        s_found[0] = r0 + tid;
-        s_found[1] = before + x - w;
-      }
-      __syncthreads();
-      if (s_found[0] >= 0) {
-        wk.r = (int)s_found[0];
-        wk.base = s_found[1];
-        break;
-      }
-      wk.base += chunk;
-    }
-  }
+  Kv4Walk wk;
+  const Kv4Line line = kv4_find_part<RT, KB, false, kThreads>(p, s_sum, s_found, wk, bad);
 
   int units = 0;
-  while (wk.pos < end) {
-    wk.enter<RT>(p);
-    const Request& rq = wk.rq;
+  while (wk.pos < line.end) {
+    wk.enter<RT, KB, false>(p);
+    const Kv4Request& rq = wk.rq;
     const int blk0 = wk.blk, head = wk.head;
-    const int nb = (int)min((long long)(rq.blocks - blk0), end - wk.pos);
+    const int nb = (int)min((long long)(rq.blocks - blk0), line.end - wk.pos);
     const int row0 = wk.rt * RT, rows = min(RT, rq.n * G - row0);
-    const int lim_min = key_limit(p, rq, row0), lim_max = wk.t_end;
+    const int lim_min = kv4_key_limit(p, rq, row0), lim_max = wk.t_end;
 
     // ---- query rows: fp16 operands, scales and key limits
     uint32_t qf[NT][D / 16][2];
     float sl2[NT][2];
     int lim[NT][2];
-    auto limit = [&](int row) { return key_limit(p, rq, row); };
+    auto limit = [&](int row) { return kv4_key_limit(p, rq, row); };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = row0 + 8 * nt + r8;
@@ -521,12 +375,8 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // a power of two that brings the row's largest element to about 1; a row
-      // of zeros or with an infinity or NaN stays as it is
-      int ex = (int)(mx >> 7) - 127;
-      ex = mx == 0 || mx >= 0x7f80 ? 0 : min(max(ex, -126), 126);
-      const float up = __uint_as_float((uint32_t)(127 - ex) << 23);
-      const float down = __uint_as_float((uint32_t)(127 + ex) << 23);
+      float up;
+      const float down = kv4_row_scale(mx, up);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         const uint32_t a = word(w[j / 2], 2 * (j & 1)), b = word(w[j / 2], 2 * (j & 1) + 1);
@@ -691,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
     } else {
       // a partial result; the CTA that brings a unit's last one merges them all
       const long long first = wk.pos - blk0, last = first + rq.blocks - 1;
-      const int c0 = owner(first), parts = owner(last) - c0 + 1;
+      const int c0 = line.owner(first), parts = line.owner(last) - c0 + 1;
       auto slot = [&](int c) {
         return reinterpret_cast<float4*>(p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * C::kSlot);
       };
@@ -770,16 +620,7 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
   }
   if (bad) atomicMax(&s_bad, bad);
   __syncthreads();
-  if (tid == 0) {
-    // the last CTA to end turns what was found into the call's status
-    if (s_bad) atomicMax(p.found, s_bad);
-    __threadfence();
-    if (atomicAdd(p.ended, 1) == (int)gridDim.x - 1) {
-      __threadfence();
-      *p.status = atomicExch(p.found, 0);
-      *p.ended = 0;
-    }
-  }
+  if (tid == 0) kv4_end(p, s_bad);
 }
 
 template <int D, int NT>
@@ -794,10 +635,9 @@ cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-Kv4AttnShape kv4_attn_shape(int D, int G, int max_q_len, int sms) {
-  const long long rows = (long long)G * max_q_len;
+Kv4AttnShape kv4_attn_shape(int D, long long rows, int sms) {
   int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 3;
-  if (D == 256) nt = nt > 2 ? 2 : nt;
+  if (D == 256) nt = 1;
   return Kv4AttnShape{8 * nt, ctas_per_sm(D, nt) * (sms < kKv4MaxSms ? sms : kKv4MaxSms), (size_t)8 * nt * (D + 16)};
 }
 
@@ -810,7 +650,6 @@ cudaError_t launch_kv4_attn(int D, const Kv4AttnShape& s, const Kv4AttnParams& p
   if (D == 128 && nt == 2) return launch<128, 2>(s.ctas, p, stream);
   if (D == 128 && nt == 3) return launch<128, 3>(s.ctas, p, stream);
   if (D == 256 && nt == 1) return launch<256, 1>(s.ctas, p, stream);
-  if (D == 256 && nt == 2) return launch<256, 2>(s.ctas, p, stream);
   return cudaErrorInvalidValue;
 }
 

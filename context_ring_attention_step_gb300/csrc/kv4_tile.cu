@@ -1,0 +1,672 @@
+// kv4_tile.cu -- attention over the paged 4-bit cache for requests with many
+// query rows (the next part of a prompt over what is cached), on tcgen05 tensor
+// cores.  Formulas as in kv4_attn.cu.
+//
+// Here the products dominate: 4 D flops a row and key against 1.125 D bytes a
+// key.  A CTA takes 256 query rows (tokens x query heads of one key/value head)
+// as two 128-row tiles, so that a key tile is expanded once for both; four warps
+// expand it from registers into the swizzled shared-memory layout that the
+// tensor cores read, ahead of the products.  Expanding 128 keys and values costs
+// each of them about 350 instructions, next to the 2048 cycles that their products take.
+//
+// Warp roles (512 threads):
+//   warps 0, 1    UMMA issuers of Q tiles 0 and 1 (warp 0 owns tensor memory)
+//   warps 4-11    softmax, output and merge of Q tile 0 (4-7) and 1 (8-11); a
+//                 thread is a row, and loads it: fp16 after a power of two
+//   warps 12-15   cache tiles -> fp16 K and V tiles in a ring of stages
+// Tensor memory (512 columns): S0 [0,128), S1 [128,256), O0, O1 behind them; P
+// (fp16) overwrites the first 64 columns of its S and feeds P.V from there.
+// Stages hold K(0), V(0), K(1), V(1), ...; both issuers release each of them.
+// The CTAs cut the line of work evenly and merge partial results as in
+// kv4_attn.cu.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv4.cuh"
+#include "kv4.h"
+#include "kv4_walk.cuh"
+#include "tc.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kRows = 256;
+constexpr int kKeys = 128;
+constexpr int kThreads = 512;
+constexpr int kSegs = 8;  // segments (and key tiles) that the expanding warps may be ahead, rounded up
+// P's reference as in kv4_attn.cu: the row's largest P is in (2^6, 2^7] when it
+// moves.  A tile whose P's add up to no more than 2^15 needs no look at its maximum.
+constexpr float kHeadroom = 7.f;
+constexpr float kMaxExp = 14.f;
+constexpr float kSumLimit = 32768.f;
+
+// fp16 x fp16 -> fp32 (formats 0 where idesc_bf16_f32 has 1)
+constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+template <int D>
+struct TileCfg {
+  static constexpr int kTile = 128 * D * 2;  // bytes of one 128-row fp16 tile
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kQBytes = 2 * kTile;
+  static constexpr int kBarOff = kQBytes + kStages * kTile;
+  static constexpr int kSmem = kBarOff + 1024 + 1024;  // barriers and notes, alignment slack
+  static constexpr int kSlot = kRows * (D + 2);        // floats of a partial result: m, l, O
+  static constexpr uint32_t kIdescQK = idesc_f16_f32(128, 128, false);
+  static constexpr uint32_t kIdescPV = idesc_f16_f32(128, D, true);
+};
+
+// What all roles know of a segment.
+struct Segment {
+  int nb, k0, row0, rows;  // blocks of the line; first key; first row of the unit, rows
+  int n;                   // key tiles that some row sees
+  int na[2];               // of these, those that a row of Q tile 0 / 1 sees (a prefix)
+  int lim_lo[2];           // keys that the tile's first row sees
+};
+
+__device__ __forceinline__ Segment segment(const Kv4AttnParams& p, const Kv4Walk& wk, long long end) {
+  Segment s;
+  const int G = p.Hq / p.cache.Hkv;
+  s.nb = (int)min((long long)(wk.rq.blocks - wk.blk), end - wk.pos);
+  s.k0 = wk.blk * kKeys;
+  s.row0 = wk.rt * kRows;
+  s.rows = min(kRows, wk.rq.n * G - s.row0);
+  const auto tiles = [&](int lim) { return max(0, min(s.nb, (lim - s.k0 + kKeys - 1) / kKeys)); };
+  s.n = tiles(wk.t_end);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const bool has = s.rows > 128 * q;
+    s.na[q] = has ? tiles(kv4_key_limit(p, wk.rq, s.row0 + min(s.rows, 128 * (q + 1)) - 1)) : 0;
+    s.lim_lo[q] = has ? kv4_key_limit(p, wk.rq, s.row0 + 128 * q) : 0;
+  }
+  return s;
+}
+
+// Barrier of the eight softmax warps / of the four expanding warps.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void expand_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// One lane's share of a 16-token cache tile: K or V codes and scales.
+template <int D>
+struct Words {
+  uint4 w[D / 64];
+  uint32_t s;
+};
+template <int D>
+__device__ __forceinline__ void load_words(Words<D>& t, const uint8_t* tile, bool v, int lane) {
+  using L = Kv4Layout<D>;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    t.w[i] = __ldg(reinterpret_cast<const uint4*>(tile + (v ? L::kVCodes : L::kKCodes) + 512 * i + 16 * lane));
+  if (D == 64)
+    t.s = v ? __ldg(reinterpret_cast<const uint32_t*>(tile + L::kVScales) + (lane >> 3) * 4 + (lane & 3))
+            : __ldg(reinterpret_cast<const uint16_t*>(tile + L::kKScales) + lane);
+  else
+    t.s = __ldg(reinterpret_cast<const uint32_t*>(tile + (v ? L::kVScales : L::kKScales)) + lane);
+}
+
+// Eight codes times a scale -> 16 bytes of fp16 at row `row`, 16-byte chunk
+// `chunk` (of 8 within 64 dims) of a 128-byte-swizzled tile.
+__device__ __forceinline__ void expand8(uint32_t base, int row, int chunk, uint32_t codes, uint32_t scale2) {
+  uint32_t h[4];
+  kv4_code_pairs(codes, h);
+  st_shared_v4(base + row * 128 + ((chunk ^ (row & 7)) << 4), hmul2(h[0], scale2), hmul2(h[1], scale2),
+               hmul2(h[2], scale2), hmul2(h[3], scale2));
+}
+
+// K words of one cache tile -> rows [16 sub, 16 sub + 16) of the K tile at
+// `base`.  Lane 4 r + c holds tokens r and r + 8 and dims [c D/4, (c+1) D/4).
+// At head_dim 128 lanes c and c + 2 write the same chunks of two halves of the
+// row: the upper two take theirs in another order, so that the eight lanes of a
+// shared-memory pass touch eight different chunks.
+template <int D>
+__device__ __forceinline__ void expand_k(uint32_t base, int sub, const Words<D>& t, int lane) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = 16 * sub + r + 8 * h;
+    if (D == 64) {
+      const uint32_t s = scale_both(t.s, h);
+      expand8(base, row, 2 * c, h ? t.w[0].z : t.w[0].x, s);
+      expand8(base, row, 2 * c + 1, h ? t.w[0].w : t.w[0].y, s);
+    } else {
+      const uint4 w = t.w[h % (D / 64)];
+      const bool sw = c >= 2;
+      const uint32_t x = sw ? w.z : w.x, y = sw ? w.w : w.y, z = sw ? w.x : w.z, u = sw ? w.y : w.w;
+      const uint32_t sc = t.s >> (16 * h);
+      const uint32_t s0 = scale_both(sc, 0), s1 = scale_both(sc, 1);
+      const uint32_t sa = sw ? s1 : s0, sb = sw ? s0 : s1;
+      const uint32_t half = base + (c >> 1) * 16384;
+      const int ch = 4 * (c & 1), o = sw ? 2 : 0;
+      expand8(half, row, ch + o, x, sa);
+      expand8(half, row, ch + o + 1, y, sa);
+      expand8(half, row, ch + (o ^ 2), z, sb);
+      expand8(half, row, ch + (o ^ 2) + 1, u, sb);
+    }
+  }
+}
+// V words.  Lane 4 r + c holds dims [r D/8, (r+1) D/8) of tokens 2c, 2c + 1,
+// 2c + 8, 2c + 9; at head_dim 128 odd r take their two chunks in turned order.
+template <int D>
+__device__ __forceinline__ void expand_v(uint32_t base, int sub, const Words<D>& t, int lane) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int h = i >> 1, e = i & 1, row = 16 * sub + 2 * c + e + 8 * h;
+    const uint32_t s = scale_both(t.s >> (8 * i), 0);
+    if (D == 64) {
+      expand8(base, row, r, i == 0 ? t.w[0].x : i == 1 ? t.w[0].y : i == 2 ? t.w[0].z : t.w[0].w, s);
+    } else {
+      const uint4 w = t.w[h % (D / 64)];
+      const uint32_t a = e ? w.z : w.x, b = e ? w.w : w.y;
+      const bool sw = r & 1;
+      const uint32_t half = base + (r >> 2) * 16384;
+      expand8(half, row, 2 * (r & 3) + (sw ? 1 : 0), sw ? b : a, s);
+      expand8(half, row, 2 * (r & 3) + (sw ? 0 : 1), sw ? a : b, s);
+    }
+  }
+}
+
+// Columns [32 c, 32 c + 32) of a finished row.
+__device__ __forceinline__ void write_cols(const Kv4AttnParams& p, size_t off, const float (&v)[32]) {
+  if (p.o_is_fp32) {
+    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + off);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + off);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                          pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnParams p) {
+  using C = TileCfg<D>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = smem_u32(smem), sKV = sQ + C::kQBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  const uint32_t b_q = smem_u32(bars);              // [2] Q tile written (4 warps)
+  const uint32_t b_full = smem_u32(bars + 2);       // [S] (4 warps)
+  const uint32_t b_empty = smem_u32(bars + 2 + S);  // [S] (2 issuers)
+  const uint32_t b_s = smem_u32(bars + 2 + 2 * S);  // [2] S ready / O final
+  const uint32_t b_p = smem_u32(bars + 4 + 2 * S);  // [2] P written (4 warps)
+  const uint32_t b_drain = smem_u32(bars + 6 + 2 * S);  // [2]
+  // notes of the expanding warps: the first key of a segment with a NaN in a
+  // group of V; the cache tiles of a key tile whose page is not one of the cache
+  int* s_nan = reinterpret_cast<int*>(bars + 8 + 2 * S);            // [kSegs][8]
+  uint8_t* s_dead = reinterpret_cast<uint8_t*>(s_nan + kSegs * 8);  // [kSegs][8]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_dead + kSegs * 8);
+  int* s_int = reinterpret_cast<int*>(tmem_slot + 1);  // abort, bad, last
+  __shared__ long long s_sum[kThreads / 32], s_found[2];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.Hq / p.cache.Hkv;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_q + 8 * i, 4);
+      mbar_init(b_s + 8 * i, 1);
+      mbar_init(b_p + 8 * i, 4);
+      mbar_init(b_drain + 8 * i, 1);
+    }
+    for (int i = 0; i < S; ++i) {
+      mbar_init(b_full + 8 * i, 4);
+      mbar_init(b_empty + 8 * i, 2);
+    }
+    s_int[0] = s_int[1] = s_int[2] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  int bad = 0;
+  Kv4Walk wk;
+  const Kv4Line line = kv4_find_part<kRows, kKeys, true, kThreads>(p, s_sum, s_found, wk, bad);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Abort ab{s_int, s_int + 1};
+  if (bad) atomicMax(s_int + 1, bad);
+
+  // Register split: 512 threads x 128 at launch = 128 x 40 + 256 x 192 + 128 x 88.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp < 2 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuers
+      const int qt = warp;
+      const uint32_t tS = tmem + qt * 128, tO = tmem + 256 + qt * D;
+      const uint64_t d0 = sdesc_sw128(sQ, 0, 1024);
+      int stage = 0;
+      uint32_t kph = 0, pph = 0, qph = 0;
+      bool ok = true;
+      auto advance = [&]() { if (++stage == S) { stage = 0; kph ^= 1; } };
+      auto qk = [&](int kst) {
+        const uint64_t b = opaque(d0);
+        const uint64_t dq = sdesc_at(b, (uint32_t)qt * C::kTile, 0);
+        const uint64_t dk = sdesc_at(b, (uint32_t)(C::kQBytes + kst * C::kTile), 0);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_ss(tS, sdesc_at(dq, off, 16), sdesc_at(dk, off, 16), C::kIdescQK, kk > 0);
+        }
+      };
+      for (; wk.pos < line.end && ok;) {
+        wk.enter<kRows, kKeys, true>(p);
+        const Segment sg = segment(p, wk, line.end);
+        wk.pos += sg.nb;
+        const int na = qt == 0 ? sg.na[0] : sg.na[1];
+        if (sg.n == 0) continue;
+        if (na > 0) {
+          if (!(ok = mbar_wait(b_q + 8 * qt, qph, ab, 130))) break;
+          qph ^= 1;
+        }
+        if (!(ok = mbar_wait(b_full + 8 * stage, kph, ab, 131))) break;
+        tc_fence_after();
+        if (na > 0) { qk(stage); umma_commit(b_s + 8 * qt); }
+        umma_commit(b_empty + 8 * stage);
+        advance();
+        for (int j = 0; j < sg.n; ++j) {
+          const int vst = stage;
+          if (!(ok = mbar_wait(b_full + 8 * vst, kph, ab, 132))) break;
+          tc_fence_after();
+          advance();  // stage now holds K of the next tile
+          if (j < na) {
+            if (!(ok = mbar_wait(b_p + 8 * qt, pph, ab, 133))) break;
+            pph ^= 1;
+            tc_fence_after();
+            const uint64_t dv = sdesc_at(opaque(d0), (uint32_t)(C::kQBytes + vst * C::kTile), 0);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts(tO, tS + kk * 8, sdesc_at(dv, kk * 2048, 16384), C::kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
+            if (j + 1 == na) umma_commit(b_s + 8 * qt);  // O final
+          }
+          umma_commit(b_empty + 8 * vst);
+          if (j + 1 < sg.n) {
+            if (!(ok = mbar_wait(b_full + 8 * stage, kph, ab, 134))) break;
+            tc_fence_after();
+            if (j + 1 < na) { qk(stage); umma_commit(b_s + 8 * qt); }
+            umma_commit(b_empty + 8 * stage);
+            advance();
+          }
+        }
+      }
+      if (!ok) {  // let issued MMAs finish before tensor memory is released
+        umma_commit(b_drain + 8 * qt);
+        mbar_wait_drain(b_drain + 8 * qt, 0);
+      }
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // ------------------------------------------------------------ softmax
+    const int qt = (warp - 4) >> 2, row_t = tid - 128 * (1 + qt);  // row within the Q tile
+    const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
+    const uint32_t tS = tmem_addr(tmem, lane_base, qt * 128), tO = tmem_addr(tmem, lane_base, 256 + qt * D);
+    uint32_t sph = 0;
+    int seg = 0, tiles = 0;  // segments with key tiles, and key tiles, so far
+    bool ok = true;
+    for (; wk.pos < line.end;) {
+      wk.enter<kRows, kKeys, true>(p);
+      const Segment sg = segment(p, wk, line.end);
+      const int na = qt == 0 ? sg.na[0] : sg.na[1];
+      const int urow = 128 * qt + row_t, row = sg.row0 + urow;  // row of the unit, of the request
+      const bool valid = urow < sg.rows;
+      const int lim_lo = qt == 0 ? sg.lim_lo[0] : sg.lim_lo[1];
+      const int lim = valid ? kv4_key_limit(p, wk.rq, row) : 0x7fffffff;
+      const int token = wk.rq.b + row / G, h = wk.head * G + row % G;
+      float sl2 = 0.f;
+      if (na > 0) {
+        // this thread's query row, as fp16 after a power of two, into the Q tile
+        // (free: the tile's products of the segment before are done)
+        uint4 w[D / 8];
+        if (valid) {
+          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                            (size_t)token * p.q_stride + (size_t)h * D);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) w[i] = src[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          mx = __vmaxu2(mx, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+          mx = __vmaxu2(mx, __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+        }
+        float up;
+        sl2 = p.scale * kLog2e * kv4_row_scale(max(mx & 0xffffu, mx >> 16), up);
+        auto cvt = [&](uint32_t x) { return pack_f16x2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          st_shared_v4(sQ + qt * C::kTile + (i >> 3) * 16384 + row_t * 128 + (((i & 7) ^ (row_t & 7)) << 4), cvt(w[i].x),
+                       cvt(w[i].y), cvt(w[i].z), cvt(w[i].w));
+        fence_proxy_async_smem();
+        tc_fence_before();  // this segment's first P.V overwrites the O read before
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_q + 8 * qt);
+      }
+      const uint64_t sl2x2 = f2_pack(sl2, sl2);
+      float m_ref = neg_inf(), l_sum = 0.f;
+      for (int j = 0; j < na; ++j) {
+        if (ok) ok = mbar_wait(b_s + 8 * qt, sph, ab, 140);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        sph ^= 1;
+        tc_fence_after();
+        uint32_t r[4][32];
+        tmem_ld32(tS + 0, r[0]);
+        tmem_ld32(tS + 32, r[1]);
+        tmem_ld32(tS + 64, r[2]);
+        tmem_ld32(tS + 96, r[3]);
+        const uint2 dead = *reinterpret_cast<const uint2*>(s_dead + ((tiles + j) & (kSegs - 1)) * 8);
+        tmem_ld_wait();
+        reg_fence32(r[0]); reg_fence32(r[1]); reg_fence32(r[2]); reg_fence32(r[3]);
+        const int kst = sg.k0 + kKeys * j;
+        if (kst + kKeys > lim_lo || (dead.x | dead.y)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            const uint32_t d = (c >> 4) < 4 ? dead.x >> (8 * (c >> 4)) : dead.y >> (8 * ((c >> 4) & 3));
+            if (kst + c >= lim || (d & 0xffu)) r[c >> 5][c & 31] = __float_as_uint(neg_inf());
+          }
+        }
+        uint64_t nm2 = 0, ls_a = 0, ls_b = 0;
+        auto p_tile = [&](float m_use) {
+          nm2 = f2_pack(-m_use, -m_use);
+          ls_a = ls_b = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x =
+                  f2_fma(f2_pack(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), sl2x2, nm2);
+              float x0, x1;
+              f2_unpack(x, x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              pk[i] = pack_f16x2(p0, p1);
+              if (i & 1) ls_b = f2_add(ls_b, f2_pack(p0, p1));
+              else ls_a = f2_add(ls_a, f2_pack(p0, p1));
+            }
+            tmem_st16(tS + 16 * c, pk);
+          }
+        };
+        auto tile_sum = [&]() {
+          float a0, a1, b0, b1;
+          f2_unpack(ls_a, a0, a1);
+          f2_unpack(ls_b, b0, b1);
+          return (a0 + a1) + (b0 + b1);
+        };
+        // As in the ring forward: try the reference as it stands; where a tile's P
+        // would grow too large (or a row has seen no key), take the maximum, move
+        // the reference and redo the tile.
+        bool exact = __any_sync(0xffffffffu, m_ref == neg_inf());
+        bool rescale = false;
+        float alpha = 1.f;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          if (exact) {
+            float mx[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx[k] = neg_inf();
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mx[k] = fmax3(mx[k], __uint_as_float(r[k >> 1][16 * (k & 1) + i]),
+                              __uint_as_float(r[k >> 1][16 * (k & 1) + i + 1]));
+            const float m_tile = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7]))) * sl2;
+            rescale = m_tile > m_ref + kMaxExp;
+            if (rescale) {
+              const float m_new = ceilf(m_tile) - kHeadroom;
+              alpha = ex2_approx(m_ref - m_new);
+              l_sum *= alpha;
+              m_ref = m_new;
+            }
+          }
+          p_tile(m_ref == neg_inf() ? 0.f : m_ref);
+          if (exact || !__any_sync(0xffffffffu, !(tile_sum() <= kSumLimit))) break;
+          tmem_st_wait();  // the redo overwrites these P stores
+          exact = true;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_ld_wait();
+            reg_fence32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tO + 32 * c, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p + 8 * qt);
+        l_sum += tile_sum();
+      }
+      if (na > 0 && ok) {
+        ok = mbar_wait(b_s + 8 * qt, sph, ab, 141);  // O final
+        ok = __all_sync(0xffffffffu, ok);
+        sph ^= 1;
+        tc_fence_after();
+      }
+
+      // ---- output, or a partial result
+      const bool direct = wk.blk == 0 && sg.nb == wk.rq.blocks;
+      const long long first = wk.pos - wk.blk, last = first + wk.rq.blocks - 1;
+      const int c0 = direct ? 0 : line.owner(first);
+      auto slot = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * C::kSlot; };
+      const float inv = !direct ? 1.f : l_sum == 0.f ? 0.f : 1.f / l_sum;
+      const int* nan_key = s_nan + (seg & (kSegs - 1)) * 8;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        __syncwarp();
+        if (na > 0 && ok) {
+          tmem_ld32(tO + 32 * c, o);
+          tmem_ld_wait();
+          reg_fence32(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * inv;
+        if (na > 0) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            if (nan_key[2 * c + g] < lim) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[16 * g + i] = quiet_nan();
+            }
+        }
+        if (!valid) continue;
+        if (direct) {
+          write_cols(p, ((size_t)token * p.Hq + h) * D + 32 * c, v);
+        } else if (m_ref != neg_inf()) {
+          float4* dst = reinterpret_cast<float4*>(slot(blockIdx.x) + 2 * kRows + urow * D + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      if (direct) {
+        if (valid) p.lse[(size_t)h * p.Tq + token] = l_sum == 0.f ? neg_inf() : (m_ref + log2f(l_sum)) * kLn2;
+      } else {
+        if (valid) {
+          slot(blockIdx.x)[urow] = m_ref;
+          slot(blockIdx.x)[kRows + urow] = l_sum;
+        }
+        __threadfence();
+        softmax_sync();
+        const int parts = line.owner(last) - c0 + 1;
+        if (tid == 128) s_int[2] = atomicAdd(&p.tickets[c0], 1) == parts - 1;
+        softmax_sync();
+        if (s_int[2]) {
+          __threadfence();
+          // a warp a row: weights from the parts' references, then the sum
+          for (int rr = warp - 4; rr < sg.rows; rr += 8) {
+            float mm = neg_inf();
+            for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, __ldcg(slot(c0 + i) + rr));
+#pragma unroll
+            for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+            constexpr int V = D / 32;
+            float acc[V] = {}, l = 0.f;
+            for (int i = 0; i < parts; ++i) {
+              const float* s = slot(c0 + i);
+              const float m = __ldcg(s + rr);
+              if (m == neg_inf()) continue;
+              const float wgt = ex2_approx(m - mm);
+              l = fmaf(__ldcg(s + kRows + rr), wgt, l);
+#pragma unroll
+              for (int v = 0; v < V; ++v) acc[v] = fmaf(__ldcg(s + 2 * kRows + rr * D + 32 * v + lane), wgt, acc[v]);
+            }
+            const int grow = sg.row0 + rr, tk = wk.rq.b + grow / G, hh = wk.head * G + grow % G;
+            const float li = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              const size_t off = ((size_t)tk * p.Hq + hh) * D + 32 * v + lane;
+              if (p.o_is_fp32) reinterpret_cast<float*>(p.o)[off] = acc[v] * li;
+              else reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(acc[v] * li);
+            }
+            if (lane == 0) p.lse[(size_t)hh * p.Tq + tk] = l == 0.f ? neg_inf() : (mm + log2f(l)) * kLn2;
+          }
+          if (tid == 128) p.tickets[c0] = 0;  // as the next call expects it
+        }
+      }
+      wk.pos += sg.nb;
+      tiles += sg.n;
+      seg += sg.n > 0;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // ------------------------------------------------------------ expansion
+    using L = Kv4Layout<D>;
+    const int dw = warp - 12;  // cache tiles 2 dw and 2 dw + 1 of every key tile
+    int issued = 0, seg = 0, tiles = 0;
+    bool ok = true;
+    for (; wk.pos < line.end;) {
+      wk.enter<kRows, kKeys, true>(p);
+      const Segment sg = segment(p, wk, line.end);
+      wk.pos += sg.nb;
+      if (sg.n == 0) continue;
+      int* nan_key = s_nan + (seg & (kSegs - 1)) * 8;
+      if (dw == 0 && lane < 8) nan_key[lane] = 0x7fffffff;
+      expand_sync();
+      const int32_t* table = p.block_table + (size_t)wk.r * p.table_stride;
+      const uint8_t* base = p.cache.pages + ((size_t)wk.head << (p.cache.page_shift - 4)) * L::kBytes;
+      const int tiles_mask = (1 << (p.cache.page_shift - 4)) - 1;
+      // lanes 0 and 1: page ids of this warp's two cache tiles of key tile j
+      auto lane_page = [&](int j) -> int {
+        const int t = sg.k0 + kKeys * j + 16 * (2 * dw + lane);
+        return lane < 2 && j < sg.n && t < wk.t_end ? table[t >> p.cache.page_shift] : 0;
+      };
+      Words<D> k[2], v[2];
+      auto fetch = [&](int page, int j) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int t = sg.k0 + kKeys * j + 16 * (2 * dw + u);
+          const int pg = __shfl_sync(0xffffffffu, page, u);
+          const bool in = j < sg.n && t < wk.t_end, good = (uint32_t)pg < (uint64_t)p.cache.num_pages;
+          if (in && !good) bad = RA_KV4_BAD_PAGE;
+          k[u].s = v[u].s = 0;
+          if (in && good) {
+            const uint8_t* at = base + (int64_t)pg * p.page_bytes + ((t >> 4) & tiles_mask) * L::kBytes;
+            load_words<D>(k[u], at, false, lane);
+            load_words<D>(v[u], at, true, lane);
+          }
+        }
+      };
+      auto dead_of = [&](int page, int j, int u) {
+        const int t = sg.k0 + kKeys * j + 16 * (2 * dw + u);
+        const int pg = __shfl_sync(0xffffffffu, page, u);
+        return t < wk.t_end && (uint32_t)pg >= (uint64_t)p.cache.num_pages;
+      };
+      int page = lane_page(0), page_next = lane_page(1);
+      fetch(page, 0);
+      for (int j = 0; j < sg.n; ++j) {
+        Words<D> kc[2] = {k[0], k[1]}, vc[2] = {v[0], v[1]};
+        const bool dead0 = dead_of(page, j, 0), dead1 = dead_of(page, j, 1);
+        page = page_next;
+        fetch(page, j + 1);
+        page_next = lane_page(j + 2);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          // V: keys that no row sees, and NaN groups, count as zero; a row that
+          // sees a key with a NaN gets it from the notes
+          const int r = lane >> 2, c = lane & 3, g = D == 64 ? r >> 1 : r;
+          const int t0 = sg.k0 + kKeys * j + 16 * (2 * dw + u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 2 * c + (i & 1) + 8 * (i >> 1);
+            if (((vc[u].s >> (8 * i)) & 0xffu) >= 0xf8u || t >= wk.t_end) {
+              if (t < wk.t_end) atomicMin(&nan_key[g], t);
+              vc[u].s &= ~(0xffu << (8 * i));
+            }
+          }
+        }
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          const int st = issued % S;
+          if (ok) ok = mbar_wait(b_empty + 8 * st, ((issued / S) & 1) ^ 1, ab, 150);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            const uint32_t dst = sKV + st * C::kTile;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (kind == 0) expand_k<D>(dst, 2 * dw + u, kc[u], lane);
+              else expand_v<D>(dst, 2 * dw + u, vc[u], lane);
+            }
+            if (kind == 0 && lane < 2) s_dead[((tiles + j) & (kSegs - 1)) * 8 + 2 * dw + lane] = lane ? dead1 : dead0;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_full + 8 * st);
+          }
+          ++issued;
+        }
+      }
+      tiles += sg.n;
+      ++seg;
+    }
+    if (bad) atomicMax(s_int + 1, bad);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0) kv4_end(p, s_int[1]);
+}
+
+template <int D>
+cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
+  auto kern = kv4_tile_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kThreads, TileCfg<D>::kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_tile(int D, int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
+  if (D == 64) return launch<64>(ctas, p, stream);
+  if (D == 128) return launch<128>(ctas, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace ra

@@ -1,0 +1,205 @@
+// kv4_walk.cuh -- device helpers shared by the two cache attention kernels: the
+// fp16 arithmetic of expanded codes, and the line of work (requests' units of
+// key blocks, one after the other) that a grid's CTAs cut into equal parts.
+#pragma once
+
+#include "kv4.h"
+#include "tc.cuh"
+
+namespace ra {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Scale byte `i` of a word as fp16 in both halves; bytes i and j in low and high half.
+__device__ __forceinline__ uint32_t scale_both(uint32_t w, int i) {
+  return __byte_perm(w, 0, 0x0404 | (i << 4) | (i << 12)) >> 1;
+}
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, int i, int j) {
+  return __byte_perm(w, 0, 0x0404 | (i << 4) | (j << 12)) >> 1;
+}
+
+// The power of two that brings a row whose largest magnitude has the bf16 bits
+// `mx` to about 1 (`up`, applied to the row) and its inverse (returned, for the
+// softmax scale); 1 for a row of zeros or with an infinity or NaN.
+__device__ __forceinline__ float kv4_row_scale(uint32_t mx, float& up) {
+  const int ex = mx == 0 || mx >= 0x7f80 ? 0 : min(max((int)(mx >> 7) - 127, -126), 126);
+  up = __uint_as_float((uint32_t)(127 - ex) << 23);
+  return __uint_as_float((uint32_t)(127 + ex) << 23);
+}
+
+// What a CTA knows of a request.
+struct Kv4Request {
+  int b, n, L;     // first query row, query tokens, keys
+  int row_tiles;
+  int blocks;      // blocks of keys of each of its units (at least one: empty rows are written too)
+  int bad;
+};
+
+// `kTiles`: the kernel of large row tiles, which takes the requests with at
+// least split_rows rows; the other one takes those with fewer (split_rows = 0:
+// all).  The requests of the other kernel have no row tiles here.
+template <int RT, int KB, bool kTiles>
+__device__ __forceinline__ Kv4Request kv4_request(const Kv4AttnParams& p, int r) {
+  Kv4Request q;
+  int b = p.cu_q[r], e = p.cu_q[r + 1];
+  int L = p.kv_lens[r];
+  q.bad = 0;
+  if (b < 0 || e < b || e > p.Tq) {
+    q.bad = RA_KV4_BAD_OFFSET;
+    b = min(max(b, 0), p.Tq);
+    e = min(max(e, b), p.Tq);
+  }
+  const long long cap = (long long)p.table_width << p.cache.page_shift;
+  if (L < 0 || L > cap) {
+    q.bad = RA_KV4_BAD_LENGTH;
+    L = L < 0 ? 0 : (int)cap;
+  }
+  q.b = b;
+  q.n = e - b;
+  q.L = L;
+  const int G = p.Hq / p.cache.Hkv;
+  const long long rows = (long long)q.n * G;
+  const bool other = p.split_rows > 0 && (kTiles ? rows < p.split_rows : rows >= p.split_rows);
+  q.row_tiles = other ? 0 : (int)((rows + RT - 1) / RT);
+  q.blocks = max(1, (int)(((long long)L + KB - 1) / KB));
+  return q;
+}
+__device__ __forceinline__ long long kv4_request_work(const Kv4Request& q, int Hkv) {
+  return (long long)q.row_tiles * Hkv * q.blocks;
+}
+
+__device__ __forceinline__ int kv4_key_limit(const Kv4AttnParams& p, const Kv4Request& q, int row) {
+  return p.causal ? max(0, min(q.L, q.L - q.n + row / (p.Hq / p.cache.Hkv) + 1)) : q.L;
+}
+
+// A place on the line of work: block `blk` of unit (r, rt, head).
+struct Kv4Walk {
+  long long pos;   // blocks before this place
+  long long base;  // blocks before request r
+  int r;
+  int rt = 0, head = 0, blk = 0, t_end = 0;  // t_end: keys that some row of the unit sees
+  Kv4Request rq;
+  // find the unit that holds pos (pos is inside the line)
+  template <int RT, int KB, bool kTiles>
+  __device__ __forceinline__ void enter(const Kv4AttnParams& p) {
+    long long work;
+    for (;; ++r) {  // (requests without rows have no work)
+      rq = kv4_request<RT, KB, kTiles>(p, r);
+      work = kv4_request_work(rq, p.cache.Hkv);
+      if (pos < base + work || r + 1 >= p.R) break;
+      base += work;
+    }
+    const long long unit = (pos - base) / rq.blocks;
+    blk = (int)(pos - base - unit * rq.blocks);
+    rt = (int)(unit / p.cache.Hkv);
+    head = (int)(unit - (long long)rt * p.cache.Hkv);
+    t_end = kv4_key_limit(p, rq, min((rt + 1) * RT, rq.n * (p.Hq / p.cache.Hkv)) - 1);
+  }
+};
+
+// The line's length and this CTA's part [begin, end) of it.
+struct Kv4Line {
+  long long total, cut, begin, end;
+  __device__ __forceinline__ int owner(long long x) const {  // the CTA whose part holds block x
+    int c = (int)(x * cut / total);
+    while (total * (c + 1) / cut <= x) ++c;
+    while (total * c / cut > x) --c;
+    return c;
+  }
+};
+
+// Cut the line for this grid; `wk` receives the place where this CTA's part
+// begins (when it has one).  All threads of the CTA; s_sum has one entry a warp.
+template <int RT, int KB, bool kTiles, int kThreads>
+__device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long long* s_sum, long long* s_found,
+                                                 Kv4Walk& wk, int& bad) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) s_found[0] = -1;
+  long long mine = 0, total = 0;  // work of request `tid`; of all
+  for (int i = tid; i < p.R; i += kThreads) {
+    const Kv4Request q = kv4_request<RT, KB, kTiles>(p, i);
+    const long long w = kv4_request_work(q, p.cache.Hkv);
+    if (i == tid) mine = w;
+    total += w;
+    bad = max(bad, q.bad);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  if (lane == 0) s_sum[warp] = total;
+  __syncthreads();
+  Kv4Line line;
+  line.total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) line.total += s_sum[w];
+  // no part is empty: a unit's partial results then lie in consecutive CTAs
+  line.cut = min((long long)gridDim.x, line.total);
+  const bool idle = blockIdx.x >= line.cut;
+  line.begin = idle ? 0 : line.total * blockIdx.x / line.cut;
+  line.end = idle ? 0 : line.total * (blockIdx.x + 1) / line.cut;
+  wk.pos = line.begin;
+  wk.base = 0;
+  wk.r = 0;
+  if (idle) return line;
+  for (int r0 = 0; r0 < p.R; r0 += kThreads) {
+    const long long w = r0 == 0           ? mine
+                        : r0 + tid < p.R ? kv4_request_work(kv4_request<RT, KB, kTiles>(p, r0 + tid), p.cache.Hkv)
+                                         : 0;
+    long long x = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    long long before = wk.base, chunk = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += s_sum[i];
+      chunk += s_sum[i];
+    }
+    if (line.begin >= before + x - w && line.begin < before + x) {
+      s_found[0] = r0 + tid;
+      s_found[1] = before + x - w;
+    }
+    __syncthreads();
+    if (s_found[0] >= 0) {
+      wk.r = (int)s_found[0];
+      wk.base = s_found[1];
+      break;
+    }
+    wk.base += chunk;
+  }
+  return line;
+}
+
+// One thread of a CTA at its end: the grid's last CTA turns what was found into
+// the call's status and leaves the counters as the next call expects them.
+__device__ __forceinline__ void kv4_end(const Kv4AttnParams& p, int bad) {
+  if (bad) atomicMax(p.found, bad);
+  __threadfence();
+  if (atomicAdd(p.ended, 1) == (int)gridDim.x - 1) {
+    __threadfence();
+    const int found = atomicExch(p.found, 0);
+    *p.status = p.status_kept ? max(*p.status, found) : found;
+    *p.ended = 0;
+  }
+}
+
+}  // namespace ra

@@ -290,6 +290,43 @@ def test_prompt_part(ra):
     c.check(ra, causal=False, o_fp32=False, max_q_len=300)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 4, 2), (128, 8, 1), (128, 3, 3), (256, 4, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_parts_among_single_tokens(ra, d, Hq, Hkv, causal):
+    """Both kernels in one call: parts of prompts (one without a prefix), single tokens, and requests without rows."""
+    lens = [700, 1, 0, 131, 129, 513, 260, 90]
+    qlens = [1, 1, 0, 131, 65, 0, 200, 1]
+    c = Case(ra, 17 + d, lens, qlens, Hq, Hkv, d, 64)
+    c.check(ra, causal=causal, max_q_len=200)
+    c.check(ra, causal=causal, max_q_len=200, o_fp32=False, scale=0.2)
+
+
+@pytest.mark.parametrize("d,G,n,L", [(64, 2, 33, 3001), (128, 4, 16, 5000), (128, 1, 64, 2100), (128, 8, 129, 1111)])
+def test_one_prompt_part_is_split(ra, d, G, n, L):
+    c = Case(ra, n + L, [L], [n], G, 1, d, 32)
+    c.check(ra, max_q_len=n)
+    first = ra.kv4_attention(c.q.cuda(), c.cache, c.table, c.lens_t, c.cu_t, max_q_len=n)
+    again = ra.kv4_attention(c.q.cuda(), c.cache, c.table, c.lens_t, c.cu_t, max_q_len=n)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_more_rows_than_keys(ra):
+    c = Case(ra, 19, [30, 0, 5], [100, 70, 80], 2, 1, 128, 16)
+    o, lse = c.check(ra, max_q_len=100)
+    assert o[:70].eq(0).all() and torch.isneginf(lse[:, :70]).all()
+
+
+def test_uneven_scores_in_row_tiles(ra):
+    rng = np.random.default_rng(13)
+    L, d, n = 900, 128, 70
+    ramp = np.concatenate([np.linspace(0.01, 30, 450), np.linspace(30, 0.01, 450)])
+    k = torch.tensor(rng.standard_normal((L, 1, d)) * ramp[:, None, None]).to(torch.bfloat16)
+    c = Case(ra, 13, [L], [n], 2, 1, d, 16, keys=[k])
+    c.q[5] = 0
+    c.q[6] *= 2.0 ** -100
+    c.check(ra, max_q_len=n)
+
+
 def test_uneven_scores_move_the_reference(ra):
     """Scores that grow along the keys by far more than the reference's headroom, and shrink again."""
     rng = np.random.default_rng(9)
@@ -338,17 +375,18 @@ def test_strided_q_and_rows_behind_the_last(ra):
     assert o[3:].eq(7).all() and lse[:, 3:].eq(5).all()
 
 
-def test_refused_contents_are_reported_and_stay_in_bounds(ra):
+@pytest.mark.parametrize("longest", [1, 64])                     # 64: single tokens beside the row-tile kernel
+def test_refused_contents_are_reported_and_stay_in_bounds(ra, longest):
     c = Case(ra, 31, [40, 90, 33], [1, 1, 1], 4, 2, 64, 16)
     q = c.q.cuda()
-    good = ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, max_q_len=1, check=True)[0]
+    good = ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, max_q_len=longest, check=True)[0]
 
     def refused(match, table=c.table, lens=c.lens_t, cu=c.cu_t):
-        ws = ra.kv4_attention_workspace(c.cache, 3, 4, 1)
-        o, _ = ra.kv4_attention(q, c.cache, table, lens, cu, max_q_len=1, workspace=ws)
+        ws = ra.kv4_attention_workspace(c.cache, 3, 4, longest)
+        o, _ = ra.kv4_attention(q, c.cache, table, lens, cu, max_q_len=longest, workspace=ws)
         with pytest.raises(ra.RingAttnError, match=match):
             ra.kv4_status(ws)
-        ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, max_q_len=1, workspace=ws, check=True)  # fresh status
+        ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, max_q_len=longest, workspace=ws, check=True)  # fresh status
         return o
     for bad in (-1, c.cache.num_pages, 2 ** 31 - 1, -2 ** 31):
         t = c.table.clone()
@@ -361,6 +399,21 @@ def test_refused_contents_are_reported_and_stay_in_bounds(ra):
         refused("length|page", lens=x)
     for cu in ([0, 1, 2, 4], [0, 2, 1, 3], [-1, 1, 2, 3], [0, 1, 2, 2 ** 31 - 1]):
         refused("offsets", cu=torch.tensor(cu, dtype=torch.int32).cuda())
+
+
+def test_bad_pages_in_row_tiles(ra):
+    """A key on a page outside the cache is left out of every row, the others stay."""
+    c = Case(ra, 33, [300, 200], [70, 80], 2, 1, 128, 16)
+    ws = ra.kv4_attention_workspace(c.cache, 150, 2, 80)
+    for bad in (-1, c.cache.num_pages, 2 ** 31 - 1, -2 ** 31):
+        t = c.table.clone()
+        t[0, 3] = bad
+        o, lse = ra.kv4_attention(c.q.cuda(), c.cache, t, c.lens_t, c.cu_t, o_fp32=True, max_q_len=80, workspace=ws)
+        with pytest.raises(ra.RingAttnError, match="page"):
+            ra.kv4_status(ws)
+        keys, values = [np.delete(x[0], np.s_[48:64], axis=0) for x in (c.keys, c.values)]
+        want, wl = O.attention(f64(c.q), [keys, c.keys[1]], [values, c.values[1]], [284, 200], c.cu, True, 1 / math.sqrt(128))
+        c.compare(f64(o), f64(lse), want, wl, 1 / math.sqrt(128), True)
 
 
 def test_empty_calls(ra):
