@@ -110,64 +110,79 @@ __device__ __forceinline__ void load_words(Words<D>& t, const uint8_t* tile, boo
     t.s = __ldg(reinterpret_cast<const uint32_t*>(tile + (v ? L::kVScales : L::kKScales)) + lane);
 }
 
-// Eight codes times a scale -> 16 bytes of fp16 at row `row`, 16-byte chunk
-// `chunk` (of 8 within 64 dims) of a 128-byte-swizzled tile.
-__device__ __forceinline__ void expand8(uint32_t base, int row, int chunk, uint32_t codes, uint32_t scale2) {
+// Eight codes times a scale -> 16 bytes of fp16.
+__device__ __forceinline__ void expand8(uint32_t addr, uint32_t codes, uint32_t scale2) {
   uint32_t h[4];
   kv4_code_pairs(codes, h);
-  st_shared_v4(base + row * 128 + ((chunk ^ (row & 7)) << 4), hmul2(h[0], scale2), hmul2(h[1], scale2),
-               hmul2(h[2], scale2), hmul2(h[3], scale2));
+  st_shared_v4(addr, hmul2(h[0], scale2), hmul2(h[1], scale2), hmul2(h[2], scale2), hmul2(h[3], scale2));
 }
 
-// K words of one cache tile -> rows [16 sub, 16 sub + 16) of the K tile at
-// `base`.  Lane 4 r + c holds tokens r and r + 8 and dims [c D/4, (c+1) D/4).
-// At head_dim 128 lanes c and c + 2 write the same chunks of two halves of the
-// row: the upper two take theirs in another order, so that the eight lanes of a
-// shared-memory pass touch eight different chunks.
+// Where a lane writes: byte offsets in a K or V tile of 128-byte-swizzled rows
+// (16-byte chunk x of row y at chunk x ^ (y & 7); 64 dims a row, the next 64
+// 16 KB on), for cache tile 0; tile `sub` lies 2048 sub bytes on, tokens 8 to 15
+// of it 1024.
+//   K: lane 4 r + c holds tokens r and r + 8 and dims [c D/4, (c+1) D/4);
+//   V: lane 4 r + c holds tokens 2c + e (+ 8) and dims [r D/8, (r+1) D/8).
+// The eight lanes of a shared-memory pass should touch eight different chunks.
+// At head_dim 128 they do not by themselves: lanes with c >= 2 write their K
+// chunks in another order (`turn`: 2 before 0), those with odd r their V chunks.
 template <int D>
-__device__ __forceinline__ void expand_k(uint32_t base, int sub, const Words<D>& t, int lane) {
-  const int r = lane >> 2, c = lane & 3;
+struct Places {
+  uint32_t k[D / 32], v[2][D / 64];
+  bool k_turn, v_turn;
+  __device__ __forceinline__ explicit Places(int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    k_turn = D == 128 && c >= 2;
+    v_turn = D == 128 && (r & 1);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int ch = D == 64 ? 2 * c + i : 4 * (c & 1) + (k_turn ? i ^ 2 : i);
+      k[i] = (D == 64 ? 0 : (c >> 1) * 16384) + r * 128 + ((ch ^ r) << 4);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int row = 2 * c + e, ch = D == 64 ? r : 2 * (r & 3) + (v_turn ? i ^ 1 : i);
+        v[e][i] = (D == 64 ? 0 : (r >> 2) * 16384) + row * 128 + ((ch ^ row) << 4);
+      }
+  }
+};
+
+// The words of one cache tile into its rows of the K / V tile; `base` is the
+// stage's address plus 2048 x the cache tile's number.
+template <int D>
+__device__ __forceinline__ void expand_k(uint32_t base, const Words<D>& t, const Places<D>& pl) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int row = 16 * sub + r + 8 * h;
     if (D == 64) {
       const uint32_t s = scale_both(t.s, h);
-      expand8(base, row, 2 * c, h ? t.w[0].z : t.w[0].x, s);
-      expand8(base, row, 2 * c + 1, h ? t.w[0].w : t.w[0].y, s);
+      expand8(base + pl.k[0] + 1024 * h, h ? t.w[0].z : t.w[0].x, s);
+      expand8(base + pl.k[1] + 1024 * h, h ? t.w[0].w : t.w[0].y, s);
     } else {
       const uint4 w = t.w[h % (D / 64)];
-      const bool sw = c >= 2;
-      const uint32_t x = sw ? w.z : w.x, y = sw ? w.w : w.y, z = sw ? w.x : w.z, u = sw ? w.y : w.w;
-      const uint32_t sc = t.s >> (16 * h);
-      const uint32_t s0 = scale_both(sc, 0), s1 = scale_both(sc, 1);
-      const uint32_t sa = sw ? s1 : s0, sb = sw ? s0 : s1;
-      const uint32_t half = base + (c >> 1) * 16384;
-      const int ch = 4 * (c & 1), o = sw ? 2 : 0;
-      expand8(half, row, ch + o, x, sa);
-      expand8(half, row, ch + o + 1, y, sa);
-      expand8(half, row, ch + (o ^ 2), z, sb);
-      expand8(half, row, ch + (o ^ 2) + 1, u, sb);
+      const uint32_t s0 = scale_both(t.s, 2 * h), s1 = scale_both(t.s, 2 * h + 1);
+      const bool sw = pl.k_turn;
+      expand8(base + pl.k[0] + 1024 * h, sw ? w.z : w.x, sw ? s1 : s0);
+      expand8(base + pl.k[1] + 1024 * h, sw ? w.w : w.y, sw ? s1 : s0);
+      expand8(base + pl.k[D == 128 ? 2 : 0] + 1024 * h, sw ? w.x : w.z, sw ? s0 : s1);
+      expand8(base + pl.k[D == 128 ? 3 : 0] + 1024 * h, sw ? w.y : w.w, sw ? s0 : s1);
     }
   }
 }
-// V words.  Lane 4 r + c holds dims [r D/8, (r+1) D/8) of tokens 2c, 2c + 1,
-// 2c + 8, 2c + 9; at head_dim 128 odd r take their two chunks in turned order.
 template <int D>
-__device__ __forceinline__ void expand_v(uint32_t base, int sub, const Words<D>& t, int lane) {
-  const int r = lane >> 2, c = lane & 3;
+__device__ __forceinline__ void expand_v(uint32_t base, const Words<D>& t, const Places<D>& pl) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int h = i >> 1, e = i & 1, row = 16 * sub + 2 * c + e + 8 * h;
-    const uint32_t s = scale_both(t.s >> (8 * i), 0);
+    const int h = i >> 1, e = i & 1;
+    const uint32_t s = scale_both(t.s, i);
     if (D == 64) {
-      expand8(base, row, r, i == 0 ? t.w[0].x : i == 1 ? t.w[0].y : i == 2 ? t.w[0].z : t.w[0].w, s);
+      expand8(base + pl.v[e][0] + 1024 * h, i == 0 ? t.w[0].x : i == 1 ? t.w[0].y : i == 2 ? t.w[0].z : t.w[0].w, s);
     } else {
       const uint4 w = t.w[h % (D / 64)];
       const uint32_t a = e ? w.z : w.x, b = e ? w.w : w.y;
-      const bool sw = r & 1;
-      const uint32_t half = base + (r >> 2) * 16384;
-      expand8(half, row, 2 * (r & 3) + (sw ? 1 : 0), sw ? b : a, s);
-      expand8(half, row, 2 * (r & 3) + (sw ? 0 : 1), sw ? a : b, s);
+      expand8(base + pl.v[e][0] + 1024 * h, pl.v_turn ? b : a, s);
+      expand8(base + pl.v[e][D == 128 ? 1 : 0] + 1024 * h, pl.v_turn ? a : b, s);
     }
   }
 }
@@ -314,11 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
     const uint32_t tS = tmem_addr(tmem, lane_base, qt * 128), tO = tmem_addr(tmem, lane_base, 256 + qt * D);
     uint32_t sph = 0;
     int seg = 0, tiles = 0;  // segments with key tiles, and key tiles, so far
+    uint32_t turns = 0;      // P tiles of the other Q tile in the segments before
     bool ok = true;
     for (; wk.pos < line.end;) {
       wk.enter<kRows, kKeys, true>(p);
       const Segment sg = segment(p, wk, line.end);
       const int na = qt == 0 ? sg.na[0] : sg.na[1];
+      const int na_other = qt == 0 ? sg.na[1] : sg.na[0];
       const int urow = 128 * qt + row_t, row = sg.row0 + urow;  // row of the unit, of the request
       const bool valid = urow < sg.rows;
       const int lim_lo = qt == 0 ? sg.lim_lo[0] : sg.lim_lo[1];
@@ -368,6 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         tmem_ld32(tS + 32, r[1]);
         tmem_ld32(tS + 64, r[2]);
         tmem_ld32(tS + 96, r[3]);
+        // The two Q tiles take turns (0's tile j after 1's tile j - 1, 1's after 0's
+        // tile j), so that one's softmax runs beside the other's products.
+        const int k_other = j - (qt == 0 ? 1 : 0);
+        if (k_other >= 0 && k_other < na_other) mbar_wait(b_p + 8 * (1 - qt), (turns + k_other) & 1u, ab, 142);
         const uint2 dead = *reinterpret_cast<const uint2*>(s_dead + ((tiles + j) & (kSegs - 1)) * 8);
         tmem_ld_wait();
         reg_fence32(r[0]); reg_fence32(r[1]); reg_fence32(r[2]); reg_fence32(r[3]);
@@ -516,45 +537,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         softmax_sync();
         if (s_int[2]) {
           __threadfence();
-          // a warp a row: weights from the parts' references, then the sum
-          for (int rr = warp - 4; rr < sg.rows; rr += 8) {
-            float mm = neg_inf();
-            for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, __ldcg(slot(c0 + i) + rr));
+          // a thread a row: the rows' largest references and their sums, kept in the
+          // Q tiles' shared memory (all products of the segment are done)
+          float* s_ref = reinterpret_cast<float*>(smem);
+          float* s_inv = s_ref + kRows;
+          float mm = neg_inf(), l = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < parts; ++i) mm = fmaxf(mm, __ldcg(slot(c0 + i) + urow));
+#pragma unroll 4
+          for (int i = 0; i < parts; ++i) {
+            const float m = __ldcg(slot(c0 + i) + urow), li = __ldcg(slot(c0 + i) + kRows + urow);
+            l += m == neg_inf() ? 0.f : li * ex2_approx(m - mm);
+          }
+          s_ref[urow] = mm;
+          s_inv[urow] = l == 0.f ? 0.f : 1.f / l;
+          if (valid) p.lse[(size_t)h * p.Tq + token] = l == 0.f ? neg_inf() : (mm + log2f(l)) * kLn2;
+          softmax_sync();
+          // a warp four rows at once: their weighted sums
+          constexpr int V = D / 32, B = 4;
+          for (int r0 = warp - 4; r0 < sg.rows; r0 += 8 * B) {
+            float acc[B][V] = {}, ref[B];
 #pragma unroll
-            for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-            constexpr int V = D / 32;
-            float acc[V] = {}, l = 0.f;
+            for (int b = 0; b < B; ++b) ref[b] = s_ref[min(r0 + 8 * b, kRows - 1)];
+#pragma unroll 2
             for (int i = 0; i < parts; ++i) {
               const float* s = slot(c0 + i);
-              const float m = __ldcg(s + rr);
-              if (m == neg_inf()) continue;
-              const float wgt = ex2_approx(m - mm);
-              l = fmaf(__ldcg(s + kRows + rr), wgt, l);
 #pragma unroll
-              for (int v = 0; v < V; ++v) acc[v] = fmaf(__ldcg(s + 2 * kRows + rr * D + 32 * v + lane), wgt, acc[v]);
-            }
-            const int grow = sg.row0 + rr, tk = wk.rq.b + grow / G, hh = wk.head * G + grow % G;
-            const float li = l == 0.f ? 0.f : 1.f / l;
+              for (int b = 0; b < B; ++b) {
+                const int rr = min(r0 + 8 * b, sg.rows - 1);
+                const float m = __ldcg(s + rr);
+                const float wgt = m == neg_inf() ? 0.f : ex2_approx(m - ref[b]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-              const size_t off = ((size_t)tk * p.Hq + hh) * D + 32 * v + lane;
-              if (p.o_is_fp32) reinterpret_cast<float*>(p.o)[off] = acc[v] * li;
-              else reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(acc[v] * li);
+                for (int v = 0; v < V; ++v) {
+                  const float x = __ldcg(s + 2 * kRows + rr * D + 32 * v + lane);
+                  acc[b][v] += m == neg_inf() ? 0.f : x * wgt;  // (a row without keys has no O there)
+                }
+              }
             }
-            if (lane == 0) p.lse[(size_t)hh * p.Tq + tk] = l == 0.f ? neg_inf() : (mm + log2f(l)) * kLn2;
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+              const int rr = r0 + 8 * b;
+              if (rr >= sg.rows) break;
+              const int grow = sg.row0 + rr, tk = wk.rq.b + grow / G, hh = wk.head * G + grow % G;
+#pragma unroll
+              for (int v = 0; v < V; ++v) {
+                const size_t off = ((size_t)tk * p.Hq + hh) * D + 32 * v + lane;
+                const float x = acc[b][v] * s_inv[rr];
+                if (p.o_is_fp32) reinterpret_cast<float*>(p.o)[off] = x;
+                else reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(x);
+              }
+            }
           }
+          softmax_sync();  // the Q tiles may be written again
           if (tid == 128) p.tickets[c0] = 0;  // as the next call expects it
         }
       }
       wk.pos += sg.nb;
       tiles += sg.n;
       seg += sg.n > 0;
+      turns += na_other;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ------------------------------------------------------------ expansion
     using L = Kv4Layout<D>;
     const int dw = warp - 12;  // cache tiles 2 dw and 2 dw + 1 of every key tile
+    const Places<D> places(lane);
     int issued = 0, seg = 0, tiles = 0;
     bool ok = true;
     for (; wk.pos < line.end;) {
@@ -573,68 +621,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         const int t = sg.k0 + kKeys * j + 16 * (2 * dw + lane);
         return lane < 2 && j < sg.n && t < wk.t_end ? table[t >> p.cache.page_shift] : 0;
       };
+      // The words of a key tile are loaded as soon as the registers of the one
+      // before are free: the way to memory is covered by a whole tile's products.
       Words<D> k[2], v[2];
-      auto fetch = [&](int page, int j) {
+      uint32_t dead = 0;  // bit u: cache tile u of key tile j lies on a page that is not one of the cache
+      auto fetch = [&](Words<D> (&w)[2], bool is_v, int page, int j) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int t = sg.k0 + kKeys * j + 16 * (2 * dw + u);
           const int pg = __shfl_sync(0xffffffffu, page, u);
           const bool in = j < sg.n && t < wk.t_end, good = (uint32_t)pg < (uint64_t)p.cache.num_pages;
-          if (in && !good) bad = RA_KV4_BAD_PAGE;
-          k[u].s = v[u].s = 0;
-          if (in && good) {
-            const uint8_t* at = base + (int64_t)pg * p.page_bytes + ((t >> 4) & tiles_mask) * L::kBytes;
-            load_words<D>(k[u], at, false, lane);
-            load_words<D>(v[u], at, true, lane);
-          }
+          if (!is_v) dead = (dead & ~(1u << u)) | (in && !good ? 1u << u : 0u);
+          w[u].s = 0;
+          if (in && good)
+            load_words<D>(w[u], base + (int64_t)pg * p.page_bytes + ((t >> 4) & tiles_mask) * L::kBytes, is_v, lane);
         }
-      };
-      auto dead_of = [&](int page, int j, int u) {
-        const int t = sg.k0 + kKeys * j + 16 * (2 * dw + u);
-        const int pg = __shfl_sync(0xffffffffu, page, u);
-        return t < wk.t_end && (uint32_t)pg >= (uint64_t)p.cache.num_pages;
       };
       int page = lane_page(0), page_next = lane_page(1);
-      fetch(page, 0);
+      fetch(k, false, page, 0);
+      fetch(v, true, page, 0);
       for (int j = 0; j < sg.n; ++j) {
-        Words<D> kc[2] = {k[0], k[1]}, vc[2] = {v[0], v[1]};
-        const bool dead0 = dead_of(page, j, 0), dead1 = dead_of(page, j, 1);
         page = page_next;
-        fetch(page, j + 1);
         page_next = lane_page(j + 2);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          // V: keys that no row sees, and NaN groups, count as zero; a row that
-          // sees a key with a NaN gets it from the notes
-          const int r = lane >> 2, c = lane & 3, g = D == 64 ? r >> 1 : r;
-          const int t0 = sg.k0 + kKeys * j + 16 * (2 * dw + u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 2 * c + (i & 1) + 8 * (i >> 1);
-            if (((vc[u].s >> (8 * i)) & 0xffu) >= 0xf8u || t >= wk.t_end) {
-              if (t < wk.t_end) atomicMin(&nan_key[g], t);
-              vc[u].s &= ~(0xffu << (8 * i));
-            }
-          }
-        }
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
           const int st = issued % S;
           if (ok) ok = mbar_wait(b_empty + 8 * st, ((issued / S) & 1) ^ 1, ab, 150);
           ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            const uint32_t dst = sKV + st * C::kTile;
+          ++issued;
+          if (!ok) continue;
+          const uint32_t dst = sKV + st * C::kTile + 4096 * dw;
+          if (kind == 0) {
+            if (dead) bad = RA_KV4_BAD_PAGE;
+            if (lane < 2) s_dead[((tiles + j) & (kSegs - 1)) * 8 + 2 * dw + lane] = (dead >> lane) & 1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) expand_k<D>(dst + 2048 * u, k[u], places);
+          } else {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              if (kind == 0) expand_k<D>(dst, 2 * dw + u, kc[u], lane);
-              else expand_v<D>(dst, 2 * dw + u, vc[u], lane);
+              // keys that no row sees, and NaN groups, count as zero; a row that
+              // sees a key with a NaN gets it from the notes
+              const int c = lane & 3, g = D == 64 ? lane >> 3 : lane >> 2;
+              const int t0 = sg.k0 + kKeys * j + 16 * (2 * dw + u);
+              if (__vcmpgeu4(v[u].s, 0xf8f8f8f8u) || t0 + 16 > wk.t_end) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int t = t0 + 2 * c + (i & 1) + 8 * (i >> 1);
+                  if (((v[u].s >> (8 * i)) & 0xffu) >= 0xf8u || t >= wk.t_end) {
+                    if (t < wk.t_end) atomicMin(&nan_key[g], t);
+                    v[u].s &= ~(0xffu << (8 * i));
+                  }
+                }
+              }
+              expand_v<D>(dst + 2048 * u, v[u], places);
             }
-            if (kind == 0 && lane < 2) s_dead[((tiles + j) & (kSegs - 1)) * 8 + 2 * dw + lane] = lane ? dead1 : dead0;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_full + 8 * st);
           }
-          ++issued;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_full + 8 * st);
+          fetch(kind == 0 ? k : v, kind == 1, page, j + 1);
         }
       }
       tiles += sg.n;
