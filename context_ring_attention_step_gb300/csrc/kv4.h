@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -78,6 +79,22 @@ __device__ __forceinline__ size_t kv4_tile_offset(const Kv4Cache& c, int64_t pag
   const size_t tiles = size_t(1) << (c.page_shift - 4);
   return (((size_t)page * c.Hkv + head) * tiles + (t >> 4)) * Kv4Layout<D>::kBytes;
 }
+
+// A kernel's dynamic shared memory limit, raised once on every device (the
+// attribute call costs about as much host time as a launch).  One per kernel.
+struct Kv4SmemLimit {
+  std::atomic<uint64_t> done{0};
+  cudaError_t raise(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 struct Kv4TablesParams {
   const int32_t* kv_lens;

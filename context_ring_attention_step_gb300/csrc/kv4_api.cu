@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -57,8 +58,12 @@ size_t page_bytes(int32_t page_size, int32_t Hkv, int32_t D) {
 }
 
 // Requests with at least this many rows (tokens x heads of a group) go to the
-// tile kernel, where a call can have them.
-constexpr int kTileMinRows = 64;
+// tile kernel, where a call can have them.  Its time hardly depends on the rows
+// up to 128 a request, the other's grows with each 24 of them; over 131072
+// cached tokens (8 heads, head_dim 128 / 64) they take, in us, at
+//   64 rows  193 / 158 (tiles), 162 / 126 (few rows)
+//   96 rows  198 / 160 (tiles), 202 / 175 (few rows).
+constexpr int kTileMinRows = 96;
 bool has_tiles(int32_t D, int32_t G, int32_t max_q_len) {
   return D <= 128 && (int64_t)G * max_q_len >= kTileMinRows;
 }
@@ -66,6 +71,18 @@ bool has_tiles(int32_t D, int32_t G, int32_t max_q_len) {
 // one token where the tile kernel takes the long ones.
 int64_t few_rows(int32_t D, int32_t G, int32_t max_q_len) {
   return has_tiles(D, G, max_q_len) ? G : (int64_t)G * max_q_len;
+}
+
+// SMs of the current device (a property of the hardware: asked once).
+cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 struct AttnLayout {
@@ -244,9 +261,8 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
   p.ended = p.status + 2;
   p.tickets = reinterpret_cast<int32_t*>(ws + l.tickets);
   p.partials = reinterpret_cast<float*>(ws + l.partials);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   const int32_t G = num_q_heads / Hkv;
   const bool tiles = has_tiles(D, G, max_q_len);

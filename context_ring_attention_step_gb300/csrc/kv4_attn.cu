@@ -627,7 +627,8 @@ template <int D, int NT>
 cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
   using C = AttnCfg<D, NT>;
   auto kern = kv4_attn_kernel<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static Kv4SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, C::kSmem, stream>>>(p);
   return cudaGetLastError();

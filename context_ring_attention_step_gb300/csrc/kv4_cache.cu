@@ -298,8 +298,9 @@ cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream) {
     cfg.blockDim = dim3(256);
     return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<256>, p);
   }
-  cudaError_t e = cudaFuncSetAttribute(kv4_tables_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (4 * kKv4MaxRequests + 3) * (int)sizeof(int32_t));
+  static Kv4SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kv4_tables_kernel<1024>),
+                                    (4 * kKv4MaxRequests + 3) * (int)sizeof(int32_t));
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(attr[0].val.clusterDim.x = 8);
   cfg.blockDim = dim3(1024);

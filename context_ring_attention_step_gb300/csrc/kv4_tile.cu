@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   const Abort ab{s_int, s_int + 1};
   if (bad) atomicMax(s_int + 1, bad);
 
-  // Register split: 512 threads x 128 at launch = 128 x 40 + 256 x 192 + 128 x 88.
+  // Register split: 512 threads x 128 at launch = 128 x 40 + 256 x 184 + 128 x 104.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp < 2 && lane == 0) {
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       }
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------ softmax
     const int qt = (warp - 4) >> 2, row_t = tid - 128 * (1 + qt);  // row within the Q tile
     const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       turns += na_other;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ------------------------------------------------------------ expansion
     using L = Kv4Layout<D>;
     const int dw = warp - 12;  // cache tiles 2 dw and 2 dw + 1 of every key tile
@@ -700,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
 template <int D>
 cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
   auto kern = kv4_tile_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<D>::kSmem);
+  static Kv4SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), TileCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, TileCfg<D>::kSmem, stream>>>(p);
   return cudaGetLastError();

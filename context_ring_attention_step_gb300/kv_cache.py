@@ -58,22 +58,34 @@ class Kv4Cache:
 Kv4Tables = collections.namedtuple("Kv4Tables", "kv_lens cu_new slot_map positions free_count status")
 
 
+def _library():
+    return _ra._lib or _ra.load_library()
+
+
 def _launch(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device current."""
     i = device.index
-    if torch.cuda.current_device() == i:
-        _ra._check(fn(*args, _current_raw_stream(i)))
+    if torch._C._cuda_getDevice() == i:
+        status = fn(*args, _current_raw_stream(i))
     else:
         with torch.cuda.device(i):
-            _ra._check(fn(*args, _current_raw_stream(i)))
+            status = fn(*args, _current_raw_stream(i))
+    if status:
+        _ra._check(status)
+
+
+def _on_gpu(name, device):
+    if device.type != "cuda":
+        raise ValueError("%s is on %s, expected a GPU" % (name, device))
 
 
 def _array(name, t, shape, dtype, device):
-    if t.dtype != dtype:
+    """Pointer of a contiguous tensor with exactly this shape, type and device."""
+    if t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != device or not t.is_cuda:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device if device.type == "cuda" else "a GPU"))
-    if tuple(t.shape) != shape:
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -82,30 +94,33 @@ def _array(name, t, shape, dtype, device):
 
 def _rows(name, t, heads, dim, device):
     """(pointer, row stride) of a [T, heads, dim] bf16 tensor whose rows are dense."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, torch.bfloat16))
-    if t.device != device or not t.is_cuda:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device if device.type == "cuda" else "a GPU"))
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError("%s has shape %s, expected [T, %d, %d]" % (name, tuple(t.shape), heads, dim))
-    if t.shape[0] == 0:
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError("%s has shape %s, expected [T, %d, %d]" % (name, tuple(shape), heads, dim))
+    if shape[0] == 0:
         return 0, heads * dim
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != dim):
         raise ValueError("%s: the heads of a row must lie one after the other (strides %s)" % (name, tuple(s)))
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), s[0] if shape[0] > 1 else heads * dim
 
 
 def _table(block_table, num_requests, device):
-    if block_table.dim() != 2 or block_table.shape[0] != num_requests:
-        raise ValueError("block_table has shape %s, expected [%d, pages]" % (tuple(block_table.shape), num_requests))
-    if block_table.dtype != torch.int32 or block_table.device != device or not block_table.is_cuda:
+    """(pointer, width, row stride) of an int32 [num_requests, width] tensor whose rows are dense."""
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != num_requests:
+        raise ValueError("block_table has shape %s, expected [%d, pages]" % (tuple(shape), num_requests))
+    if block_table.dtype is not torch.int32 or block_table.device != device:
         raise ValueError("block_table must be an int32 tensor on %s" % device)
-    w = block_table.shape[1]
-    if w > 1 and block_table.stride(1) != 1:
+    w = shape[1]
+    s = block_table.stride()
+    if w > 1 and s[1] != 1:
         raise ValueError("block_table rows must be dense")
-    stride = block_table.stride(0) if num_requests > 1 else max(w, 1)
-    return block_table.data_ptr(), w, stride
+    return block_table.data_ptr(), w, s[0] if num_requests > 1 else max(w, 1)
 
 
 def kv4_tables_out(num_requests, num_slots, device="cuda"):
@@ -129,8 +144,9 @@ def kv4_tables(kv_lens, new_lens, block_table, page_size, num_slots, free_pages=
     enough pages, ...) changes nothing and says so in ``status``;
     ``check=True`` synchronises and raises.
     """
-    lib = _ra.load_library()
+    lib = _library()
     dev, R = kv_lens.device, kv_lens.shape[0]
+    _on_gpu("kv_lens", dev)
     num_slots = int(num_slots)
     if out is None:
         out = kv4_tables_out(R, num_slots, dev)
@@ -164,10 +180,11 @@ def kv4_store(cache, k, v, slot_map, check=False):
     slot, or one outside the cache, are left out.  A slot must not occur twice;
     ``check=True`` synchronises and raises if one does or lies outside.
     """
-    lib = _ra.load_library()
+    lib = _library()
     dev, T = cache.device, slot_map.shape[0]
     kp, ks = _rows("k", k, cache.num_kv_heads, cache.head_dim, dev)
     vp, vs = _rows("v", v, cache.num_kv_heads, cache.head_dim, dev)
+    _on_gpu("cache", dev)
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("k, v and slot_map have %d, %d and %d rows" % (k.shape[0], v.shape[0], T))
     slots = _array("slot_map", slot_map, (T,), torch.int64, dev)
@@ -185,8 +202,9 @@ def kv4_load(cache, slot_map, out=None):
 
     Rows with a negative slot, or one outside the cache, become zero.
     """
-    lib = _ra.load_library()
+    lib = _library()
     dev, T = cache.device, slot_map.shape[0]
+    _on_gpu("cache", dev)
     shape = (T, cache.num_kv_heads, cache.head_dim)
     slots = _array("slot_map", slot_map, (T,), torch.int64, dev)
     if out is None:
@@ -219,12 +237,13 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None,
     the kernel variant.  Not differentiable.  ``check=True`` synchronises and
     raises if the lengths, offsets or pages were out of range.
     """
-    lib = _ra.load_library()
+    lib = _library()
     if q.requires_grad and torch.is_grad_enabled():
         raise ValueError("kv4_attention has no gradient: call it under torch.no_grad()")
     dev, R = cache.device, kv_lens.shape[0]
     if q.dim() != 3:
         raise ValueError("q has shape %s, expected [T, heads, %d]" % (tuple(q.shape), cache.head_dim))
+    _on_gpu("cache", dev)
     T, Hq, D = q.shape
     qp, qs = _rows("q", q, Hq, cache.head_dim, dev)
     table, width, stride = _table(block_table, R, dev)
@@ -253,5 +272,5 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None,
 def kv4_status(status):
     """Synchronise and raise if the status word at the start of ``status`` (``Kv4Tables.status``,
     or the workspace of ``kv4_attention``) reports a refusal."""
-    lib = _ra.load_library()
+    lib = _library()
     _launch(status.device, lib.ra_kv4_status, status.data_ptr())
