@@ -28,7 +28,7 @@ __device__ __forceinline__ uint32_t kv4_scale_byte(float amax, float& scale) {
 
 // 16 bf16 elements (two 16-byte words) -> 8 bytes of codes, element 2b in the
 // low and 2b + 1 in the high half of byte b; returns the scale byte.
-__device__ __forceinline__ uint32_t kv4_round_group(const uint4* __restrict__ src, uint2& codes) {
+__device__ __forceinline__ uint32_t kv4_round_group(const uint4 (&src)[2], uint2& codes) {
   const uint4 a = src[0], b = src[1];
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   // magnitudes as integers order like the numbers; both halves of a word at once
@@ -74,23 +74,19 @@ __device__ __forceinline__ void kv4_code_pairs(uint32_t w, uint32_t (&r)[4]) {
       : "r"(w));
 }
 
-// Codes and scale byte of a group -> 16 bf16 values (exact: 6 significant bits).
-__device__ __forceinline__ void kv4_expand_group(uint2 codes, uint32_t scale, uint4 (&out)[2]) {
+// Eight codes and their group's scale byte -> eight bf16 values (exact: 6
+// significant bits).
+__device__ __forceinline__ uint4 kv4_expand_half(uint32_t codes, uint32_t scale) {
   const float s = __half2float(__ushort_as_half((unsigned short)(scale << 7)));
-  uint32_t o[8];
+  uint32_t h[4], o[4];
+  kv4_code_pairs(codes, h);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t h[4];
-    kv4_code_pairs(i ? codes.y : codes.x, h);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-      const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
-      o[4 * i + j] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
+    o[j] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 }  // namespace ra

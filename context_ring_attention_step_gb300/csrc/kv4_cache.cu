@@ -3,6 +3,8 @@
 //     of a step, from the requests' lengths;
 //   * store: bf16 rows rounded to 4 bits into the pages;
 //   * load: cached rows back as bf16.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,11 +25,14 @@ struct Counts {
   int32_t add, need, back;
 };
 
-// One cluster runs the whole step.  Every CTA computes the prefix sums of all
+// One launch runs the whole step.  Every CTA computes the prefix sums of all
 // requests for itself (at most 4096 of them: a few loads a thread), then the
-// cluster shares out the pages and the slots.  Nothing is written before every
-// CTA has read the lengths and the free count, so the new lengths and the new
-// free count may replace the old ones in place.
+// CTAs share out the pages and the slots.  What one CTA reads no other writes:
+// pages taken in this step are computed again rather than read back, table
+// entries and free pages are written only where none are read.  The new lengths
+// and the new free count are the exception when they replace the old ones in
+// place: the grid is then one cluster, which waits until all have read them.
+// 262144 slots of 256 requests: 26 us as one cluster of 8 CTAs, 13 us as 256 CTAs.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesParams p) {
   extern __shared__ int32_t sm[];
@@ -38,7 +43,6 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
   int32_t* s_back = s_need + R + 1;   // [R + 1] pages given back before request r
   __shared__ Counts s_warp[kThreads / 32];
   __shared__ int s_bad;
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool alloc = p.free_pages != nullptr;
   const int32_t count = alloc ? *p.free_count : 0;
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
   const bool ok = code == 0;
   int32_t ea = (int32_t)ba + xa - (int32_t)add64, en = (int32_t)bn + xn - (int32_t)need64,
           eb = (int32_t)bb + xb - (int32_t)back64;
-  const bool lead = cluster.block_rank() == 0;
+  const bool lead = blockIdx.x == 0;
   for (int r = r0; r < r1; ++r) {
     int32_t len;
     const Counts c = counts(r, len);
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
   bool gone[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) gone[i] = r0 + i < r1 && p.new_lens[r0 + i] < 0;
-  cluster.sync();  // every CTA has read its inputs; this CTA's prefix sums are in place
+  cg::this_cluster().sync();  // the cluster has read its inputs; this CTA's prefix sums are in place
 
   if (lead) {
     for (int r = r0; r < r1; ++r) {
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
     const int r = find(s_back, i - count);
     return p.block_table[(size_t)r * p.table_stride + (i - count - s_back[r])];
   };
-  const int g0 = cluster.block_rank() * kThreads + tid, gn = cluster.num_blocks() * kThreads;
+  const int g0 = blockIdx.x * kThreads + tid, gn = gridDim.x * kThreads;
   for (int32_t i = g0; i < back; i += gn) p.free_pages[count + i] = free_page(count + i);
   for (int32_t i = g0; i < need; i += gn) {
     const int r = find(s_need, i);
@@ -213,71 +217,155 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
 
 // ------------------------------------------------------------------ store / load
 
-// One thread a group of 16 elements: 32 bytes of the row.
-template <int D>
-__global__ void __launch_bounds__(256) kv4_store_kernel(const Kv4RowsParams p) {
-  using L = Kv4Layout<D>;
-  const int groups = p.cache.Hkv * L::kGroups;
-  const int64_t n = p.T * groups;
-  const int64_t pmask = (int64_t(1) << p.cache.page_shift) - 1;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = i / groups;
-    const int gi = (int)(i - t * groups);
-    const int64_t slot = p.slots[t];
-    const int64_t page = slot >> p.cache.page_shift;
-    if (slot < 0 || page >= p.cache.num_pages) continue;
-    const int head = gi / L::kGroups, g = gi % L::kGroups, tok = (int)(slot & pmask);
-    uint8_t* tile = p.cache.pages + kv4_tile_offset<D>(p.cache, page, head, tok);
-    const int tt = tok & 15;
-    uint2 codes;
-    uint32_t sc = kv4_round_group(reinterpret_cast<const uint4*>(
-        reinterpret_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + gi * 16), codes);
-    *reinterpret_cast<uint2*>(tile + L::k_code(tt, g)) = codes;
-    tile[L::k_scale(tt, g)] = (uint8_t)sc;
-    sc = kv4_round_group(reinterpret_cast<const uint4*>(
-        reinterpret_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride + gi * 16), codes);
-    *reinterpret_cast<uint32_t*>(tile + L::v_code(tt, g, 0)) = codes.x;
-    *reinterpret_cast<uint32_t*>(tile + L::v_code(tt, g, 1)) = codes.y;
-    tile[L::v_scale(tt, g)] = (uint8_t)sc;
+// Tokens are taken four at a time (Q = 4): value codes of four neighbouring
+// slots (the first a multiple of four) share 32-byte sectors, so that a prompt's
+// rows move whole sectors.  Few rows go one at a time (Q = 1), to more threads.
+// Threads of a block walk (quad, column) pairs, columns first.
+struct Columns {
+  uint32_t n, magic;  // columns of a quad; x / n = umulhi(x, magic) for x < 2^32 / n
+};
+
+// Slots of the quad's tokens, -1 where there is none; true if they are four
+// neighbours, the first a multiple of four.
+template <int Q>
+__device__ __forceinline__ bool quad_slots(const Kv4RowsParams& p, int64_t q, int64_t (&slot)[Q]) {
+  const int64_t end = p.cache.num_pages << p.cache.page_shift;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    slot[i] = Q * q + i < p.T ? __ldg(p.slots + Q * q + i) : -1;
+    if (slot[i] >= end) slot[i] = -1;
   }
+  bool neighbours = Q == 4 && slot[0] >= 0 && (slot[0] & 3) == 0;
+#pragma unroll
+  for (int i = 1; i < Q; ++i) neighbours &= slot[i] == slot[0] + i;
+  return neighbours;
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4RowsParams p) {
-  using L = Kv4Layout<D>;
-  const int groups = p.cache.Hkv * L::kGroups;
-  const int64_t n = p.T * groups;
+__device__ __forceinline__ uint8_t* tile_of(const Kv4RowsParams& p, int64_t slot, int head) {
   const int64_t pmask = (int64_t(1) << p.cache.page_shift) - 1;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = i / groups;
-    const int gi = (int)(i - t * groups);
-    const int64_t slot = p.slots[t];
-    const int64_t page = slot >> p.cache.page_shift;
-    uint4 ko[2] = {}, vo[2] = {};
-    if (slot >= 0 && page < p.cache.num_pages) {
-      const int head = gi / L::kGroups, g = gi % L::kGroups, tok = (int)(slot & pmask);
-      const uint8_t* tile = p.cache.pages + kv4_tile_offset<D>(p.cache, page, head, tok);
-      const int tt = tok & 15;
-      kv4_expand_group(*reinterpret_cast<const uint2*>(tile + L::k_code(tt, g)), tile[L::k_scale(tt, g)], ko);
-      kv4_expand_group(make_uint2(*reinterpret_cast<const uint32_t*>(tile + L::v_code(tt, g, 0)),
-                                  *reinterpret_cast<const uint32_t*>(tile + L::v_code(tt, g, 1))),
-                       tile[L::v_scale(tt, g)], vo);
+  return p.cache.pages + kv4_tile_offset<D>(p.cache, slot >> p.cache.page_shift, head, (int)(slot & pmask));
+}
+
+// A column is a group of 16 elements: 32 bytes of each of the four rows, of K and
+// of V.
+template <int D, int Q>
+__global__ void __launch_bounds__(256) kv4_store_kernel(const Kv4RowsParams p, const Columns col, int quads_per_block) {
+  using L = Kv4Layout<D>;
+  const int64_t quads = (p.T + Q - 1) / Q;
+  for (int64_t q0 = blockIdx.x * (int64_t)quads_per_block; q0 < quads; q0 += (int64_t)gridDim.x * quads_per_block) {
+    for (uint32_t i = threadIdx.x; i < quads_per_block * col.n; i += 256) {
+      const uint32_t ql = __umulhi(i, col.magic);
+      const int gi = (int)(i - ql * col.n);
+      const int64_t q = q0 + ql;
+      if (q >= quads) break;
+      int64_t slot[Q];
+      const bool neighbours = quad_slots<Q>(p, q, slot);
+      const int head = gi / L::kGroups, g = gi % L::kGroups;
+      uint4 k[Q][2], v[Q][2];
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        if (slot[j] < 0) continue;
+        const uint4* ks = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.k) + (Q * q + j) * p.k_stride + gi * 16);
+        const uint4* vs = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.v) + (Q * q + j) * p.v_stride + gi * 16);
+        k[j][0] = __ldg(ks);
+        k[j][1] = __ldg(ks + 1);
+        v[j][0] = __ldg(vs);
+        v[j][1] = __ldg(vs + 1);
+      }
+      uint2 vc[Q];
+      uint32_t vb[Q];
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        if (slot[j] < 0) continue;
+        uint8_t* tile = tile_of<D>(p, slot[j], head);
+        const int t = (int)(slot[j] & 15);
+        uint2 c;
+        const uint32_t b = kv4_round_group(k[j], c);
+        *reinterpret_cast<uint2*>(tile + L::k_code(t, g)) = c;
+        tile[L::k_scale(t, g)] = (uint8_t)b;
+        vb[j] = kv4_round_group(v[j], vc[j]);
+        if (!neighbours) {
+          *reinterpret_cast<uint32_t*>(tile + L::v_code(t, g, 0)) = vc[j].x;
+          *reinterpret_cast<uint32_t*>(tile + L::v_code(t, g, 1)) = vc[j].y;
+          tile[L::v_scale(t, g)] = (uint8_t)vb[j];
+        }
+      }
+      if constexpr (Q == 4) {
+        if (!neighbours) continue;
+        uint8_t* tile = tile_of<D>(p, slot[0], head);
+        const int t = (int)(slot[0] & 15);
+        if (D == 128) {  // tokens t .. t + 3: 32 bytes
+          uint4* dst = reinterpret_cast<uint4*>(tile + L::v_code(t, g, 0));
+          dst[0] = make_uint4(vc[0].x, vc[0].y, vc[1].x, vc[1].y);
+          dst[1] = make_uint4(vc[2].x, vc[2].y, vc[3].x, vc[3].y);
+        } else if (D == 64) {  // two tokens of one half: 8 bytes
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            *reinterpret_cast<uint2*>(tile + L::v_code(t + j, g, 0)) = make_uint2(vc[j].x, vc[j + 1].x);
+            *reinterpret_cast<uint2*>(tile + L::v_code(t + j, g, 1)) = make_uint2(vc[j].y, vc[j + 1].y);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint2*>(tile + L::v_code(t + j, g, 0)) = vc[j];
+        }
+        *reinterpret_cast<uint16_t*>(tile + L::v_scale(t, g)) = (uint16_t)(vb[0] | vb[1] << 8);
+        *reinterpret_cast<uint16_t*>(tile + L::v_scale(t + 2, g)) = (uint16_t)(vb[2] | vb[3] << 8);
+      }
     }
-    uint4* kd = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.k_out) + i * 16);
-    uint4* vd = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.v_out) + i * 16);
-    kd[0] = ko[0];
-    kd[1] = ko[1];
-    vd[0] = vo[0];
-    vd[1] = vo[1];
   }
 }
 
+// A column is 8 elements: one 16-byte word of each of the four rows, of K and of
+// V, so that the lanes of a warp write whole rows.
+template <int D, int Q>
+__global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4RowsParams p, const Columns col, int quads_per_block) {
+  using L = Kv4Layout<D>;
+  const int64_t quads = (p.T + Q - 1) / Q;
+  const int64_t row = (int64_t)p.cache.Hkv * D;
+  for (int64_t q0 = blockIdx.x * (int64_t)quads_per_block; q0 < quads; q0 += (int64_t)gridDim.x * quads_per_block) {
+    for (uint32_t i = threadIdx.x; i < quads_per_block * col.n; i += 256) {
+      const uint32_t ql = __umulhi(i, col.magic);
+      const int ci = (int)(i - ql * col.n);
+      const int64_t q = q0 + ql;
+      if (q >= quads) break;
+      int64_t slot[Q];
+      quad_slots<Q>(p, q, slot);
+      const int head = ci / (2 * L::kGroups), g = (ci >> 1) % L::kGroups, half = ci & 1;
+      uint32_t kc[Q] = {}, vc[Q] = {}, kb[Q] = {}, vb[Q] = {};
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        if (slot[j] < 0) continue;
+        const uint8_t* tile = tile_of<D>(p, slot[j], head);
+        const int t = (int)(slot[j] & 15);
+        kc[j] = __ldg(reinterpret_cast<const uint32_t*>(tile + L::k_code(t, g) + 4 * half));
+        vc[j] = __ldg(reinterpret_cast<const uint32_t*>(tile + L::v_code(t, g, half)));
+        kb[j] = __ldg(tile + L::k_scale(t, g));
+        vb[j] = __ldg(tile + L::v_scale(t, g));
+      }
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        if (Q * q + j >= p.T) break;
+        const int64_t off = (Q * q + j) * row + ci * 8;
+        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.k_out) + off), kv4_expand_half(kc[j], kb[j]));
+        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.v_out) + off), kv4_expand_half(vc[j], vb[j]));
+      }
+    }
+  }
+}
+
+// Four tokens a thread where that still fills the GPU (152 SMs x 2048 threads),
+// else one: 64 rows of 8 heads are stored and read back in 11.4 us one by one and
+// in 13.4 by fours, 32768 of them in 81 and 73 us.
 template <typename F>
-cudaError_t launch_rows(F kernel, int D, const Kv4RowsParams& p, cudaStream_t stream) {
-  const int64_t n = p.T * p.cache.Hkv * (D / 16);
-  if (n == 0) return cudaSuccess;
-  const int64_t blocks = (n + 255) / 256;
-  kernel<<<(unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), 256, 0, stream>>>(p);
+cudaError_t launch_rows(F by_one, F by_four, uint32_t columns, const Kv4RowsParams& p, cudaStream_t stream) {
+  if (p.T == 0) return cudaSuccess;
+  const bool four = p.T * columns >= 4 * 152 * 2048;
+  const int per_block = columns >= 256 ? 1 : 256 / columns;  // quads: about one column a thread
+  const int64_t quads = four ? (p.T + 3) / 4 : p.T;
+  const int64_t blocks = std::min<int64_t>((quads + per_block - 1) / per_block, 1 << 20);
+  const Columns col{columns, (uint32_t)((uint64_t(1) << 32) / columns + 1)};
+  (four ? by_four : by_one)<<<(unsigned)blocks, 256, 0, stream>>>(p, col, per_block);
   return cudaGetLastError();
 }
 
@@ -293,31 +381,34 @@ cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.num_slots <= 1024 && p.num_requests <= 256) {
-    cfg.gridDim = dim3(attr[0].val.clusterDim.x = 1);
-    cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<256>, p);
-  }
+  const bool in_place = p.kv_lens_out == p.kv_lens || (p.free_pages && p.free_count_out == p.free_count);
+  // 256 threads take up to four requests each; four slots a thread
+  const bool small = p.num_requests <= 1024;
+  const int64_t threads = small ? 256 : 1024;
+  const int64_t want = std::max<int64_t>(1, (p.num_slots + 4 * threads - 1) / (4 * threads));
+  const int64_t most = in_place ? 8 : small ? 304 : 152;
+  cfg.gridDim = dim3((unsigned)std::min(want, most));
+  cfg.blockDim = dim3((unsigned)threads);
+  attr[0].val.clusterDim.x = in_place ? cfg.gridDim.x : 1;
+  if (small) return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<256>, p);
   static Kv4SmemLimit limit;
   const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kv4_tables_kernel<1024>),
                                     (4 * kKv4MaxRequests + 3) * (int)sizeof(int32_t));
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(attr[0].val.clusterDim.x = 8);
-  cfg.blockDim = dim3(1024);
   return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<1024>, p);
 }
 
 cudaError_t launch_kv4_store(int D, const Kv4RowsParams& p, cudaStream_t stream) {
-  if (D == 64) return launch_rows(kv4_store_kernel<64>, D, p, stream);
-  if (D == 128) return launch_rows(kv4_store_kernel<128>, D, p, stream);
-  if (D == 256) return launch_rows(kv4_store_kernel<256>, D, p, stream);
+  if (D == 64) return launch_rows(kv4_store_kernel<64, 1>, kv4_store_kernel<64, 4>, p.cache.Hkv * 4, p, stream);
+  if (D == 128) return launch_rows(kv4_store_kernel<128, 1>, kv4_store_kernel<128, 4>, p.cache.Hkv * 8, p, stream);
+  if (D == 256) return launch_rows(kv4_store_kernel<256, 1>, kv4_store_kernel<256, 4>, p.cache.Hkv * 16, p, stream);
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_kv4_load(int D, const Kv4RowsParams& p, cudaStream_t stream) {
-  if (D == 64) return launch_rows(kv4_load_kernel<64>, D, p, stream);
-  if (D == 128) return launch_rows(kv4_load_kernel<128>, D, p, stream);
-  if (D == 256) return launch_rows(kv4_load_kernel<256>, D, p, stream);
+  if (D == 64) return launch_rows(kv4_load_kernel<64, 1>, kv4_load_kernel<64, 4>, p.cache.Hkv * 8, p, stream);
+  if (D == 128) return launch_rows(kv4_load_kernel<128, 1>, kv4_load_kernel<128, 4>, p.cache.Hkv * 16, p, stream);
+  if (D == 256) return launch_rows(kv4_load_kernel<256, 1>, kv4_load_kernel<256, 4>, p.cache.Hkv * 32, p, stream);
   return cudaErrorInvalidValue;
 }
 

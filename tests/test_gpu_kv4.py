@@ -85,6 +85,35 @@ def test_store_load_are_exact(ra, d, H, page, T):
     assert torch.equal(torch.nan_to_num(k2[:n]), torch.nan_to_num(k2[n:2 * n])) and k2[2 * n:].eq(0).all()
 
 
+@pytest.mark.parametrize("d,T", [(64, 39001), (128, 19458), (256, 9733)])
+def test_store_load_of_a_long_prompt(ra, d, T):
+    """Enough rows for the kernels that take four at a time: neighbouring slots, at every alignment, and gaps."""
+    rng = np.random.default_rng(T)
+    H, page = 8, 64
+    pages = T // page + 4
+    t = np.arange(T) + 3                                         # the first slot is not a multiple of four
+    slots = rng.permutation(pages)[t // page] * page + t % page
+    for a in rng.integers(0, T - 300, 40):                       # stretches that start at other alignments
+        n = int(rng.integers(1, 200))
+        slots[a:a + n] = np.roll(slots[a:a + n], int(rng.integers(1, 9)))
+    given = slots.copy()
+    given[rng.random(T) < 0.01] = -1
+    given[rng.random(T) < 0.01] = pages * page + 5
+    keep = (given >= 0) & (given < pages * page)
+    k, v = bf16(rng, T, H, d), bf16(rng, T, H, d)
+    cache = ra.Kv4Cache(pages, page, H, d)
+    ra.kv4_store(cache, k.cuda(), v.cuda(), torch.tensor(given).cuda())
+    ko, vo = ra.kv4_load(cache, torch.tensor(slots).cuda())
+    kg, vg = ra.kv4_load(cache, torch.tensor(given).cuda())
+    for got, again, x in ((ko, kg, k), (vo, vg, v)):
+        want = O.rounded(f64(x))
+        want[~keep] = 0
+        np.testing.assert_array_equal(f64(got), want)
+        assert torch.equal(got, again)
+    some = torch.tensor(slots[5:5000:7]).cuda()                  # the same rows, one at a time
+    assert torch.equal(ra.kv4_load(cache, some)[1], vo[5:5000:7])
+
+
 def test_store_leaves_other_slots(ra):
     rng = np.random.default_rng(5)
     cache = ra.Kv4Cache(3, 32, 2, 128)
@@ -158,6 +187,30 @@ def test_tables_match_the_lists(ra, R, page, width, in_place):
         want = O.tables(lens, new, table, page, slots, free, count)
         got = run_tables(ra, lens, new, table, page, slots, free, count, in_place, stride=width + 3 if spare else None)
         assert got == (0,) + want
+
+
+@pytest.mark.parametrize("R", [7, 1500])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_tables_of_long_prompts(ra, R, in_place):
+    """Many CTAs: prompts of thousands of tokens beside single tokens and requests that leave."""
+    rng = random.Random(R)
+    page, width = 32, 700
+    lens = [rng.choice([0, 5, rng.randrange(0, 2000)]) for _ in range(R)]
+    new = [rng.choice([-1, 1, 1, 1, 0]) for _ in range(R)]
+    for r in rng.sample(range(R), 5):
+        new[r] = rng.randrange(3000, 20000)
+    held = [-(-n // page) for n in lens]
+    total = sum(held) + sum(-(-(n + max(a, 0)) // page) for n, a in zip(lens, new))
+    ids = list(range(total))
+    rng.shuffle(ids)
+    table, at = [], 0
+    for h in held:
+        table.append(ids[at:at + h] + [-3] * (width - h))
+        at += h
+    free = ids[at:] + [-5] * at
+    slots = sum(max(a, 0) for a in new) + 1003
+    want = O.tables(lens, new, table, page, slots, free, total - at)
+    assert run_tables(ra, lens, new, table, page, slots, free, total - at, in_place) == (0,) + want
 
 
 @pytest.mark.parametrize("R", [1, 33, 300])
