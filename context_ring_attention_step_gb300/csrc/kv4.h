@@ -142,7 +142,8 @@ struct Kv4AttnParams {
   float* lse;  // [Hq, Tq]
   int32_t* status;
   // Zero between calls: what the CTAs found wrong (RA_KV4_BAD_...), how many of
-  // them have ended, and how many partial results the unit that a CTA began has.
+  // them have ended, and how many of the partial results that are merged together
+  // are there (by the slot of the first one, then by the CTA that began the unit).
   int32_t *found, *ended, *tickets;
   int32_t status_kept;  // the status holds what the other kernel of this call found
   int32_t split_rows;   // rows (query tokens x heads of a group) from which a request is the tile kernel's; 0: see kv4_walk.cuh

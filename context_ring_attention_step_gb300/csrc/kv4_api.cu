@@ -97,7 +97,7 @@ AttnLayout attn_layout(int32_t D, int32_t G, int32_t max_q_len) {
   }
   AttnLayout l;
   l.tickets = kHeader;
-  l.partials = align256(l.tickets + ctas * sizeof(int32_t));
+  l.partials = align256(l.tickets + 3 * ctas * sizeof(int32_t));
   l.total = align256(l.partials + floats * sizeof(float));
   return l;
 }

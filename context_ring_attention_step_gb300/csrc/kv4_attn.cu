@@ -41,6 +41,11 @@ namespace ra {
 namespace {
 
 constexpr int kWarps = 4;
+// What beginning a unit costs, in blocks of 64 keys: 128 ragged requests (lognormal
+// lengths around 2000) take 172 us with 0, 140 with 4 and 8, 150 with 16.
+constexpr int kUnit = 6;
+constexpr int kFan = 8;    // partial results merged at once
+constexpr int kAlone = 4;  // parts of a unit that one warp merges
 constexpr int kThreads = 32 * kWarps;
 constexpr int KB = 16 * kWarps;  // keys of one block: a tile a warp
 // P's reference: a row's largest P is in (2^6, 2^7] when the reference moves,
@@ -67,51 +72,60 @@ struct TileRegs {
   uint32_t ks[D == 256 ? 2 : 1], vs[D == 256 ? 2 : 1];
 };
 
-// Loads of a lane's share; `at` is the tile's address plus 16 x lane.
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// Asynchronous copies of a lane's own words into its warp's ring; `n` bytes (all
+// or none: then zeros) are read.  A lane reads back only what it copied itself, so
+// that waiting for its own copies is all the synchronisation there is.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ uint32_t ldg4(const uint8_t* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups are there
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D>
-__device__ __forceinline__ void load_k(TileRegs<D>& t, const uint8_t* at, int lane) {
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* tile, bool in, int lane) {
   using L = Kv4Layout<D>;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) t.k[i] = ldg16(at + L::kKCodes + 512 * i);
-  const uint8_t* s = at - 16 * lane + L::kKScales;
-  if (D == 64) {
-    t.ks[0] = ldg4(s + (2 * lane & ~3)) >> (16 * (lane & 1));
-  } else if (D == 128) {
-    t.ks[0] = ldg4(s + 4 * lane);
-  } else {
-    const uint2 a = ldg8(s + 8 * lane);
-    t.ks[0] = a.x; t.ks[D == 256 ? 1 : 0] = a.y;
+  for (int i = 0; i < D / 64; ++i) {
+    copy16(dst + L::kKCodes + 512 * i + 16 * lane, tile + L::kKCodes + 512 * i + 16 * lane, in ? 16 : 0);
+    copy16(dst + L::kVCodes + 512 * i + 16 * lane, tile + L::kVCodes + 512 * i + 16 * lane, in ? 16 : 0);
+  }
+  if (D == 256) {
+    copy8(dst + L::kKScales + 8 * lane, tile + L::kKScales + 8 * lane, in ? 8 : 0);
+    copy8(dst + L::kVScales + 8 * lane, tile + L::kVScales + 8 * lane, in ? 8 : 0);
+  } else {  // at head_dim 64 two lanes share a word, and both copy it
+    const int k = D == 64 ? 2 * lane & ~3 : 4 * lane, v = D == 64 ? 4 * ((lane >> 3) * 4 + (lane & 3)) : 4 * lane;
+    copy4(dst + L::kKScales + k, tile + L::kKScales + k, in ? 4 : 0);
+    copy4(dst + L::kVScales + v, tile + L::kVScales + v, in ? 4 : 0);
   }
 }
 template <int D>
-__device__ __forceinline__ void load_v(TileRegs<D>& t, const uint8_t* at, int lane) {
+__device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* tile, int lane) {
   using L = Kv4Layout<D>;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) t.v[i] = ldg16(at + L::kVCodes + 512 * i);
-  const uint8_t* s = at - 16 * lane + L::kVScales;
+  for (int i = 0; i < D / 64; ++i) {
+    t.k[i] = *reinterpret_cast<const uint4*>(tile + L::kKCodes + 512 * i + 16 * lane);
+    t.v[i] = *reinterpret_cast<const uint4*>(tile + L::kVCodes + 512 * i + 16 * lane);
+  }
   if (D == 64) {
-    t.vs[0] = ldg4(s + 4 * ((lane >> 3) * 4 + (lane & 3)));
+    t.ks[0] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + 2 * lane);
+    t.vs[0] = *reinterpret_cast<const uint32_t*>(tile + L::kVScales + 4 * ((lane >> 3) * 4 + (lane & 3)));
   } else if (D == 128) {
-    t.vs[0] = ldg4(s + 4 * lane);
+    t.ks[0] = *reinterpret_cast<const uint32_t*>(tile + L::kKScales + 4 * lane);
+    t.vs[0] = *reinterpret_cast<const uint32_t*>(tile + L::kVScales + 4 * lane);
   } else {
-    const uint2 a = ldg8(s + 8 * lane);
-    t.vs[0] = a.x; t.vs[D == 256 ? 1 : 0] = a.y;
+    const uint2 a = *reinterpret_cast<const uint2*>(tile + L::kKScales + 8 * lane);
+    const uint2 b = *reinterpret_cast<const uint2*>(tile + L::kVScales + 8 * lane);
+    t.ks[0] = a.x; t.ks[D == 256 ? 1 : 0] = a.y;
+    t.vs[0] = b.x; t.vs[D == 256 ? 1 : 0] = b.y;
   }
 }
 
@@ -315,7 +329,11 @@ struct AttnCfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kPerSm = ctas_per_sm(D, NT);
   static constexpr int kFrag = NT * (D / 16);       // float4 accumulators of a lane
-  static constexpr int kSmem = (kWarps / 2) * kFrag * 512;
+  static constexpr int kMerge = (kWarps / 2) * kFrag * 512;
+  static constexpr int kFit = ((220 / kPerSm - 2) * 1024 - kMerge) / (kWarps * Kv4Layout<D>::kBytes);
+  static constexpr int kSlots = kFit > 6 ? 6 : kFit;  // ring of each warp
+  static constexpr int kSmem = kSlots * kWarps * Kv4Layout<D>::kBytes + kMerge;
+  static_assert(kSlots >= 3, "tiles under way");
   static constexpr int kSlot = (kFrag + NT) * 128;  // floats of a partial result
 };
 
@@ -323,7 +341,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_kernel(const Kv4AttnParams p) {
   using C = AttnCfg<D, NT>;
   using L = Kv4Layout<D>;
-  constexpr int RT = C::kRows;
+  constexpr int RT = C::kRows, S = C::kSlots;
   extern __shared__ __align__(128) uint8_t s_dyn[];
   __shared__ __align__(16) float4 s_ml[2][kWarps][NT][4];  // m and l of a warp's rows, for two units in turn
   __shared__ long long s_sum[kWarps];
@@ -332,21 +350,54 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r8 = lane >> 2, c4 = lane & 3;
   const int G = p.Hq / p.cache.Hkv, Hkv = p.cache.Hkv;
-  float4* s_o = reinterpret_cast<float4*>(s_dyn);  // [kWarps / 2][kFrag][32]
+  uint8_t* ring = s_dyn + warp * S * L::kBytes;
+  float4* s_o = reinterpret_cast<float4*>(s_dyn + kWarps * S * L::kBytes);  // [kWarps / 2][kFrag][32]
   if (tid == 0) s_bad = 0;
 
   int bad = 0;
   Kv4Walk wk;
-  const Kv4Line line = kv4_find_part<RT, KB, false, kThreads>(p, s_sum, s_found, wk, bad);
+  const Kv4Line line = kv4_find_part<RT, KB, kUnit, false, kThreads>(p, s_sum, s_found, wk, bad);
 
   int units = 0;
   while (wk.pos < line.end) {
-    wk.enter<RT, KB, false>(p);
+    wk.enter<RT, KB, kUnit, false>(p, line.end);
     const Kv4Request& rq = wk.rq;
     const int blk0 = wk.blk, head = wk.head;
-    const int nb = (int)min((long long)(rq.blocks - blk0), line.end - wk.pos);
+    const int nb = wk.nb;
+    if (nb == 0) {
+      wk.leave(line.end);
+      continue;
+    }
     const int row0 = wk.rt * RT, rows = min(RT, rq.n * G - row0);
     const int lim_min = kv4_key_limit(p, rq, row0), lim_max = wk.t_end;
+
+    // ---- this warp's tiles: keys t0, t0 + KB, ...  S - 1 tiles are under way into
+    // the ring while one is worked on, without a branch or a barrier: behind the
+    // last tile, and for a page that is not one of the cache, zeros.  A slot is
+    // filled again one tile after it was read.
+    const int t_stop = min((blk0 + nb) * KB, lim_max);
+    const int32_t* table = p.block_table + (size_t)wk.r * p.table_stride;
+    const int tiles_mask = (1 << (p.cache.page_shift - 4)) - 1;
+    const uint8_t* base = p.cache.pages + ((size_t)head << (p.cache.page_shift - 4)) * L::kBytes;
+    auto page_of = [&](int t) -> int { return t < t_stop ? table[t >> p.cache.page_shift] : 0; };
+    uint32_t oks = 0;  // bit i: the (i + 1)-th last tile asked for comes from a page of the cache
+    auto ask = [&](int slot, int page, int tok) {
+      const bool good = (uint32_t)page < (uint64_t)p.cache.num_pages;
+      oks = oks << 1 | (good ? 1u : 0u);
+      if (!good) bad = RA_KV4_BAD_PAGE;
+      copy_tile<D>(smem_u32(ring) + slot, base + (int64_t)(good ? page : 0) * p.page_bytes + ((tok >> 4) & tiles_mask) * L::kBytes,
+                   good && tok < t_stop, lane);
+      copy_commit();
+    };
+    int t0 = blk0 * KB + 16 * warp;
+    int page = page_of(t0 + (S - 1) * KB);
+    {
+      int pages[S - 1];
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) pages[i] = page_of(t0 + i * KB);
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) ask(i * L::kBytes, pages[i], t0 + i * KB);
+    }
 
     // ---- query rows: fp16 operands, scales and key limits
     uint32_t qf[NT][D / 16][2];
@@ -395,32 +446,18 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
     Acc<D, NT> acc;
     acc.clear();
 
-    // ---- this warp's tiles: keys t0, t0 + KB, ...  The next tile's words and the
-    // page id after that are under way while one is worked on.  For a page that is
-    // not one of the cache, page 0 is read instead, and masked.
-    const int t_stop = min((blk0 + nb) * KB, lim_max);
-    const int32_t* table = p.block_table + (size_t)wk.r * p.table_stride;
-    const int tiles_mask = (1 << (p.cache.page_shift - 4)) - 1;
-    const uint8_t* base = p.cache.pages + ((size_t)head << (p.cache.page_shift - 4)) * L::kBytes + 16 * lane;
-    auto page_of = [&](int t) -> int { return t < t_stop ? table[t >> p.cache.page_shift] : 0; };
-    auto fetch = [&](TileRegs<D>& t, int page, int tok) {
-      const uint32_t pg = (uint32_t)page < (uint64_t)p.cache.num_pages ? page : 0;
-      const uint8_t* at = base + (int64_t)pg * p.page_bytes + ((tok >> 4) & tiles_mask) * L::kBytes;
-      load_k<D>(t, at, lane);
-      load_v<D>(t, at, lane);
-    };
-    int t0 = blk0 * KB + 16 * warp;
-    TileRegs<D> next;
-    int page = page_of(t0), page_next = page_of(t0 + KB);
-    if (t0 < t_stop) fetch(next, page, t0);
+    int slot = 0, slot_ask = (S - 1) * L::kBytes;
 #pragma unroll 1
     for (; t0 < t_stop; t0 += KB) {
-      TileRegs<D> cur = next;
-      const bool page_ok = (uint32_t)page < (uint64_t)p.cache.num_pages;
-      if (!page_ok) bad = RA_KV4_BAD_PAGE;
-      page = page_next;
-      if (t0 + KB < t_stop) fetch(next, page, t0 + KB);
-      page_next = page_of(t0 + 2 * KB);
+      copy_wait<S - 2>();
+      TileRegs<D> cur;
+      load_tile<D>(cur, ring + slot, lane);
+      const bool page_ok = (oks >> (S - 2)) & 1;
+      ask(slot_ask, page, t0 + (S - 1) * KB);
+      slot_ask = slot;
+      slot = slot == (S - 1) * L::kBytes ? 0 : slot + L::kBytes;
+      page = page_of(t0 + S * KB);
+
       // S^T = K Q^T
       float s[NT][4];
 #pragma unroll
@@ -532,50 +569,66 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
       if (masked && __any_sync(0xffffffffu, (nan0 | nan1) != 0)) add_nan<D, NT>(acc, nan0, nan1, t0, lim, lane);
     }
 
+    copy_wait<0>();
+
     // ---- merge the warps; warp 0 then holds the segment's result
     merge_warps<D, NT>(acc, s_ml[units & 1], s_o, warp, lane);
     ++units;
-    const bool direct = blk0 == 0 && nb == rq.blocks;
+    const bool direct = wk.whole();
     if (direct) {
       if (warp == 0) write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
     } else {
-      // a partial result; the CTA that brings a unit's last one merges them all
-      const long long first = wk.pos - blk0, last = first + rq.blocks - 1;
-      const int c0 = line.owner(first), parts = line.owner(last) - c0 + 1;
-      auto slot = [&](int c) {
-        return reinterpret_cast<float4*>(p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * C::kSlot);
-      };
-      if (warp == 0) {
-        float4* dst = slot(blockIdx.x);
+      // A partial result.  Of every kFan neighbours the CTA that brings the last one
+      // merges them into the first one's slot, and of a unit's merged ones the CTA
+      // that brings the last one merges those.
+      const int c0 = line.owner(wk.first), parts = line.owner(wk.first + rq.blocks - 1) - c0 + 1;
+      auto place = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };
+      auto slot = [&](int i) { return reinterpret_cast<float4*>(p.partials + (size_t)place(c0 + i) * C::kSlot); };
+      int at = blockIdx.x - c0, from = at / kFan * kFan, count = min(kFan, parts - from), stride = 1;
+      int* ticket = p.tickets + place(c0 + from);
+      // A unit in few parts is warp 0's business alone; the others go on meanwhile.
+      const bool all = parts > kAlone;
+#pragma unroll 1
+      while (all || warp == 0) {
+        bool is_last = false;
+        if (warp == 0) {
+          float4* dst = slot(at);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          dst[32 * nt + lane] = make_float4(acc.ref(nt, 0), acc.ref(nt, 1), acc.l[nt][0], acc.l[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            dst[32 * nt + lane] = make_float4(acc.ref(nt, 0), acc.ref(nt, 1), acc.l[nt][0], acc.l[nt][1]);
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d)
-            dst[32 * (NT + nt * (D / 16) + d) + lane] =
-                make_float4(acc.o[nt][d][0], acc.o[nt][d][1], acc.o[nt][d][2], acc.o[nt][d][3]);
+            for (int d = 0; d < D / 16; ++d)
+              dst[32 * (NT + nt * (D / 16) + d) + lane] =
+                  make_float4(acc.o[nt][d][0], acc.o[nt][d][1], acc.o[nt][d][2], acc.o[nt][d][3]);
+          }
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) {
+            is_last = atomicAdd(ticket, 1) == count - 1;
+            if (is_last) *ticket = 0;  // as the next call expects it
+            s_last = is_last;
+          }
+          is_last = __shfl_sync(0xffffffffu, is_last, 0);
         }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) s_last = atomicAdd(&p.tickets[c0], 1) == parts - 1;
-      }
-      __syncthreads();
-      if (s_last) {
+        if (all) {
+          __syncthreads();
+          is_last = s_last;
+        }
+        if (!is_last) break;
         __threadfence();
         acc.clear();
         // the rows' largest reference first: the weights, and with them all loads
         // of the partial results, then depend on nothing
         float mm[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mm[nt][0] = mm[nt][1] = neg_inf();
-#pragma unroll 4
-        for (int i = r8; i < parts; i += 8)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float4 ml = __ldcg(slot(c0 + i) + 32 * nt + lane);
+        for (int nt = 0; nt < NT; ++nt) {
+          mm[nt][0] = mm[nt][1] = neg_inf();
+          for (int i = r8; i < count; i += 8) {
+            const float4 ml = __ldcg(slot(from + i * stride) + 32 * nt + lane);
             mm[nt][0] = fmaxf(mm[nt][0], ml.x);
             mm[nt][1] = fmaxf(mm[nt][1], ml.y);
           }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -587,9 +640,9 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
               acc.top[nt][e] = kMaxExp;
             }
           }
-#pragma unroll 4
-        for (int i = warp; i < parts; i += kWarps) {
-          const float4* src = slot(c0 + i);
+#pragma unroll 2
+        for (int i = warp; i < count; i += all ? kWarps : 1) {
+          const float4* src = slot(from + i * stride);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (8 * nt + 2 * c4 >= rows) continue;  // rows that nobody asks for
@@ -608,15 +661,22 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
             }
           }
         }
-        merge_warps<D, NT>(acc, s_ml[units & 1], s_o, warp, lane, false);
-        ++units;
-        if (warp == 0) {
-          write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
-          if (lane == 0) p.tickets[c0] = 0;  // as the next call expects it
+        if (all) {
+          merge_warps<D, NT>(acc, s_ml[units & 1], s_o, warp, lane, false);
+          ++units;
         }
+        if (stride > 1 || parts <= kFan) {
+          if (warp == 0) write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
+          break;
+        }
+        at = from;
+        from = 0;
+        count = (parts + kFan - 1) / kFan;
+        stride = kFan;
+        ticket = p.tickets + 2 * gridDim.x + c0;
       }
     }
-    wk.pos += nb;
+    wk.leave(line.end);
   }
   if (bad) atomicMax(&s_bad, bad);
   __syncthreads();

@@ -33,6 +33,7 @@ namespace {
 constexpr int kRows = 256;
 constexpr int kKeys = 128;
 constexpr int kThreads = 512;
+constexpr int kUnit = 1;  // what beginning a unit costs, in blocks of 128 keys
 constexpr int kSegs = 8;  // segments (and key tiles) that the expanding warps may be ahead, rounded up
 // P's reference as in kv4_attn.cu: the row's largest P is in (2^6, 2^7] when it
 // moves.  A tile whose P's add up to no more than 2^15 needs no look at its maximum.
@@ -59,20 +60,19 @@ struct TileCfg {
 
 // What all roles know of a segment.
 struct Segment {
-  int nb, k0, row0, rows;  // blocks of the line; first key; first row of the unit, rows
+  int k0, row0, rows;  // first key; first row of the unit, rows
   int n;                   // key tiles that some row sees
   int na[2];               // of these, those that a row of Q tile 0 / 1 sees (a prefix)
   int lim_lo[2];           // keys that the tile's first row sees
 };
 
-__device__ __forceinline__ Segment segment(const Kv4AttnParams& p, const Kv4Walk& wk, long long end) {
+__device__ __forceinline__ Segment segment(const Kv4AttnParams& p, const Kv4Walk& wk) {
   Segment s;
   const int G = p.Hq / p.cache.Hkv;
-  s.nb = (int)min((long long)(wk.rq.blocks - wk.blk), end - wk.pos);
   s.k0 = wk.blk * kKeys;
   s.row0 = wk.rt * kRows;
   s.rows = min(kRows, wk.rq.n * G - s.row0);
-  const auto tiles = [&](int lim) { return max(0, min(s.nb, (lim - s.k0 + kKeys - 1) / kKeys)); };
+  const auto tiles = [&](int lim) { return max(0, min(wk.nb, (lim - s.k0 + kKeys - 1) / kKeys)); };
   s.n = tiles(wk.t_end);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   }
   int bad = 0;
   Kv4Walk wk;
-  const Kv4Line line = kv4_find_part<kRows, kKeys, true, kThreads>(p, s_sum, s_found, wk, bad);
+  const Kv4Line line = kv4_find_part<kRows, kKeys, kUnit, true, kThreads>(p, s_sum, s_found, wk, bad);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -277,9 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         }
       };
       for (; wk.pos < line.end && ok;) {
-        wk.enter<kRows, kKeys, true>(p);
-        const Segment sg = segment(p, wk, line.end);
-        wk.pos += sg.nb;
+        wk.enter<kRows, kKeys, kUnit, true>(p, line.end);
+        const Segment sg = segment(p, wk);
+        wk.leave(line.end);
         const int na = qt == 0 ? sg.na[0] : sg.na[1];
         if (sg.n == 0) continue;
         if (na > 0) {
@@ -332,8 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
     uint32_t turns = 0;      // P tiles of the other Q tile in the segments before
     bool ok = true;
     for (; wk.pos < line.end;) {
-      wk.enter<kRows, kKeys, true>(p);
-      const Segment sg = segment(p, wk, line.end);
+      wk.enter<kRows, kKeys, kUnit, true>(p, line.end);
+      if (wk.nb == 0) {
+        wk.leave(line.end);
+        continue;
+      }
+      const Segment sg = segment(p, wk);
       const int na = qt == 0 ? sg.na[0] : sg.na[1];
       const int na_other = qt == 0 ? sg.na[1] : sg.na[0];
       const int urow = 128 * qt + row_t, row = sg.row0 + urow;  // row of the unit, of the request
@@ -485,9 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       }
 
       // ---- output, or a partial result
-      const bool direct = wk.blk == 0 && sg.nb == wk.rq.blocks;
-      const long long first = wk.pos - wk.blk, last = first + wk.rq.blocks - 1;
-      const int c0 = direct ? 0 : line.owner(first);
+      const bool direct = wk.whole();
+      const int c0 = direct ? 0 : line.owner(wk.first);
       auto slot = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * C::kSlot; };
       const float inv = !direct ? 1.f : l_sum == 0.f ? 0.f : 1.f / l_sum;
       const int* nan_key = s_nan + (seg & (kSegs - 1)) * 8;
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         }
         __threadfence();
         softmax_sync();
-        const int parts = line.owner(last) - c0 + 1;
+        const int parts = line.owner(wk.first + wk.rq.blocks - 1) - c0 + 1;
         if (tid == 128) s_int[2] = atomicAdd(&p.tickets[c0], 1) == parts - 1;
         softmax_sync();
         if (s_int[2]) {
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
           if (tid == 128) p.tickets[c0] = 0;  // as the next call expects it
         }
       }
-      wk.pos += sg.nb;
+      wk.leave(line.end);
       tiles += sg.n;
       seg += sg.n > 0;
       turns += na_other;
@@ -606,9 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
     int issued = 0, seg = 0, tiles = 0;
     bool ok = true;
     for (; wk.pos < line.end;) {
-      wk.enter<kRows, kKeys, true>(p);
-      const Segment sg = segment(p, wk, line.end);
-      wk.pos += sg.nb;
+      wk.enter<kRows, kKeys, kUnit, true>(p, line.end);
+      const Segment sg = segment(p, wk);
+      wk.leave(line.end);
       if (sg.n == 0) continue;
       int* nan_key = s_nan + (seg & (kSegs - 1)) * 8;
       if (dw == 0 && lane < 8) nan_key[lane] = 0x7fffffff;

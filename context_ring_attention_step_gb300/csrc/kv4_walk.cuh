@@ -78,53 +78,69 @@ __device__ __forceinline__ Kv4Request kv4_request(const Kv4AttnParams& p, int r)
   q.blocks = max(1, (int)(((long long)L + KB - 1) / KB));
   return q;
 }
+// A unit's length on the line: its blocks, and before them `KU` places that
+// stand for what beginning a unit costs (query rows, first tiles, merge).
+template <int KU>
 __device__ __forceinline__ long long kv4_request_work(const Kv4Request& q, int Hkv) {
-  return (long long)q.row_tiles * Hkv * q.blocks;
+  return (long long)q.row_tiles * Hkv * (q.blocks + KU);
 }
 
 __device__ __forceinline__ int kv4_key_limit(const Kv4AttnParams& p, const Kv4Request& q, int row) {
   return p.causal ? max(0, min(q.L, q.L - q.n + row / (p.Hq / p.cache.Hkv) + 1)) : q.L;
 }
 
-// A place on the line of work: block `blk` of unit (r, rt, head).
+// Quotient of numbers that hardly ever need 64 bits.
+__device__ __forceinline__ long long kv4_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// A place on the line of work, and what a CTA whose part ends at `end` does of
+// the unit (r, rt, head) there: blocks [blk, blk + nb), possibly none.
 struct Kv4Walk {
-  long long pos;   // blocks before this place
-  long long base;  // blocks before request r
+  long long pos;    // places before this one
+  long long base;   // places before request r
+  long long first;  // place of the unit's first block
   int r;
-  int rt = 0, head = 0, blk = 0, t_end = 0;  // t_end: keys that some row of the unit sees
+  int rt = 0, head = 0, blk = 0, nb = 0, t_end = 0;  // t_end: keys that some row of the unit sees
   Kv4Request rq;
-  // find the unit that holds pos (pos is inside the line)
-  template <int RT, int KB, bool kTiles>
-  __device__ __forceinline__ void enter(const Kv4AttnParams& p) {
+  // look at the unit that holds pos (pos is inside the line)
+  template <int RT, int KB, int KU, bool kTiles>
+  __device__ __forceinline__ void enter(const Kv4AttnParams& p, long long end) {
     long long work;
     for (;; ++r) {  // (requests without rows have no work)
       rq = kv4_request<RT, KB, kTiles>(p, r);
-      work = kv4_request_work(rq, p.cache.Hkv);
+      work = kv4_request_work<KU>(rq, p.cache.Hkv);
       if (pos < base + work || r + 1 >= p.R) break;
       base += work;
     }
-    const long long unit = (pos - base) / rq.blocks;
-    blk = (int)(pos - base - unit * rq.blocks);
-    rt = (int)(unit / p.cache.Hkv);
+    const int len = rq.blocks + KU;
+    const long long unit = kv4_div(pos - base, len);
+    first = base + unit * len + KU;
+    rt = (int)kv4_div(unit, p.cache.Hkv);
     head = (int)(unit - (long long)rt * p.cache.Hkv);
+    blk = (int)max(pos - first, 0ll);
+    nb = (int)max(min(first + rq.blocks, end) - (first + blk), 0ll);
     t_end = kv4_key_limit(p, rq, min((rt + 1) * RT, rq.n * (p.Hq / p.cache.Hkv)) - 1);
   }
+  // on to the next unit (or the end of the part)
+  __device__ __forceinline__ void leave(long long end) { pos = min(first + rq.blocks, end); }
+  // does the part hold all of the unit's blocks?
+  __device__ __forceinline__ bool whole() const { return blk == 0 && nb == rq.blocks; }
 };
 
-// The line's length and this CTA's part [begin, end) of it.
+// The line's length and this CTA's part [begin, end) of it.  Of `cut` parts the
+// first `rest` have `size` + 1 places, the others `size`.
 struct Kv4Line {
-  long long total, cut, begin, end;
-  __device__ __forceinline__ int owner(long long x) const {  // the CTA whose part holds block x
-    int c = (int)(x * cut / total);
-    while (total * (c + 1) / cut <= x) ++c;
-    while (total * c / cut > x) --c;
-    return c;
+  long long total, cut, size, rest, begin, end;
+  __device__ __forceinline__ int owner(long long x) const {  // the CTA whose part holds place x
+    const long long longer = rest * (size + 1);
+    return (int)(x < longer ? kv4_div(x, size + 1) : rest + kv4_div(x - longer, size));
   }
 };
 
 // Cut the line for this grid; `wk` receives the place where this CTA's part
 // begins (when it has one).  All threads of the CTA; s_sum has one entry a warp.
-template <int RT, int KB, bool kTiles, int kThreads>
+template <int RT, int KB, int KU, bool kTiles, int kThreads>
 __device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long long* s_sum, long long* s_found,
                                                  Kv4Walk& wk, int& bad) {
   constexpr int kWarps = kThreads / 32;
@@ -133,7 +149,7 @@ __device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long lo
   long long mine = 0, total = 0;  // work of request `tid`; of all
   for (int i = tid; i < p.R; i += kThreads) {
     const Kv4Request q = kv4_request<RT, KB, kTiles>(p, i);
-    const long long w = kv4_request_work(q, p.cache.Hkv);
+    const long long w = kv4_request_work<KU>(q, p.cache.Hkv);
     if (i == tid) mine = w;
     total += w;
     bad = max(bad, q.bad);
@@ -146,18 +162,20 @@ __device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long lo
   line.total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) line.total += s_sum[w];
-  // no part is empty: a unit's partial results then lie in consecutive CTAs
+  // no part is empty: a unit's blocks, and its partial results, then lie in consecutive CTAs
   line.cut = min((long long)gridDim.x, line.total);
   const bool idle = blockIdx.x >= line.cut;
-  line.begin = idle ? 0 : line.total * blockIdx.x / line.cut;
-  line.end = idle ? 0 : line.total * (blockIdx.x + 1) / line.cut;
+  line.size = idle ? 0 : kv4_div(line.total, line.cut);
+  line.rest = line.total - line.size * line.cut;
+  line.begin = idle ? 0 : line.size * blockIdx.x + min((long long)blockIdx.x, line.rest);
+  line.end = idle ? 0 : line.begin + line.size + (blockIdx.x < line.rest ? 1 : 0);
   wk.pos = line.begin;
   wk.base = 0;
   wk.r = 0;
   if (idle) return line;
   for (int r0 = 0; r0 < p.R; r0 += kThreads) {
     const long long w = r0 == 0           ? mine
-                        : r0 + tid < p.R ? kv4_request_work(kv4_request<RT, KB, kTiles>(p, r0 + tid), p.cache.Hkv)
+                        : r0 + tid < p.R ? kv4_request_work<KU>(kv4_request<RT, KB, kTiles>(p, r0 + tid), p.cache.Hkv)
                                          : 0;
     long long x = w;
 #pragma unroll
