@@ -17,6 +17,7 @@ constexpr int kKv4Tile = 16;               // tokens of one tile
 constexpr int kKv4Group = 16;              // elements sharing one scale
 constexpr float kKv4MaxScale = 10240.f;    // largest scale: 6 * 10240 is finite in fp16
 constexpr int kKv4NanScale = 0xff;         // scale byte of a group with a non-finite element
+constexpr int kKv4MaxLength = 1 << 30;     // cached tokens of a request (positions a few tiles on still fit 32 bits)
 constexpr int kKv4MaxRequests = 4096;      // kv4_tables keeps per-request prefix sums in shared memory
 
 // One tile: K codes (8 D bytes), K scales (D), V codes (8 D), V scales (D).
@@ -161,7 +162,8 @@ struct Kv4AttnShape {
   int rows, ctas;
   size_t slot_floats;
 };
-constexpr int kKv4MaxSms = 160;  // workspaces are sized for this many SMs
+constexpr int kKv4MaxSms = 160;            // workspaces are sized for this many SMs
+constexpr int kKv4MaxCtas = 4 * kKv4MaxSms;  // and at most four CTAs on each
 Kv4AttnShape kv4_attn_shape(int D, long long rows, int sms);
 // The tile kernel (kv4_tile.cu): one CTA an SM, head_dim 64 and 128.
 constexpr size_t kv4_tile_slot_floats(int D) { return 256 * ((size_t)D + 2); }

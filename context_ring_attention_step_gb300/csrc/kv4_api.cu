@@ -88,16 +88,15 @@ cudaError_t sm_count(int* sms) {
 struct AttnLayout {
   size_t tickets, partials, total;
 };
+// The counters lie in the same place for every variant, so that one workspace
+// serves calls of different kinds in turn.
 AttnLayout attn_layout(int32_t D, int32_t G, int32_t max_q_len) {
   const ra::Kv4AttnShape s = ra::kv4_attn_shape(D, few_rows(D, G, max_q_len), ra::kKv4MaxSms);
-  size_t ctas = s.ctas, floats = (size_t)s.ctas * 2 * s.slot_floats;
-  if (has_tiles(D, G, max_q_len)) {
-    ctas = std::max(ctas, (size_t)ra::kKv4MaxSms);
-    floats = std::max(floats, (size_t)ra::kKv4MaxSms * 2 * ra::kv4_tile_slot_floats(D));
-  }
+  size_t floats = (size_t)s.ctas * 2 * s.slot_floats;
+  if (has_tiles(D, G, max_q_len)) floats = std::max(floats, (size_t)ra::kKv4MaxSms * 2 * ra::kv4_tile_slot_floats(D));
   AttnLayout l;
   l.tickets = kHeader;
-  l.partials = align256(l.tickets + 3 * ctas * sizeof(int32_t));
+  l.partials = align256(l.tickets + 3 * (size_t)ra::kKv4MaxCtas * sizeof(int32_t));
   l.total = align256(l.partials + floats * sizeof(float));
   return l;
 }
@@ -218,6 +217,8 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
   if (rs != RA_OK) return rs;
   if (num_q_tokens < 0 || num_requests < 0)
     return fail(RA_ERR_INVALID_ARG, "num_q_tokens %d, num_requests %d must not be negative", num_q_tokens, num_requests);
+  if ((int64_t)num_q_tokens * num_q_heads > (int64_t(1) << 30))
+    return fail(RA_ERR_INVALID_ARG, "%d query tokens of %d heads: more than 2^30 rows in one call", num_q_tokens, num_q_heads);
   if (table_width < 1 || table_stride < table_width)
     return fail(RA_ERR_INVALID_ARG, "table_width %d, table_stride %lld: need 1 <= width <= stride", table_width,
                 (long long)table_stride);

@@ -321,7 +321,7 @@ __device__ __forceinline__ void add_nan(Acc<D, NT>& acc, uint32_t nan0, uint32_t
 // (accumulators and query operands 48 NT D / 128 a thread, two tiles 36 D / 128,
 // and about 40 more): 128 registers at four CTAs, 168 at three, 255 at two.
 __host__ __device__ constexpr int ctas_per_sm(int D, int NT) {
-  return D == 64 ? (NT < 3 ? 4 : 3) : D == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : 2;
+  return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 && NT == 1 ? 3 : 2;
 }
 
 template <int D, int NT>
@@ -331,7 +331,8 @@ struct AttnCfg {
   static constexpr int kFrag = NT * (D / 16);       // float4 accumulators of a lane
   static constexpr int kMerge = (kWarps / 2) * kFrag * 512;
   static constexpr int kFit = ((220 / kPerSm - 2) * 1024 - kMerge) / (kWarps * Kv4Layout<D>::kBytes);
-  static constexpr int kSlots = kFit > 6 ? 6 : kFit;  // ring of each warp
+  static constexpr int kMost = D == 64 ? 6 : D == 128 ? 4 : 3;
+  static constexpr int kSlots = kFit > kMost ? kMost : kFit;  // ring of each warp
   static constexpr int kSmem = kSlots * kWarps * Kv4Layout<D>::kBytes + kMerge;
   static_assert(kSlots >= 3, "tiles under way");
   static constexpr int kSlot = (kFrag + NT) * 128;  // floats of a partial result

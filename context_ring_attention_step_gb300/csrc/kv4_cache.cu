@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
   auto counts = [&](int r, int32_t& len) {
     len = p.kv_lens[r];
     const int32_t nw = p.new_lens[r];
-    const long long cap = (long long)p.table_width * P;
+    const long long cap = min((long long)p.table_width * P, (long long)kKv4MaxLength);
     Counts c{0, 0, 0};
     if (len < 0 || nw < -1 || (long long)len + max(nw, 0) > cap) {
       bad = RA_KV4_BAD_LENGTH;

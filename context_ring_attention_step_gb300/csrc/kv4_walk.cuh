@@ -58,15 +58,14 @@ __device__ __forceinline__ Kv4Request kv4_request(const Kv4AttnParams& p, int r)
   int b = p.cu_q[r], e = p.cu_q[r + 1];
   int L = p.kv_lens[r];
   q.bad = 0;
-  if (b < 0 || e < b || e > p.Tq) {
+  if (b < 0 || e < b || e > p.Tq) {  // the request has no rows
     q.bad = RA_KV4_BAD_OFFSET;
-    b = min(max(b, 0), p.Tq);
-    e = min(max(e, b), p.Tq);
+    b = e = 0;
   }
-  const long long cap = (long long)p.table_width << p.cache.page_shift;
-  if (L < 0 || L > cap) {
+  const long long cap = min((long long)p.table_width << p.cache.page_shift, (long long)kKv4MaxLength);
+  if (L < 0 || L > cap) {  // its rows see no key
     q.bad = RA_KV4_BAD_LENGTH;
-    L = L < 0 ? 0 : (int)cap;
+    L = 0;
   }
   q.b = b;
   q.n = e - b;

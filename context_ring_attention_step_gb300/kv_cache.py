@@ -216,8 +216,9 @@ def kv4_load(cache, slot_map, out=None):
 
 
 def kv4_attention_workspace(cache, num_q_tokens, num_q_heads, max_q_len=None):
-    """Workspace for ``kv4_attention`` calls with up to ``max_q_len`` query tokens a request
-    (default: ``num_q_tokens``).  Calls that may overlap need one each."""
+    """Workspace (zeroed, as its first use needs it) for ``kv4_attention`` calls with up to
+    ``max_q_len`` query tokens a request (default: ``num_q_tokens``).  Calls that may overlap
+    need one each; calls in turn may share one that is large enough for all of them."""
     lib = _ra.load_library()
     n = ctypes.c_size_t()
     longest = max(1, int(num_q_tokens if max_q_len is None else max_q_len))

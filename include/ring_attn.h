@@ -425,7 +425,7 @@ ra_status ra_noalloc_status(void* stream);
  *
  * All lengths, tables and maps are device memory and are read by the kernels,
  * so a captured step replays with new contents; no call allocates or waits
- * (ra_kv4_status does wait).  What a kernel finds wrong in them it refuses
+ * (ra_kv4_status does wait).  A request has at most 2^30 cached tokens.  What a kernel finds wrong in them it refuses
  * without reading or writing out of bounds, and says so in a status word.
  */
 typedef struct ra_kv4_cache {
@@ -440,7 +440,7 @@ typedef struct ra_kv4_cache {
 /* Status words of the calls below. */
 typedef enum {
   RA_KV4_BAD_PAGE = 1001,        /* a block table entry is not a page of the cache */
-  RA_KV4_BAD_LENGTH = 1002,      /* a length is negative or passes the block table's row */
+  RA_KV4_BAD_LENGTH = 1002,      /* a length is negative, or passes the block table's row or 2^30 */
   RA_KV4_BAD_OFFSET = 1003,      /* query offsets fall or pass the number of query tokens */
   RA_KV4_TOO_MANY_TOKENS = 1004, /* more new tokens than slots */
   RA_KV4_NO_PAGES = 1005,        /* not enough free pages */
@@ -522,9 +522,11 @@ ra_status ra_kv4_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_h
  * A row that sees no key gets o = 0 and lse = -inf.  Rows outside
  * [cu_q[0], cu_q[R]) are left as they were.  The workspace (device, 256-byte
  * aligned) must be zero before its first use (a call leaves it ready for the
- * next) and must not be shared by calls that may overlap; its first word is the
- * status of the last call (ra_kv4_status): a page id outside the cache, a length
- * or an offset out of range is left out of the result and reported there.
+ * next, of whatever shape, if it is large enough for it) and must not be shared
+ * by calls that may overlap.  Its first word is the status of the last call
+ * (ra_kv4_status): keys on a page outside the cache are left out, a request
+ * with a length out of range sees no key, one with offsets out of range has no
+ * rows, and the status says so.  num_q_tokens * num_q_heads <= 2^30.
  */
 ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_stride, int32_t num_q_tokens,
                            int32_t num_q_heads, const int32_t* block_table, int32_t table_width, int64_t table_stride,

@@ -450,6 +450,10 @@ def test_refused_contents_are_reported_and_stay_in_bounds(ra, longest):
         x = c.lens_t.clone()
         x[1] = bad
         refused("length|page", lens=x)
+    x = c.lens_t.clone()
+    x[1] = -5
+    o = refused("length", lens=x)
+    assert torch.equal(o[0], good[0]) and o[1].eq(0).all() and torch.equal(o[2], good[2])
     for cu in ([0, 1, 2, 4], [0, 2, 1, 3], [-1, 1, 2, 3], [0, 1, 2, 2 ** 31 - 1]):
         refused("offsets", cu=torch.tensor(cu, dtype=torch.int32).cuda())
 
@@ -516,6 +520,21 @@ def test_other_streams_and_two_workspaces(ra):
     for c, (o, lse) in zip((a, b), outs):
         want, wl = O.attention(f64(c.q), c.keys, c.values, c.lens, c.cu, True, 1 / math.sqrt(128))
         c.compare(f64(o), f64(lse), want, wl, 1 / math.sqrt(128), True)
+
+
+def test_one_workspace_for_calls_of_different_kinds(ra):
+    """Its counters are ready for the next call whatever the one before was."""
+    ws = ra.kv4_attention_workspace(Case(ra, 1, [5], [1], 8, 1, 128, 16).cache, 200, 8, 200)
+    cases = [(Case(ra, 81, [3000, 40], [1, 1], 8, 1, 128, 32), 1), (Case(ra, 82, [900, 500], [100, 2], 8, 1, 128, 32), 100),
+             (Case(ra, 83, [2500], [1], 2, 1, 64, 16), 1), (Case(ra, 84, [1800, 90], [3, 1], 8, 1, 128, 64), 3),
+             (Case(ra, 85, [4000], [1], 4, 2, 256, 64), 1), (Case(ra, 86, [700], [130], 1, 1, 64, 16), 130)]
+    for _ in range(2):
+        for c, longest in cases:
+            sc = 1 / math.sqrt(c.d)
+            o, lse = ra.kv4_attention(c.q.cuda(), c.cache, c.table, c.lens_t, c.cu_t, o_fp32=True, max_q_len=longest,
+                                      workspace=ws, check=True)
+            want, wl = O.attention(f64(c.q), c.keys, c.values, c.lens, c.cu, True, sc)
+            c.compare(f64(o), f64(lse), want, wl, sc, True)
 
 
 def test_results_repeat(ra):

@@ -138,6 +138,7 @@ def test_attention_refusals(ra):
         assert call(**{name: 0}) == 1, name
         assert call(**{name: 4098}) == 1, name
     assert call(q=4104) == 1 and call(qs=4095 * 1) == 1 and call(qs=4100) == 1
+    assert call(T=(1 << 25) + 1) == 1 and call(T=2 ** 31 - 1) == 1
 
 
 def test_python_checks(ra):
