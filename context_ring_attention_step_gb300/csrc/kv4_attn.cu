@@ -22,13 +22,24 @@
 //     (half a step: 2^-12); its reference keeps the row's largest P between 2^6
 //     and 2^15, so that keys down to 2^-20 of the largest keep all 11 bits;
 //   * a tile's bytes lie in the order of the operand registers: a lane's share
-//     is whole 16-byte words, loaded straight into registers;
+//     is whole 16-byte words.  Lanes copy them into a ring in shared memory
+//     (cp.async), a few tiles ahead, and read back only what they copied
+//     themselves: no barrier and no branch stands between a tile's expansions
+//     and its products, which the compiler mixes only inside one basic block;
 //   * the work of all requests, 64 keys at a time, is one line that the grid's
 //     CTAs cut into equal parts (lengths are on the device: the grid is fixed,
 //     and each CTA finds its part from the lengths).  A unit (request, row
 //     tile, head) that spans CTAs leaves partial results in the workspace, and
 //     the CTA that brings the last one merges them (in the CTAs' order, so the
 //     result does not depend on which one that is).
+// What bounds it: with long caches the steady state reads 4.7 TB/s (4 x 131072
+// tokens, 8 heads, head_dim 128: 604 MB in 128 us), where the conversions (ALU
+// pipe 52 % of all cycles, two cycles each) and the multiplications (half rate)
+// leave little more; expanding and multiplying a 16-token tile alone takes 155 ns
+// of each scheduler, 66 % of what it then takes in all.  A single 131072-token
+// request (151 MB, 22 us at the measured 6.78 TB/s) takes 43 us: about 7 us until
+// the first tiles are there, 25 to 30 of reading, 8 for the two merges.  128
+// ragged requests (579 MB): 117 us, 5.0 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -317,9 +328,10 @@ __device__ __forceinline__ void add_nan(Acc<D, NT>& acc, uint32_t nan0, uint32_t
   }
 }
 
-// CTAs of four warps per SM: as many as the registers of a variant allow
-// (accumulators and query operands 48 NT D / 128 a thread, two tiles 36 D / 128,
-// and about 40 more): 128 registers at four CTAs, 168 at three, 255 at two.
+// CTAs of four warps per SM: 128 registers a thread at four, 168 at three, 255 at
+// two.  More registers beat more warps as soon as the compiler can use them: at
+// head_dim 128 three CTAs take 126 us for 128 ragged requests, four 138, two 138;
+// at 16 query rows two take 65 us over 131072 tokens, three 77 (they spill).
 __host__ __device__ constexpr int ctas_per_sm(int D, int NT) {
   return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 && NT == 1 ? 3 : 2;
 }
