@@ -226,7 +226,9 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
 // rows move whole sectors.  Few rows go one at a time (Q = 1), to more threads.
 // Threads of a block walk (quad, column) pairs, columns first.
 struct Columns {
-  uint32_t n, magic;  // columns of a quad; x / n = umulhi(x, magic) for x < 2^32 / n
+  // columns of a quad; x / n = umulhi(x, magic) for the x < 256 of several quads a
+  // block (magic 0: one quad)
+  uint32_t n, magic;
 };
 
 // Slots of the quad's tokens, -1 where there is none; true if they are four
@@ -368,7 +370,7 @@ cudaError_t launch_rows(F by_one, F by_four, uint32_t columns, const Kv4RowsPara
   const int per_block = columns >= 256 ? 1 : 256 / columns;  // quads: about one column a thread
   const int64_t quads = four ? (p.T + 3) / 4 : p.T;
   const int64_t blocks = std::min<int64_t>((quads + per_block - 1) / per_block, 1 << 20);
-  const Columns col{columns, (uint32_t)((uint64_t(1) << 32) / columns + 1)};
+  const Columns col{columns, per_block > 1 ? (uint32_t)((uint64_t(1) << 32) / columns + 1) : 0};
   (four ? by_four : by_one)<<<(unsigned)blocks, 256, 0, stream>>>(p, col, per_block);
   return cudaGetLastError();
 }

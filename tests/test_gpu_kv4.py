@@ -114,6 +114,18 @@ def test_store_load_of_a_long_prompt(ra, d, T):
     assert torch.equal(ra.kv4_load(cache, some)[1], vo[5:5000:7])
 
 
+@pytest.mark.parametrize("H,d", [(4096, 256), (4096, 64), (37, 128)])
+def test_store_load_of_many_heads(ra, H, d):
+    """Rows of more columns than a block has threads."""
+    rng = np.random.default_rng(H + d)
+    cache = ra.Kv4Cache(2, 16, H, d)
+    k, v = bf16(rng, 5, H, d), bf16(rng, 5, H, d)
+    slots = torch.tensor([20, 21, 22, 23, 3]).cuda()
+    ra.kv4_store(cache, k.cuda(), v.cuda(), slots)
+    for got, x in zip(ra.kv4_load(cache, slots), (k, v)):
+        np.testing.assert_array_equal(f64(got), O.rounded(f64(x)))
+
+
 def test_store_leaves_other_slots(ra):
     rng = np.random.default_rng(5)
     cache = ra.Kv4Cache(3, 32, 2, 128)
