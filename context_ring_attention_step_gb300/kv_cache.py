@@ -62,10 +62,18 @@ def _library():
     return _ra._lib or _ra.load_library()
 
 
+_I32, _I64, _BF16, _F32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
+_current_device = torch._C._cuda_getDevice
+
+
+def _library():
+    return _ra._lib or _ra.load_library()
+
+
 def _launch(device, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device current."""
     i = device.index
-    if torch._C._cuda_getDevice() == i:
+    if _current_device() == i:
         status = fn(*args, _current_raw_stream(i))
     else:
         with torch.cuda.device(i):
@@ -80,22 +88,25 @@ def _on_gpu(name, device):
 
 
 def _array(name, t, shape, dtype, device):
-    """Pointer of a contiguous tensor with exactly this shape, type and device."""
+    """Pointer of a contiguous tensor with exactly this shape, type and device.
+
+    (One expression for the common case: a step makes a dozen of these checks,
+    and they are most of its host time.)"""
+    if t.dtype is dtype and t.get_device() == device.index and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _rows(name, t, heads, dim, device):
     """(pointer, row stride) of a [T, heads, dim] bf16 tensor whose rows are dense."""
-    if t.dtype is not torch.bfloat16:
-        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, torch.bfloat16))
+    if t.dtype is not _BF16:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, _BF16))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     shape = t.shape
@@ -114,7 +125,7 @@ def _table(block_table, num_requests, device):
     shape = block_table.shape
     if len(shape) != 2 or shape[0] != num_requests:
         raise ValueError("block_table has shape %s, expected [%d, pages]" % (tuple(shape), num_requests))
-    if block_table.dtype is not torch.int32 or block_table.device != device:
+    if block_table.dtype is not _I32 or block_table.device != device:
         raise ValueError("block_table must be an int32 tensor on %s" % device)
     w = shape[1]
     s = block_table.stride()
@@ -150,8 +161,9 @@ def kv4_tables(kv_lens, new_lens, block_table, page_size, num_slots, free_pages=
     num_slots = int(num_slots)
     if out is None:
         out = kv4_tables_out(R, num_slots, dev)
-    lens = _array("kv_lens", kv_lens, (R,), torch.int32, dev)
-    new = _array("new_lens", new_lens, (R,), torch.int32, dev)
+    per_r, one = (R,), (1,)
+    lens = _array("kv_lens", kv_lens, per_r, _I32, dev)
+    new = _array("new_lens", new_lens, per_r, _I32, dev)
     table, width, stride = _table(block_table, R, dev)
     free = count = None
     num_pages = 0
@@ -159,15 +171,16 @@ def kv4_tables(kv_lens, new_lens, block_table, page_size, num_slots, free_pages=
         if free_count is None:
             raise ValueError("free_pages needs free_count")
         num_pages = free_pages.shape[0]
-        free = _array("free_pages", free_pages, (num_pages,), torch.int32, dev)
-        count = _array("free_count", free_count, (1,), torch.int32, dev)
+        free = _array("free_pages", free_pages, (num_pages,), _I32, dev)
+        count = _array("free_count", free_count, one, _I32, dev)
+    o_lens, o_cu, o_slots, o_pos, o_count, o_status = out
     _launch(dev, lib.ra_kv4_tables, lens, new, R, table, width, stride, int(page_size), free, num_pages, count,
-            num_slots, _array("out.kv_lens", out.kv_lens, (R,), torch.int32, dev),
-            _array("out.cu_new", out.cu_new, (R + 1,), torch.int32, dev),
-            _array("out.slot_map", out.slot_map, (num_slots,), torch.int64, dev),
-            _array("out.positions", out.positions, (num_slots,), torch.int32, dev),
-            _array("out.free_count", out.free_count, (1,), torch.int32, dev),
-            _array("out.status", out.status, (1,), torch.int32, dev))
+            num_slots, _array("out.kv_lens", o_lens, per_r, _I32, dev),
+            _array("out.cu_new", o_cu, (R + 1,), _I32, dev),
+            _array("out.slot_map", o_slots, (num_slots,), _I64, dev),
+            _array("out.positions", o_pos, (num_slots,), _I32, dev),
+            _array("out.free_count", o_count, one, _I32, dev),
+            _array("out.status", o_status, one, _I32, dev))
     if check:
         kv4_status(out.status)
     return out
@@ -187,7 +200,7 @@ def kv4_store(cache, k, v, slot_map, check=False):
     _on_gpu("cache", dev)
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("k, v and slot_map have %d, %d and %d rows" % (k.shape[0], v.shape[0], T))
-    slots = _array("slot_map", slot_map, (T,), torch.int64, dev)
+    slots = _array("slot_map", slot_map, (T,), _I64, dev)
     if check:
         used = slot_map[slot_map >= 0]
         if used.numel() and int(used.max()) >= cache.num_pages * cache.page_size:
@@ -206,12 +219,12 @@ def kv4_load(cache, slot_map, out=None):
     dev, T = cache.device, slot_map.shape[0]
     _on_gpu("cache", dev)
     shape = (T, cache.num_kv_heads, cache.head_dim)
-    slots = _array("slot_map", slot_map, (T,), torch.int64, dev)
+    slots = _array("slot_map", slot_map, (T,), _I64, dev)
     if out is None:
         out = (torch.empty(shape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev))
     k, v = out
-    _launch(dev, lib.ra_kv4_load, cache._ref, slots, T, _array("k", k, shape, torch.bfloat16, dev),
-            _array("v", v, shape, torch.bfloat16, dev))
+    _launch(dev, lib.ra_kv4_load, cache._ref, slots, T, _array("k", k, shape, _BF16, dev),
+            _array("v", v, shape, _BF16, dev))
     return k, v
 
 
@@ -248,8 +261,8 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None,
     T, Hq, D = q.shape
     qp, qs = _rows("q", q, Hq, cache.head_dim, dev)
     table, width, stride = _table(block_table, R, dev)
-    lens = _array("kv_lens", kv_lens, (R,), torch.int32, dev)
-    cu = _array("cu_q", cu_q, (R + 1,), torch.int32, dev)
+    lens = _array("kv_lens", kv_lens, (R,), _I32, dev)
+    cu = _array("cu_q", cu_q, (R + 1,), _I32, dev)
     ot = torch.float32 if o_fp32 else torch.bfloat16
     if out is None:
         o = torch.zeros((T, Hq, D), dtype=ot, device=dev)
@@ -263,7 +276,7 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None,
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     _launch(dev, lib.ra_kv4_attention, cache._ref, qp, qs, T, Hq, table, width, stride, lens, cu, R, longest,
             int(bool(causal)), float(scale) if scale else 0.0, _array("o", o, (T, Hq, D), ot, dev), int(bool(o_fp32)),
-            _array("lse", lse, (Hq, T), torch.float32, dev), workspace.data_ptr(),
+            _array("lse", lse, (Hq, T), _F32, dev), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
     if check:
         kv4_status(workspace)
