@@ -189,21 +189,20 @@ struct Acc {
 
 // Add the warps' accumulators up in warp 0: all take the rows' largest
 // reference, then half of those left hand theirs to the other half, until one is
-// left.  `sum_l`: l is still one sum per lane.  The buffers of the next call are
-// other ones (ml) or are written behind its first barrier (so).
+// left; l, one sum a lane before, becomes the row's.  The buffers of the next call
+// are other ones (ml) or are written behind its first barrier (so).
 template <int D, int NT>
-__device__ __forceinline__ void merge_warps(Acc<D, NT>& acc, float4 (&ml)[kWarps][NT][4], float4* so, int warp, int lane,
-                                            bool sum_l = true) {
+__device__ __forceinline__ void merge_warps(Acc<D, NT>& acc, float4 (&ml)[kWarps][NT][4], float4* so, int warp,
+                                            int lane) {
   constexpr int F = NT * (D / 16);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    if (sum_l)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 4);
-        acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 8);
-        acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 16);
-      }
+    for (int e = 0; e < 2; ++e) {
+      acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 4);
+      acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 8);
+      acc.l[nt][e] += __shfl_xor_sync(0xffffffffu, acc.l[nt][e], 16);
+    }
     if (lane < 4) ml[warp][nt][lane] = make_float4(acc.ref(nt, 0), acc.ref(nt, 1), acc.l[nt][0], acc.l[nt][1]);
   }
   __syncthreads();
@@ -591,48 +590,26 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
     if (direct) {
       if (warp == 0) write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
     } else {
-      // A partial result.  Of every kFan neighbours the CTA that brings the last one
-      // merges them into the first one's slot, and of a unit's merged ones the CTA
-      // that brings the last one merges those.
+      // A partial result; the CTA that brings the last one merges them.
       const int c0 = line.owner(wk.first), parts = line.owner(wk.first + rq.blocks - 1) - c0 + 1;
       auto place = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };
       auto slot = [&](int i) { return reinterpret_cast<float4*>(p.partials + (size_t)place(c0 + i) * C::kSlot); };
-      int at = blockIdx.x - c0, from = at / kFan * kFan, count = min(kFan, parts - from), stride = 1;
-      int* ticket = p.tickets + place(c0 + from);
-      // A unit in few parts is warp 0's business alone; the others go on meanwhile.
-      const bool all = parts > kAlone;
-#pragma unroll 1
-      while (all || warp == 0) {
-        bool is_last = false;
-        if (warp == 0) {
-          float4* dst = slot(at);
+      const int at = blockIdx.x - c0;
+      if (warp == 0) {
+        float4* dst = slot(at);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            dst[32 * nt + lane] = make_float4(acc.ref(nt, 0), acc.ref(nt, 1), acc.l[nt][0], acc.l[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          dst[32 * nt + lane] = make_float4(acc.ref(nt, 0), acc.ref(nt, 1), acc.l[nt][0], acc.l[nt][1]);
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d)
-              dst[32 * (NT + nt * (D / 16) + d) + lane] =
-                  make_float4(acc.o[nt][d][0], acc.o[nt][d][1], acc.o[nt][d][2], acc.o[nt][d][3]);
-          }
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) {
-            is_last = atomicAdd(ticket, 1) == count - 1;
-            if (is_last) *ticket = 0;  // as the next call expects it
-            s_last = is_last;
-          }
-          is_last = __shfl_sync(0xffffffffu, is_last, 0);
+          for (int d = 0; d < D / 16; ++d)
+            dst[32 * (NT + nt * (D / 16) + d) + lane] =
+                make_float4(acc.o[nt][d][0], acc.o[nt][d][1], acc.o[nt][d][2], acc.o[nt][d][3]);
         }
-        if (all) {
-          __syncthreads();
-          is_last = s_last;
-        }
-        if (!is_last) break;
         __threadfence();
-        acc.clear();
-        // the rows' largest reference first: the weights, and with them all loads
-        // of the partial results, then depend on nothing
-        float mm[NT][2];
+        __syncwarp();
+      }
+      // the rows' largest reference over `count` partial results, `stride` apart
+      auto largest = [&](float (&mm)[NT][2], int from, int count, int stride) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mm[nt][0] = mm[nt][1] = neg_inf();
@@ -641,52 +618,135 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
             mm[nt][0] = fmaxf(mm[nt][0], ml.x);
             mm[nt][1] = fmaxf(mm[nt][1], ml.y);
           }
-        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mm[nt][e] = fmaxf(mm[nt][e], __shfl_xor_sync(0xffffffffu, mm[nt][e], d));
-            if (mm[nt][e] != neg_inf()) {
-              acc.m[nt][e] = mm[nt][e];
-              acc.top[nt][e] = kMaxExp;
+        }
+      };
+      auto weight = [](float m, float mm) { return m == neg_inf() ? 0.f : ex2_approx(m - mm); };
+      if (parts <= kAlone) {
+        // few parts: warp 0's business alone; the others go on meanwhile
+        bool is_last = false;
+        if (warp == 0 && lane == 0) {
+          int* ticket = p.tickets + place(c0);
+          is_last = atomicAdd(ticket, 1) == parts - 1;
+          if (is_last) *ticket = 0;  // as the next call expects it
+        }
+        if (__shfl_sync(0xffffffffu, is_last, 0)) {
+          __threadfence();
+          float mm[NT][2];
+          largest(mm, 0, parts, 1);
+          acc.clear();
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (mm[nt][e] != neg_inf()) {
+                acc.m[nt][e] = mm[nt][e];
+                acc.top[nt][e] = kMaxExp;
+              }
+#pragma unroll 1
+          for (int i = 0; i < parts; ++i) {
+            const float4* src = slot(i);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float4 ml = __ldcg(src + 32 * nt + lane);
+              const float w0 = weight(ml.x, mm[nt][0]), w1 = weight(ml.y, mm[nt][1]);
+              acc.l[nt][0] = fmaf(ml.z, w0, acc.l[nt][0]);
+              acc.l[nt][1] = fmaf(ml.w, w1, acc.l[nt][1]);
+#pragma unroll
+              for (int d = 0; d < D / 16; ++d) {
+                const float4 x = __ldcg(src + 32 * (NT + nt * (D / 16) + d) + lane);
+                acc.o[nt][d][0] = fmaf(x.x, w0, acc.o[nt][d][0]);
+                acc.o[nt][d][1] = fmaf(x.y, w1, acc.o[nt][d][1]);
+                acc.o[nt][d][2] = fmaf(x.z, w0, acc.o[nt][d][2]);
+                acc.o[nt][d][3] = fmaf(x.w, w1, acc.o[nt][d][3]);
+              }
             }
           }
-#pragma unroll 2
-        for (int i = warp; i < count; i += all ? kWarps : 1) {
-          const float4* src = slot(from + i * stride);
+          write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
+        }
+      } else {
+        // many: by neighbours of kFan, then those; each warp takes a quarter of the columns
+        constexpr int DW = D / 64;
+        int from = at / kFan * kFan, count = min(kFan, parts - from), stride = 1;
+        int* ticket = p.tickets + place(c0 + from);
+#pragma unroll 1
+        for (;;) {
+          __syncthreads();  // the slot is written (and s_last was read)
+          if (tid == 0) {
+            s_last = atomicAdd(ticket, 1) == count - 1;
+            if (s_last) *ticket = 0;
+          }
+          __syncthreads();
+          if (!s_last) break;
+          __threadfence();
+          float mm[NT][2], l[NT][2];
+          largest(mm, from, count, stride);
+          float4 o[NT][DW];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (8 * nt + 2 * c4 >= rows) continue;  // rows that nobody asks for
-            const float4 ml = __ldcg(src + 32 * nt + lane);
-            const float w0 = ml.x == neg_inf() ? 0.f : ex2_approx(ml.x - mm[nt][0]);
-            const float w1 = ml.y == neg_inf() ? 0.f : ex2_approx(ml.y - mm[nt][1]);
-            acc.l[nt][0] = fmaf(ml.z, w0, acc.l[nt][0]);
-            acc.l[nt][1] = fmaf(ml.w, w1, acc.l[nt][1]);
+            l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-              const float4 x = __ldcg(src + 32 * (NT + nt * (D / 16) + d) + lane);
-              acc.o[nt][d][0] = fmaf(x.x, w0, acc.o[nt][d][0]);
-              acc.o[nt][d][1] = fmaf(x.y, w1, acc.o[nt][d][1]);
-              acc.o[nt][d][2] = fmaf(x.z, w0, acc.o[nt][d][2]);
-              acc.o[nt][d][3] = fmaf(x.w, w1, acc.o[nt][d][3]);
+            for (int d = 0; d < DW; ++d) o[nt][d] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll 8
+          for (int i = 0; i < count; ++i) {
+            const float4* src = slot(from + i * stride);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float4 ml = __ldcg(src + 32 * nt + lane);
+              const float w0 = weight(ml.x, mm[nt][0]), w1 = weight(ml.y, mm[nt][1]);
+              l[nt][0] = fmaf(ml.z, w0, l[nt][0]);
+              l[nt][1] = fmaf(ml.w, w1, l[nt][1]);
+#pragma unroll
+              for (int d = 0; d < DW; ++d) {
+                const float4 x = __ldcg(src + 32 * (NT + nt * (D / 16) + warp * DW + d) + lane);
+                o[nt][d].x = fmaf(x.x, w0, o[nt][d].x);
+                o[nt][d].y = fmaf(x.y, w1, o[nt][d].y);
+                o[nt][d].z = fmaf(x.z, w0, o[nt][d].z);
+                o[nt][d].w = fmaf(x.w, w1, o[nt][d].w);
+              }
             }
           }
+          if (stride > 1 || parts <= kFan) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int row = 8 * nt + 2 * c4 + e;
+                if (row >= rows) continue;
+                const int token = rq.b + (row0 + row) / G, h = head * G + (row0 + row) % G;
+                const float sum = l[nt][e], inv = sum == 0.f ? 0.f : 1.f / sum;
+                const size_t off = ((size_t)token * p.Hq + h) * D + r8 * (D / 8) + 2 * warp * DW;
+#pragma unroll
+                for (int d = 0; d < DW; ++d) {
+                  const float x = (e ? o[nt][d].y : o[nt][d].x) * inv, y = (e ? o[nt][d].w : o[nt][d].z) * inv;
+                  if (p.o_is_fp32)
+                    *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.o) + off + 2 * d) = make_float2(x, y);
+                  else
+                    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.o) + off + 2 * d) = pack_bf16x2(x, y);
+                }
+                if (warp == 0 && r8 == 0)
+                  p.lse[(size_t)h * p.Tq + token] = sum == 0.f ? neg_inf() : (mm[nt][e] + log2f(sum)) * kLn2;
+              }
+            break;
+          }
+          float4* dst = slot(from);  // (read above by other warps too: they are done behind the barrier)
+          __syncthreads();
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (warp == 0) dst[32 * nt + lane] = make_float4(mm[nt][0], mm[nt][1], l[nt][0], l[nt][1]);
+#pragma unroll
+            for (int d = 0; d < DW; ++d) dst[32 * (NT + nt * (D / 16) + warp * DW + d) + lane] = o[nt][d];
+          }
+          __threadfence();
+          from = 0;
+          count = (parts + kFan - 1) / kFan;
+          stride = kFan;
+          ticket = p.tickets + 2 * gridDim.x + c0;
         }
-        if (all) {
-          merge_warps<D, NT>(acc, s_ml[units & 1], s_o, warp, lane, false);
-          ++units;
-        }
-        if (stride > 1 || parts <= kFan) {
-          if (warp == 0) write_rows<D, NT>(p, acc, rq.b, head, row0, rows, G, lane);
-          break;
-        }
-        at = from;
-        from = 0;
-        count = (parts + kFan - 1) / kFan;
-        stride = kFan;
-        ticket = p.tickets + 2 * gridDim.x + c0;
       }
     }
     wk.leave(line.end);
