@@ -165,7 +165,7 @@ struct Kv4AttnShape {
 constexpr int kKv4MaxSms = 160;            // workspaces are sized for this many SMs
 constexpr int kKv4MaxCtas = 4 * kKv4MaxSms;  // and at most four CTAs on each
 Kv4AttnShape kv4_attn_shape(int D, long long rows, int sms);
-// The tile kernel (kv4_tile.cu): one CTA an SM, head_dim 64 and 128.
+// The tile kernel (kv4_tile.cu): one CTA an SM.
 constexpr size_t kv4_tile_slot_floats(int D) { return 256 * ((size_t)D + 2); }
 cudaError_t launch_kv4_tile(int D, int ctas, const Kv4AttnParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_attn(int D, const Kv4AttnShape& shape, const Kv4AttnParams& p, cudaStream_t stream);

@@ -59,18 +59,18 @@ size_t page_bytes(int32_t page_size, int32_t Hkv, int32_t D) {
 
 // Requests with at least this many rows (tokens x heads of a group) go to the
 // tile kernel, where a call can have them.  Its time hardly depends on the rows
-// up to 128 a request, the other's grows with each 24 of them; over 131072
-// cached tokens (8 heads, head_dim 128 / 64) they take, in us, at
-//   64 rows  193 / 158 (tiles), 162 / 126 (few rows)
-//   96 rows  198 / 160 (tiles), 202 / 175 (few rows).
+// up to 128 a request, the other's grows with each 24 (head_dim 256: 8) of them;
+// over 131072 cached tokens in 8 requests (8 heads at head_dim 128 and 64, 2 at
+// 256) they take, in us, at
+//    64 rows  193 / 158 / 118 (tiles), 162 / 126 / 118 (few rows)
+//    96 rows  198 / 160       (tiles), 202 / 175       (few rows)
+//   128 rows              154 (tiles),             206 (few rows).
 constexpr int kTileMinRows = 96;
-bool has_tiles(int32_t D, int32_t G, int32_t max_q_len) {
-  return D <= 128 && (int64_t)G * max_q_len >= kTileMinRows;
-}
+bool has_tiles(int32_t G, int32_t max_q_len) { return (int64_t)G * max_q_len >= kTileMinRows; }
 // Rows that the other kernel's CTAs take: those of the longest request, or of
 // one token where the tile kernel takes the long ones.
-int64_t few_rows(int32_t D, int32_t G, int32_t max_q_len) {
-  return has_tiles(D, G, max_q_len) ? G : (int64_t)G * max_q_len;
+int64_t few_rows(int32_t G, int32_t max_q_len) {
+  return has_tiles(G, max_q_len) ? G : (int64_t)G * max_q_len;
 }
 
 // SMs of the current device (a property of the hardware: asked once).
@@ -91,9 +91,9 @@ struct AttnLayout {
 // The counters lie in the same place for every variant, so that one workspace
 // serves calls of different kinds in turn.
 AttnLayout attn_layout(int32_t D, int32_t G, int32_t max_q_len) {
-  const ra::Kv4AttnShape s = ra::kv4_attn_shape(D, few_rows(D, G, max_q_len), ra::kKv4MaxSms);
+  const ra::Kv4AttnShape s = ra::kv4_attn_shape(D, few_rows(G, max_q_len), ra::kKv4MaxSms);
   size_t floats = (size_t)s.ctas * 2 * s.slot_floats;
-  if (has_tiles(D, G, max_q_len)) floats = std::max(floats, (size_t)ra::kKv4MaxSms * 2 * ra::kv4_tile_slot_floats(D));
+  if (has_tiles(G, max_q_len)) floats = std::max(floats, (size_t)ra::kKv4MaxSms * 2 * ra::kv4_tile_slot_floats(D));
   AttnLayout l;
   l.tickets = kHeader;
   l.partials = align256(l.tickets + 3 * (size_t)ra::kKv4MaxCtas * sizeof(int32_t));
@@ -266,10 +266,10 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   const int32_t G = num_q_heads / Hkv;
-  const bool tiles = has_tiles(D, G, max_q_len);
+  const bool tiles = has_tiles(G, max_q_len);
   if (!tiles || num_requests > 1) {  // (a single long request is the tile kernel's, whatever its real length)
     p.split_rows = tiles ? kTileMinRows : 0;
-    e = ra::launch_kv4_attn(D, ra::kv4_attn_shape(D, few_rows(D, G, max_q_len), sms), p, st);
+    e = ra::launch_kv4_attn(D, ra::kv4_attn_shape(D, few_rows(G, max_q_len), sms), p, st);
     if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
     p.status_kept = 1;
   }

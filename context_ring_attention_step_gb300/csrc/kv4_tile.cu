@@ -18,6 +18,8 @@
 //   warps 4-11    softmax, output and merge of Q tile 0 (4-7) and 1 (8-11); a
 //                 thread is a row, and loads it: fp16 after a power of two
 //   warps 12-15   cache tiles -> fp16 K and V tiles in a ring of stages
+// At head_dim 256, whose O alone takes half of tensor memory, there is one Q tile;
+// warps 8-11 expand too.
 // Tensor memory (512 columns): S0 [0,128), S1 [128,256), O0, O1 behind them; P
 // (fp16) overwrites the first 64 columns of its S and feeds P.V from there.
 // Stages hold K(0), V(0), K(1), V(1), ...; both issuers release each of them.
@@ -34,9 +36,9 @@
 namespace ra {
 namespace {
 
-constexpr int kRows = 256;
 constexpr int kKeys = 128;
 constexpr int kThreads = 512;
+constexpr int kFan = 8;  // partial results merged at once
 constexpr int kUnit = 1;  // what beginning a unit costs, in blocks of 128 keys
 constexpr int kSegs = 8;  // segments (and key tiles) that the expanding warps may be ahead, rounded up
 // P's reference as in kv4_attn.cu: the row's largest P is in (2^6, 2^7] when it
@@ -52,9 +54,14 @@ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
 
 template <int D>
 struct TileCfg {
+  static constexpr int kQt = D == 256 ? 1 : 2;  // 128-row Q tiles (tensor memory: 128 + D columns each)
+  static constexpr int kRows = 128 * kQt;
+  static constexpr int kSoft = 4 * kQt;         // softmax warps, then the expanding ones
+  static constexpr int kExpand = 12 - kSoft;
+  static constexpr int kSubs = 8 / kExpand;     // cache tiles of a key tile that an expanding warp takes
   static constexpr int kTile = 128 * D * 2;  // bytes of one 128-row fp16 tile
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kQBytes = 2 * kTile;
+  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 5 : 8;
+  static constexpr int kQBytes = kQt * kTile;
   static constexpr int kBarOff = kQBytes + kStages * kTile;
   static constexpr int kSmem = kBarOff + 1024 + 1024;  // barriers and notes, alignment slack
   static constexpr int kSlot = kRows * (D + 2);        // floats of a partial result: m, l, O
@@ -70,7 +77,9 @@ struct Segment {
   int lim_lo[2];           // keys that the tile's first row sees
 };
 
+template <int kQt>
 __device__ __forceinline__ Segment segment(const Kv4AttnParams& p, const Kv4Walk& wk) {
+  constexpr int kRows = 128 * kQt;
   Segment s;
   const int G = p.Hq / p.cache.Hkv;
   s.k0 = wk.blk * kKeys;
@@ -87,9 +96,11 @@ __device__ __forceinline__ Segment segment(const Kv4AttnParams& p, const Kv4Walk
   return s;
 }
 
-// Barrier of the eight softmax warps / of the four expanding warps.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void expand_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+// Barrier of the softmax warps / of the expanding warps.
+template <int kWarps>
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+template <int kWarps>
+__device__ __forceinline__ void expand_sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -99,7 +110,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 template <int D>
 struct Words {
   uint4 w[D / 64];
-  uint32_t s;
+  uint32_t s, s1;  // scales (s1: the second word, head_dim 256)
 };
 template <int D>
 __device__ __forceinline__ void load_words(Words<D>& t, const uint8_t* tile, bool v, int lane) {
@@ -107,7 +118,11 @@ __device__ __forceinline__ void load_words(Words<D>& t, const uint8_t* tile, boo
 #pragma unroll
   for (int i = 0; i < D / 64; ++i)
     t.w[i] = __ldg(reinterpret_cast<const uint4*>(tile + (v ? L::kVCodes : L::kKCodes) + 512 * i + 16 * lane));
-  if (D == 64)
+  if (D == 256) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(tile + (v ? L::kVScales : L::kKScales)) + lane);
+    t.s = x.x;
+    t.s1 = x.y;
+  } else if (D == 64)
     t.s = v ? __ldg(reinterpret_cast<const uint32_t*>(tile + L::kVScales) + (lane >> 3) * 4 + (lane & 3))
             : __ldg(reinterpret_cast<const uint16_t*>(tile + L::kKScales) + lane);
   else
@@ -130,6 +145,8 @@ __device__ __forceinline__ void expand8(uint32_t addr, uint32_t codes, uint32_t 
 // The eight lanes of a shared-memory pass should touch eight different chunks.
 // At head_dim 128 they do not by themselves: lanes with c >= 2 write their K
 // chunks in another order (`turn`: 2 before 0), those with odd r their V chunks.
+// (At head_dim 256 they share banks, four lanes K and two V: the one Q tile's
+// products leave the time.)
 template <int D>
 struct Places {
   uint32_t k[D / 32], v[2][D / 64];
@@ -140,15 +157,15 @@ struct Places {
     v_turn = D == 128 && (r & 1);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const int ch = D == 64 ? 2 * c + i : 4 * (c & 1) + (k_turn ? i ^ 2 : i);
-      k[i] = (D == 64 ? 0 : (c >> 1) * 16384) + r * 128 + ((ch ^ r) << 4);
+      const int ch = D == 64 ? 2 * c + i : D == 256 ? i : 4 * (c & 1) + (k_turn ? i ^ 2 : i);
+      k[i] = (D == 64 ? 0 : D == 256 ? c * 16384 : (c >> 1) * 16384) + r * 128 + ((ch ^ r) << 4);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        const int row = 2 * c + e, ch = D == 64 ? r : 2 * (r & 3) + (v_turn ? i ^ 1 : i);
-        v[e][i] = (D == 64 ? 0 : (r >> 2) * 16384) + row * 128 + ((ch ^ row) << 4);
+        const int row = 2 * c + e, ch = D == 64 ? r : D == 256 ? 4 * (r & 1) + i : 2 * (r & 3) + (v_turn ? i ^ 1 : i);
+        v[e][i] = (D == 64 ? 0 : D == 256 ? (r >> 1) * 16384 : (r >> 2) * 16384) + row * 128 + ((ch ^ row) << 4);
       }
   }
 };
@@ -163,6 +180,13 @@ __device__ __forceinline__ void expand_k(uint32_t base, const Words<D>& t, const
       const uint32_t s = scale_both(t.s, h);
       expand8(base + pl.k[0] + 1024 * h, h ? t.w[0].z : t.w[0].x, s);
       expand8(base + pl.k[1] + 1024 * h, h ? t.w[0].w : t.w[0].y, s);
+    } else if (D == 256) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 w = t.w[(2 * h + (i >> 2)) % (D / 64)];
+        expand8(base + pl.k[i % (D / 32)] + 1024 * h, (i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w,
+                scale_both(h ? t.s1 : t.s, i >> 1));
+      }
     } else {
       const uint4 w = t.w[h % (D / 64)];
       const uint32_t s0 = scale_both(t.s, 2 * h), s1 = scale_both(t.s, 2 * h + 1);
@@ -182,6 +206,13 @@ __device__ __forceinline__ void expand_v(uint32_t base, const Words<D>& t, const
     const uint32_t s = scale_both(t.s, i);
     if (D == 64) {
       expand8(base + pl.v[e][0] + 1024 * h, i == 0 ? t.w[0].x : i == 1 ? t.w[0].y : i == 2 ? t.w[0].z : t.w[0].w, s);
+    } else if (D == 256) {
+      const uint4 w = t.w[i % (D / 64)];
+      const uint32_t s1 = scale_both(t.s1, i);
+      expand8(base + pl.v[e][0] + 1024 * h, w.x, s);
+      expand8(base + pl.v[e][1 % (D / 64)] + 1024 * h, w.y, s);
+      expand8(base + pl.v[e][2 % (D / 64)] + 1024 * h, w.z, s1);
+      expand8(base + pl.v[e][3 % (D / 64)] + 1024 * h, w.w, s1);
     } else {
       const uint4 w = t.w[h % (D / 64)];
       const uint32_t a = e ? w.z : w.x, b = e ? w.w : w.y;
@@ -209,7 +240,7 @@ __device__ __forceinline__ void write_cols(const Kv4AttnParams& p, size_t off, c
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnParams p) {
   using C = TileCfg<D>;
-  constexpr int S = C::kStages;
+  constexpr int S = C::kStages, kRows = C::kRows, kQt = C::kQt, kGroups = D / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(smem), sKV = sQ + C::kQBytes;
@@ -222,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   const uint32_t b_drain = smem_u32(bars + 6 + 2 * S);  // [2]
   // notes of the expanding warps: the first key of a segment with a NaN in a
   // group of V; the cache tiles of a key tile whose page is not one of the cache
-  int* s_nan = reinterpret_cast<int*>(bars + 8 + 2 * S);            // [kSegs][8]
-  uint8_t* s_dead = reinterpret_cast<uint8_t*>(s_nan + kSegs * 8);  // [kSegs][8]
+  int* s_nan = reinterpret_cast<int*>(bars + 8 + 2 * S);            // [kSegs][16]
+  uint8_t* s_dead = reinterpret_cast<uint8_t*>(s_nan + kSegs * 16);  // [kSegs][8]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_dead + kSegs * 8);
   int* s_int = reinterpret_cast<int*>(tmem_slot + 1);  // abort, bad, last
   __shared__ long long s_sum[kThreads / 32], s_found[2];
@@ -238,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       mbar_init(b_drain + 8 * i, 1);
     }
     for (int i = 0; i < S; ++i) {
-      mbar_init(b_full + 8 * i, 4);
-      mbar_init(b_empty + 8 * i, 2);
+      mbar_init(b_full + 8 * i, C::kExpand);
+      mbar_init(b_empty + 8 * i, kQt);
     }
     s_int[0] = s_int[1] = s_int[2] = 0;
     fence_mbar_init();
@@ -261,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   // Register split: 512 threads x 128 at launch = 128 x 40 + 256 x 184 + 128 x 104.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp < 2 && lane == 0) {
+    if (warp < kQt && lane == 0) {
       // ---------------------------------------------------------- MMA issuers
       const int qt = warp;
       const uint32_t tS = tmem + qt * 128, tO = tmem + 256 + qt * D;
@@ -282,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       };
       for (; wk.pos < line.end && ok;) {
         wk.enter<kRows, kKeys, kUnit, true>(p, line.end);
-        const Segment sg = segment(p, wk);
+        const Segment sg = segment<C::kQt>(p, wk);
         wk.leave(line.end);
         const int na = qt == 0 ? sg.na[0] : sg.na[1];
         if (sg.n == 0) continue;
@@ -325,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         mbar_wait_drain(b_drain + 8 * qt, 0);
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < 4 + C::kSoft) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ------------------------------------------------------------ softmax
     const int qt = (warp - 4) >> 2, row_t = tid - 128 * (1 + qt);  // row within the Q tile
@@ -341,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         wk.leave(line.end);
         continue;
       }
-      const Segment sg = segment(p, wk);
+      const Segment sg = segment<C::kQt>(p, wk);
       const int na = qt == 0 ? sg.na[0] : sg.na[1];
       const int na_other = qt == 0 ? sg.na[1] : sg.na[0];
       const int urow = 128 * qt + row_t, row = sg.row0 + urow;  // row of the unit, of the request
@@ -497,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       const int c0 = direct ? 0 : line.owner(wk.first);
       auto slot = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * C::kSlot; };
       const float inv = !direct ? 1.f : l_sum == 0.f ? 0.f : 1.f / l_sum;
-      const int* nan_key = s_nan + (seg & (kSegs - 1)) * 8;
+      const int* nan_key = s_nan + (seg & (kSegs - 1)) * 16;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -537,41 +568,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
           slot(blockIdx.x)[urow] = m_ref;
           slot(blockIdx.x)[kRows + urow] = l_sum;
         }
-        __threadfence();
-        softmax_sync();
+        // Of every kFan neighbours the CTA that brings the last one merges them into
+        // the first one's slot, and of those the CTA that brings the last one the unit.
         const int parts = line.owner(wk.first + wk.rq.blocks - 1) - c0 + 1;
-        if (tid == 128) s_int[2] = atomicAdd(&p.tickets[c0], 1) == parts - 1;
-        softmax_sync();
-        if (s_int[2]) {
+        int from = ((int)blockIdx.x - c0) / kFan * kFan, count = min(kFan, parts - from), stride = 1;
+        int* ticket = p.tickets + 2 * (c0 + from) + (from == 0 ? 1 : 0);
+#pragma unroll 1
+        for (;;) {
           __threadfence();
+          softmax_sync<C::kSoft>();
+          if (tid == 128) {
+            s_int[2] = atomicAdd(ticket, 1) == count - 1;
+            if (s_int[2]) *ticket = 0;  // as the next call expects it
+          }
+          softmax_sync<C::kSoft>();
+          if (!s_int[2]) break;
+          __threadfence();
+          const bool done = stride > 1 || parts <= kFan;
+          auto part = [&](int i) { return slot(c0 + from + i * stride); };
           // a thread a row: the rows' largest references and their sums, kept in the
           // Q tiles' shared memory (all products of the segment are done)
           float* s_ref = reinterpret_cast<float*>(smem);
           float* s_inv = s_ref + kRows;
           float mm = neg_inf(), l = 0.f;
 #pragma unroll 4
-          for (int i = 0; i < parts; ++i) mm = fmaxf(mm, __ldcg(slot(c0 + i) + urow));
+          for (int i = 0; i < count; ++i) mm = fmaxf(mm, __ldcg(part(i) + urow));
 #pragma unroll 4
-          for (int i = 0; i < parts; ++i) {
-            const float m = __ldcg(slot(c0 + i) + urow), li = __ldcg(slot(c0 + i) + kRows + urow);
+          for (int i = 0; i < count; ++i) {
+            const float m = __ldcg(part(i) + urow), li = __ldcg(part(i) + kRows + urow);
             l += m == neg_inf() ? 0.f : li * ex2_approx(m - mm);
           }
           s_ref[urow] = mm;
-          s_inv[urow] = l == 0.f ? 0.f : 1.f / l;
-          if (valid) p.lse[(size_t)h * p.Tq + token] = l == 0.f ? neg_inf() : (mm + log2f(l)) * kLn2;
-          softmax_sync();
+          s_inv[urow] = !done ? 1.f : l == 0.f ? 0.f : 1.f / l;
+          if (done && valid) p.lse[(size_t)h * p.Tq + token] = l == 0.f ? neg_inf() : (mm + log2f(l)) * kLn2;
+          softmax_sync<C::kSoft>();
           // a warp four rows at once: their weighted sums
           constexpr int V = D / 32, B = 4;
-          for (int r0 = warp - 4; r0 < sg.rows; r0 += 8 * B) {
+          for (int r0 = warp - 4; r0 < sg.rows; r0 += C::kSoft * B) {
             float acc[B][V] = {}, ref[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) ref[b] = s_ref[min(r0 + 8 * b, kRows - 1)];
+            for (int b = 0; b < B; ++b) ref[b] = s_ref[min(r0 + C::kSoft * b, kRows - 1)];
 #pragma unroll 2
-            for (int i = 0; i < parts; ++i) {
-              const float* s = slot(c0 + i);
+            for (int i = 0; i < count; ++i) {
+              const float* s = part(i);
 #pragma unroll
               for (int b = 0; b < B; ++b) {
-                const int rr = min(r0 + 8 * b, sg.rows - 1);
+                const int rr = min(r0 + C::kSoft * b, sg.rows - 1);
                 const float m = __ldcg(s + rr);
                 const float wgt = m == neg_inf() ? 0.f : ex2_approx(m - ref[b]);
 #pragma unroll
@@ -583,20 +625,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-              const int rr = r0 + 8 * b;
+              const int rr = r0 + C::kSoft * b;
               if (rr >= sg.rows) break;
               const int grow = sg.row0 + rr, tk = wk.rq.b + grow / G, hh = wk.head * G + grow % G;
 #pragma unroll
               for (int v = 0; v < V; ++v) {
                 const size_t off = ((size_t)tk * p.Hq + hh) * D + 32 * v + lane;
                 const float x = acc[b][v] * s_inv[rr];
-                if (p.o_is_fp32) reinterpret_cast<float*>(p.o)[off] = x;
+                if (!done) part(0)[2 * kRows + rr * D + 32 * v + lane] = x;  // (read by this warp only)
+                else if (p.o_is_fp32) reinterpret_cast<float*>(p.o)[off] = x;
                 else reinterpret_cast<__nv_bfloat16*>(p.o)[off] = __float2bfloat16_rn(x);
               }
             }
           }
-          softmax_sync();  // the Q tiles may be written again
-          if (tid == 128) p.tickets[c0] = 0;  // as the next call expects it
+          softmax_sync<C::kSoft>();  // the Q tiles, and the merged slot's m and l, may be written again
+          if (done) break;
+          if (valid) {
+            part(0)[urow] = mm;
+            part(0)[kRows + urow] = l;
+          }
+          from = 0;
+          count = (parts + kFan - 1) / kFan;
+          stride = kFan;
+          ticket = p.tickets + 2 * gridDim.x + c0;
         }
       }
       wk.leave(line.end);
@@ -608,38 +659,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ------------------------------------------------------------ expansion
     using L = Kv4Layout<D>;
-    const int dw = warp - 12;  // cache tiles 2 dw and 2 dw + 1 of every key tile
+    constexpr int kSubs = C::kSubs;
+    const int dw = warp - 4 - C::kSoft;  // cache tiles kSubs dw ... of every key tile
     const Places<D> places(lane);
     int issued = 0, seg = 0, tiles = 0;
     bool ok = true;
     for (; wk.pos < line.end;) {
       wk.enter<kRows, kKeys, kUnit, true>(p, line.end);
-      const Segment sg = segment(p, wk);
+      const Segment sg = segment<C::kQt>(p, wk);
       wk.leave(line.end);
       if (sg.n == 0) continue;
-      int* nan_key = s_nan + (seg & (kSegs - 1)) * 8;
-      if (dw == 0 && lane < 8) nan_key[lane] = 0x7fffffff;
-      expand_sync();
+      int* nan_key = s_nan + (seg & (kSegs - 1)) * 16;
+      if (dw == 0 && lane < kGroups) nan_key[lane] = 0x7fffffff;
+      expand_sync<C::kExpand>();
       const int32_t* table = p.block_table + (size_t)wk.r * p.table_stride;
       const uint8_t* base = p.cache.pages + ((size_t)wk.head << (p.cache.page_shift - 4)) * L::kBytes;
       const int tiles_mask = (1 << (p.cache.page_shift - 4)) - 1;
-      // lanes 0 and 1: page ids of this warp's two cache tiles of key tile j
+      // lanes u < kSubs: page ids of this warp's cache tiles of key tile j
       auto lane_page = [&](int j) -> int {
-        const int t = sg.k0 + kKeys * j + 16 * (2 * dw + lane);
-        return lane < 2 && j < sg.n && t < wk.t_end ? table[t >> p.cache.page_shift] : 0;
+        const int t = sg.k0 + kKeys * j + 16 * (kSubs * dw + lane);
+        return lane < kSubs && j < sg.n && t < wk.t_end ? table[t >> p.cache.page_shift] : 0;
       };
       // The words of a key tile are loaded as soon as the registers of the one
       // before are free: the way to memory is covered by a whole tile's products.
-      Words<D> k[2], v[2];
+      Words<D> k[kSubs], v[kSubs];
       uint32_t dead = 0;  // bit u: cache tile u of key tile j lies on a page that is not one of the cache
-      auto fetch = [&](Words<D> (&w)[2], bool is_v, int page, int j) {
+      auto fetch = [&](Words<D> (&w)[kSubs], bool is_v, int page, int j) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int t = sg.k0 + kKeys * j + 16 * (2 * dw + u);
+        for (int u = 0; u < kSubs; ++u) {
+          const int t = sg.k0 + kKeys * j + 16 * (kSubs * dw + u);
           const int pg = __shfl_sync(0xffffffffu, page, u);
           const bool in = j < sg.n && t < wk.t_end, good = (uint32_t)pg < (uint64_t)p.cache.num_pages;
           if (!is_v) dead = (dead & ~(1u << u)) | (in && !good ? 1u << u : 0u);
-          w[u].s = 0;
+          w[u].s = w[u].s1 = 0;
           if (in && good)
             load_words<D>(w[u], base + (int64_t)pg * p.page_bytes + ((t >> 4) & tiles_mask) * L::kBytes, is_v, lane);
         }
@@ -657,29 +709,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
           ok = __all_sync(0xffffffffu, ok);
           ++issued;
           if (!ok) continue;
-          const uint32_t dst = sKV + st * C::kTile + 4096 * dw;
+          const uint32_t dst = sKV + st * C::kTile + 2048 * kSubs * dw;
           if (kind == 0) {
             if (dead) bad = RA_KV4_BAD_PAGE;
-            if (lane < 2) s_dead[((tiles + j) & (kSegs - 1)) * 8 + 2 * dw + lane] = (dead >> lane) & 1;
+            if (lane < kSubs) s_dead[((tiles + j) & (kSegs - 1)) * 8 + kSubs * dw + lane] = (dead >> lane) & 1;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) expand_k<D>(dst + 2048 * u, k[u], places);
+            for (int u = 0; u < kSubs; ++u) expand_k<D>(dst + 2048 * u, k[u], places);
           } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kSubs; ++u) {
               // keys that no row sees, and NaN groups, count as zero; a row that
               // sees a key with a NaN gets it from the notes
-              const int c = lane & 3, g = D == 64 ? lane >> 3 : lane >> 2;
-              const int t0 = sg.k0 + kKeys * j + 16 * (2 * dw + u);
-              if (__vcmpgeu4(v[u].s, 0xf8f8f8f8u) || t0 + 16 > wk.t_end) {
+              const int t0 = sg.k0 + kKeys * j + 16 * (kSubs * dw + u);
+              auto clean = [&](uint32_t& sc, int g) {
+                if (!__vcmpgeu4(sc, 0xf8f8f8f8u) && t0 + 16 <= wk.t_end) return;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const int t = t0 + 2 * c + (i & 1) + 8 * (i >> 1);
-                  if (((v[u].s >> (8 * i)) & 0xffu) >= 0xf8u || t >= wk.t_end) {
+                  const int t = t0 + 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
+                  if (((sc >> (8 * i)) & 0xffu) >= 0xf8u || t >= wk.t_end) {
                     if (t < wk.t_end) atomicMin(&nan_key[g], t);
-                    v[u].s &= ~(0xffu << (8 * i));
+                    sc &= ~(0xffu << (8 * i));
                   }
                 }
-              }
+              };
+              clean(v[u].s, D == 64 ? lane >> 3 : D == 128 ? lane >> 2 : 2 * (lane >> 2));
+              if (D == 256) clean(v[u].s1, 2 * (lane >> 2) + 1);
               expand_v<D>(dst + 2048 * u, v[u], places);
             }
           }
@@ -719,6 +773,7 @@ cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
 cudaError_t launch_kv4_tile(int D, int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
   if (D == 64) return launch<64>(ctas, p, stream);
   if (D == 128) return launch<128>(ctas, p, stream);
+  if (D == 256) return launch<256>(ctas, p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -366,7 +366,8 @@ def test_prompt_parts_among_single_tokens(ra, d, Hq, Hkv, causal):
     c.check(ra, causal=causal, max_q_len=200, o_fp32=False, scale=0.2)
 
 
-@pytest.mark.parametrize("d,G,n,L", [(64, 2, 33, 3001), (128, 4, 16, 5000), (128, 1, 64, 2100), (128, 8, 129, 1111)])
+@pytest.mark.parametrize("d,G,n,L", [(64, 2, 33, 3001), (64, 2, 70, 3001), (128, 4, 16, 5000), (128, 4, 30, 5000),
+                                         (128, 1, 110, 2100), (128, 8, 129, 1111), (256, 4, 31, 2500), (256, 2, 90, 600)])
 def test_one_prompt_part_is_split(ra, d, G, n, L):
     c = Case(ra, n + L, [L], [n], G, 1, d, 32)
     c.check(ra, max_q_len=n)
@@ -413,14 +414,14 @@ def test_wide_ranges_of_q(ra):
 def test_nan_stays_in_its_rows(ra):
     """A NaN value or key of a late token reaches the rows that see it, and no other."""
     rng = np.random.default_rng(12)
-    for d, Hq in ((64, 2), (128, 4), (256, 2)):
-        L, n = 150, 40
+    for d, Hq, n in ((64, 2, 40), (128, 4, 20), (256, 2, 40), (64, 3, 40), (128, 4, 40), (256, 3, 40)):
+        L = 150                                                  # both kernels: fewer than 96 rows, and more
         k, v = bf16(rng, L, 1, d), bf16(rng, L, 1, d)
-        v[130, 0, 3] = float("nan")
-        v[131, 0, d - 1] = float("inf")
+        v[140, 0, 3] = float("nan")
+        v[141, 0, d - 1] = float("inf")
         c = Case(ra, d, [L], [n], Hq, 1, d, 16, keys=[k], values=[v])
         c.check(ra, max_q_len=n)
-        assert not np.isnan(f64(c.check(ra, max_q_len=n)[0])[:20]).any()
+        assert not np.isnan(f64(c.check(ra, max_q_len=n)[0])[:n - 10]).any()
         k[149, 0, 5] = float("nan")
         c = Case(ra, d, [L], [n], Hq, 1, d, 16, keys=[k], values=[v])
         c.check(ra, max_q_len=n)
