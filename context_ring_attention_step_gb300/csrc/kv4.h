@@ -81,19 +81,23 @@ __device__ __forceinline__ size_t kv4_tile_offset(const Kv4Cache& c, int64_t pag
   return (((size_t)page * c.Hkv + head) * tiles + (t >> 4)) * Kv4Layout<D>::kBytes;
 }
 
-// A kernel's dynamic shared memory limit, raised once on every device (the
-// attribute call costs about as much host time as a launch).  One per kernel.
+// Launches of a kernel whose dynamic shared memory limit has to be raised: once on
+// every device (the attribute call costs about as much host time as a launch),
+// and again if a launch is refused, as after a cudaDeviceReset.  One per kernel.
 struct Kv4SmemLimit {
   std::atomic<uint64_t> done{0};
-  cudaError_t raise(const void* kernel, int bytes) {
+  template <typename F>
+  cudaError_t launch(const void* kernel, int bytes, F launch_kernel) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const bool known = (done.load(std::memory_order_relaxed) & bit) != 0;
+    if (known && (e = launch_kernel()) != cudaErrorInvalidValue) return e;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return launch_kernel();
   }
 };
 

@@ -37,8 +37,8 @@
 // pipe 52 % of all cycles, two cycles each) and the multiplications (half rate)
 // leave little more; expanding and multiplying a 16-token tile alone takes 155 ns
 // of each scheduler, 66 % of what it then takes in all.  A single 131072-token
-// request (151 MB, 22 us at the measured 6.78 TB/s) takes 43 us: about 7 us until
-// the first tiles are there, 25 to 30 of reading, 8 for the two merges.  128
+// request (151 MB, 22 us at the measured 6.78 TB/s) takes 42 us: about 7 us until
+// the first tiles are there, 25 to 30 of reading, 6 for the two merges.  128
 // ragged requests (579 MB): 117 us, 5.0 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -761,10 +761,10 @@ cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
   using C = AttnCfg<D, NT>;
   auto kern = kv4_attn_kernel<D, NT>;
   static Kv4SmemLimit limit;
-  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), C::kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, C::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return limit.launch(reinterpret_cast<const void*>(kern), C::kSmem, [&] {
+    kern<<<ctas, kThreads, C::kSmem, stream>>>(p);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace

@@ -398,10 +398,9 @@ cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream) {
   attr[0].val.clusterDim.x = in_place ? cfg.gridDim.x : 1;
   if (small) return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<256>, p);
   static Kv4SmemLimit limit;
-  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kv4_tables_kernel<1024>),
-                                    (4 * kKv4MaxRequests + 3) * (int)sizeof(int32_t));
-  if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<1024>, p);
+  return limit.launch(reinterpret_cast<const void*>(kv4_tables_kernel<1024>),
+                      (4 * kKv4MaxRequests + 3) * (int)sizeof(int32_t),
+                      [&] { return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<1024>, p); });
 }
 
 cudaError_t launch_kv4_store(int D, const Kv4RowsParams& p, cudaStream_t stream) {

@@ -762,10 +762,10 @@ template <int D>
 cudaError_t launch(int ctas, const Kv4AttnParams& p, cudaStream_t stream) {
   auto kern = kv4_tile_kernel<D>;
   static Kv4SmemLimit limit;
-  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), TileCfg<D>::kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, TileCfg<D>::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return limit.launch(reinterpret_cast<const void*>(kern), TileCfg<D>::kSmem, [&] {
+    kern<<<ctas, kThreads, TileCfg<D>::kSmem, stream>>>(p);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace
