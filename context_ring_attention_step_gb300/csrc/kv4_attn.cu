@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
   __shared__ int s_bad, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r8 = lane >> 2, c4 = lane & 3;
-  const int G = p.Hq / p.cache.Hkv, Hkv = p.cache.Hkv;
+  const int G = p.Hq / p.cache.Hkv;
   uint8_t* ring = s_dyn + warp * S * L::kBytes;
   float4* s_o = reinterpret_cast<float4*>(s_dyn + kWarps * S * L::kBytes);  // [kWarps / 2][kFrag][32]
   if (tid == 0) s_bad = 0;

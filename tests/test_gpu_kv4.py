@@ -535,6 +535,46 @@ def test_other_streams_and_two_workspaces(ra):
         c.compare(f64(o), f64(lse), want, wl, 1 / math.sqrt(128), True)
 
 
+def test_sliced_block_table(ra):
+    """Rows further apart than they are long; rows without distance are refused."""
+    c = Case(ra, 91, [100, 60, 7], [1, 40, 2], 4, 1, 128, 16)
+    wide = torch.full((3, c.table.shape[1] + 9), 2 ** 30, dtype=torch.int32).cuda()
+    wide[:, 4:4 + c.table.shape[1]] = c.table
+    c.table = wide[:, 4:4 + c.table.shape[1]]
+    c.check(ra, max_q_len=40)
+    c.check(ra, max_q_len=1)
+    with pytest.raises(ra.RingAttnError, match="stride"):
+        ra.kv4_attention(c.q.cuda(), c.cache, c.table[:1].expand(3, -1), c.lens_t, c.cu_t)
+    with pytest.raises(ValueError, match="shape"):
+        ra.kv4_attention(c.q.cuda(), c.cache, c.table[:2], c.lens_t, c.cu_t)
+
+
+def test_captured_prompt_parts_follow_their_lengths(ra):
+    """One captured call over other lengths and offsets: what the row-tile kernel and the other one take changes."""
+    lens = [300, 500, 40]
+    a, b = Case(ra, 92, lens, [100, 1, 30], 4, 2, 128, 16), Case(ra, 93, lens, [3, 120, 8], 4, 2, 128, 16)
+    q, table, lens_t, cu = (t.clone() for t in (a.q.cuda(), a.table, a.lens_t, a.cu_t))
+    pages = a.cache.pages.clone()
+    out = torch.zeros(131, 4, 128).cuda(), torch.zeros(4, 131).cuda()
+    ws = ra.kv4_attention_workspace(a.cache, 131, 4, 131)
+    call = lambda: ra.kv4_attention(q, a.cache, table, lens_t, cu, o_fp32=True, max_q_len=131, workspace=ws, out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for c in (b, a, b):
+        q.copy_(c.q), table.copy_(c.table), lens_t.copy_(c.lens_t), cu.copy_(c.cu_t)
+        a.cache.pages.copy_(b.cache.pages if c is b else pages)
+        graph.replay()
+        ra.kv4_status(ws)
+        want, wl = O.attention(f64(c.q), c.keys, c.values, c.lens, c.cu, True, 1 / math.sqrt(128))
+        c.compare(f64(out[0]), f64(out[1]), want, wl, 1 / math.sqrt(128), True)
+
+
 def test_one_workspace_for_calls_of_different_kinds(ra):
     """Its counters are ready for the next call whatever the one before was."""
     ws = ra.kv4_attention_workspace(Case(ra, 1, [5], [1], 8, 1, 128, 16).cache, 200, 8, 200)
