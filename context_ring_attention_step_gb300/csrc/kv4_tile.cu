@@ -40,6 +40,7 @@ constexpr int kKeys = 128;
 constexpr int kThreads = 512;
 constexpr int kFan = 8;  // partial results merged at once
 constexpr int kUnit = 1;  // what beginning a unit costs, in blocks of 128 keys
+constexpr int kTurnLimit = 1 << 12;  // polls of a wait for the other Q tile's turn
 constexpr int kSegs = 8;  // segments (and key tiles) that the expanding warps may be ahead, rounded up
 // P's reference as in kv4_attn.cu: the row's largest P is in (2^6, 2^7] when it
 // moves.  A tile whose P's add up to no more than 2^15 needs no look at its maximum.
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   uint8_t* s_dead = reinterpret_cast<uint8_t*>(s_nan + kSegs * 16);  // [kSegs][8]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_dead + kSegs * 8);
   int* s_int = reinterpret_cast<int*>(tmem_slot + 1);  // abort, bad, last
+  volatile uint32_t* s_turns = reinterpret_cast<uint32_t*>(s_int + 3);  // [2] warps' P tiles of Q tile 0 / 1 so far
   __shared__ long long s_sum[kThreads / 32], s_found[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       mbar_init(b_empty + 8 * i, kQt);
     }
     s_int[0] = s_int[1] = s_int[2] = 0;
+    s_turns[0] = s_turns[1] = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -425,9 +428,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         tmem_ld32(tS + 64, r[2]);
         tmem_ld32(tS + 96, r[3]);
         // The two Q tiles take turns (0's tile j after 1's tile j - 1, 1's after 0's
-        // tile j), so that one's softmax runs beside the other's products.
+        // tile j), so that one's softmax runs beside the other's products.  A phase's
+        // parity cannot tell whether it is the other's turn: at a segment's first
+        // tile, and where a Q tile sees no key, nothing holds one back, so the other
+        // may be two phases behind or ahead.  The count of its P tiles decides, and
+        // the barrier only passes the time until the next one.  The order is for
+        // speed alone: a wait that takes too long is given up.
         const int k_other = j - (qt == 0 ? 1 : 0);
-        if (k_other >= 0 && k_other < na_other) mbar_wait(b_p + 8 * (1 - qt), (turns + k_other) & 1u, ab, 142);
+        if (k_other >= 0 && k_other < na_other) {
+          const uint32_t k = turns + k_other, want = 4 * (k + 1);
+          for (int n = 0; n < kTurnLimit && (int32_t)(s_turns[1 - qt] - want) < 0 && !*ab.flag; ++n)
+            mbar_try_wait(b_p + 8 * (1 - qt), k & 1u);
+          __syncwarp();
+        }
         const uint2 dead = *reinterpret_cast<const uint2*>(s_dead + ((tiles + j) & (kSegs - 1)) * 8);
         tmem_ld_wait();
         reg_fence32(r[0]); reg_fence32(r[1]); reg_fence32(r[2]); reg_fence32(r[3]);
@@ -513,7 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_p + 8 * qt);
+        if (lane == 0) {
+          atomicAdd(const_cast<uint32_t*>(s_turns) + qt, 1u);
+          mbar_arrive(b_p + 8 * qt);
+        }
         l_sum += tile_sum();
       }
       if (na > 0 && ok) {

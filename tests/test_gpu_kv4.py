@@ -678,3 +678,76 @@ def test_prompt_then_tokens_in_a_captured_step(ra):
             assert np.abs(f64(res[1][:, :n]) - wl).max() <= 1e-4
     used = [p for r in range(R) for p in table[r, :-(-len(hist_k[r]) // page)].tolist()]
     assert sorted(used + free[:int(count)].tolist()) == list(range(N))
+
+
+# ------------------------------------------------------------------ many units a CTA
+
+def by_heads(c, causal, scale):
+    """O.attention's formula, a head's rows at once (many rows)."""
+    T = c.cu[-1]
+    o, lse = np.zeros((T, c.Hq, c.d)), np.full((c.Hq, T), -np.inf)
+    q, G = f64(c.q), c.Hq // c.Hkv
+    for r, (L, n) in enumerate(zip(c.lens, c.qlens)):
+        if L == 0 or n == 0:
+            continue
+        b = slice(c.cu[r], c.cu[r + 1])
+        see = (L - n + 1 + np.arange(n)).clip(0, L) if causal else np.full(n, L)
+        hidden = np.arange(L)[None] >= see[:, None]
+        for h in range(c.Hq):
+            s = scale * (q[b, h] @ c.keys[r][:, h // G].T)
+            s[hidden] = -np.inf
+            m = s.max(-1, keepdims=True)
+            p = np.exp(s - np.where(np.isneginf(m), 0, m))
+            z = p.sum(-1, keepdims=True)
+            with np.errstate(divide="ignore"):
+                o[b, h] = (p / np.where(z == 0, 1, z)) @ c.values[r][:, h // G]
+                lse[h, b] = (m + np.log(z))[:, 0]
+    return o, lse
+
+
+def test_by_heads_is_the_same_formula(ra):
+    c = Case(ra, 5, [30, 0, 5, 64], [7, 2, 9, 64], 4, 2, 64, 16)
+    for causal in (True, False):
+        for a, b in zip(by_heads(c, causal, 0.2), O.attention(f64(c.q), c.keys, c.values, c.lens, c.cu, causal, 0.2)):
+            np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-13)
+
+
+def run_units(ra, c, longest, causal=True, o_fp32=True):
+    """Twice, with one workspace: the formula's values, bit by bit the same."""
+    sc = 1 / math.sqrt(c.d)
+    want, wl = by_heads(c, causal, sc)
+    q = c.q.cuda()
+    ws = ra.kv4_attention_workspace(c.cache, c.cu[-1], c.Hq, longest)
+    outs = [ra.kv4_attention(q, c.cache, c.table, c.lens_t, c.cu_t, causal=causal, o_fp32=o_fp32, max_q_len=longest,
+                             workspace=ws, check=True) for _ in range(2)]
+    c.compare(f64(outs[0][0]), f64(outs[0][1]), want, wl, sc, o_fp32)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+MIXED = [(40 + 45 * i, 40 + 45 * i if i % 3 == 0 else (1, 7, 130)[i % 3] if i % 2 else 33) for i in range(24)]
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", [
+    (128, 32, 32, [256] * 32, [256] * 32),                       # whole units of 1 and 2 key tiles
+    (128, 32, 8, [900] * 16, [280] * 16),                        # the last row tile has 96 rows: an empty second Q tile
+    (64, 32, 8, [600] * 64, [90] * 64),
+    (128, 32, 8, [a for a, _ in MIXED], [b for _, b in MIXED]),  # prompts, parts of prompts, few rows and single tokens
+    (64, 16, 4, [a for a, _ in MIXED], [b for _, b in MIXED]),
+    (256, 16, 2, [a for a, _ in MIXED], [b for _, b in MIXED])])
+def test_many_prompt_parts(ra, d, Hq, Hkv, lens, qlens):
+    """Several units of the row-tile kernel a CTA: phases, notes and tiles carried from one to the next."""
+    c = Case(ra, d + len(lens), lens, qlens, Hq, Hkv, d, 32)
+    run_units(ra, c, max(qlens))
+
+
+def test_many_prompt_parts_without_causal_mask(ra):
+    c = Case(ra, 95, [a for a, _ in MIXED], [b for _, b in MIXED], 8, 4, 128, 64)
+    run_units(ra, c, 1075, causal=False, o_fp32=False)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,R,rows", [(64, 2, 1, 700, 50), (128, 8, 8, 300, 1), (64, 4, 1, 1100, 3), (256, 2, 2, 200, 2)])
+def test_more_requests_than_threads(ra, d, Hq, Hkv, R, rows):
+    rng = random.Random(R)
+    lens = [rng.choice([0, 1, 17, 64, rng.randrange(200)]) for _ in range(R)]
+    c = Case(ra, R, lens, [rows if i % 5 else 0 for i in range(R)], Hq, Hkv, d, 16)
+    run_units(ra, c, rows)
