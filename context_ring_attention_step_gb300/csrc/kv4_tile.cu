@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   const uint32_t b_q = smem_u32(bars);              // [2] Q tile written (4 warps)
   const uint32_t b_full = smem_u32(bars + 2);       // [S] (4 warps)
   const uint32_t b_empty = smem_u32(bars + 2 + S);  // [S] (2 issuers)
-  const uint32_t b_s = smem_u32(bars + 2 + 2 * S);  // [2] S ready / O final
+  const uint32_t b_s = smem_u32(bars + 2 + 2 * S);  // [2] S ready / O final (Q tile without a key: once a segment)
   const uint32_t b_p = smem_u32(bars + 4 + 2 * S);  // [2] P written (4 warps)
   const uint32_t b_drain = smem_u32(bars + 6 + 2 * S);  // [2]
   // notes of the expanding warps: the first key of a segment with a NaN in a
@@ -320,13 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         wk.leave(line.end);
         const int na = qt == 0 ? sg.na[0] : sg.na[1];
         if (sg.n == 0) continue;
-        if (na > 0) {
-          if (!(ok = mbar_wait(b_q + 8 * qt, qph, ab, 130))) break;
-          qph ^= 1;
-        }
+        if (!(ok = mbar_wait(b_q + 8 * qt, qph, ab, 130))) break;
+        qph ^= 1;
         if (!(ok = mbar_wait(b_full + 8 * stage, kph, ab, 131))) break;
         tc_fence_after();
-        if (na > 0) { qk(stage); umma_commit(b_s + 8 * qt); }
+        if (na > 0) qk(stage);
+        umma_commit(b_s + 8 * qt);
         umma_commit(b_empty + 8 * stage);
         advance();
         for (int j = 0; j < sg.n; ++j) {
@@ -411,6 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
           st_shared_v4(sQ + qt * C::kTile + (i >> 3) * 16384 + row_t * 128 + (((i & 7) ^ (row_t & 7)) << 4), cvt(w[i].x),
                        cvt(w[i].y), cvt(w[i].z), cvt(w[i].w));
         fence_proxy_async_smem();
+      }
+      if (sg.n > 0) {
+        // (A Q tile without a key in this segment too: its issuer, and with it the
+        // ring of stages, may not leave these warps behind, which still read the
+        // notes of the segment before.)
         tc_fence_before();  // this segment's first P.V overwrites the O read before
         __syncwarp();
         if (lane == 0) mbar_arrive(b_q + 8 * qt);
@@ -532,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         }
         l_sum += tile_sum();
       }
-      if (na > 0 && ok) {
-        ok = mbar_wait(b_s + 8 * qt, sph, ab, 141);  // O final
+      if (sg.n > 0 && ok) {
+        ok = mbar_wait(b_s + 8 * qt, sph, ab, 141);  // O final (without a key: the issuer is here as well)
         ok = __all_sync(0xffffffffu, ok);
         sph ^= 1;
         tc_fence_after();

@@ -35,8 +35,9 @@ class Barrier:
 
 
 class Cta:
-    def __init__(self, segments, stages, rng, turns="count", q_tiles=2, slow=None):
+    def __init__(self, segments, stages, rng, turns="count", together=True, q_tiles=2, slow=None):
         self.segments, self.S, self.rng, self.turns, self.Q = segments, stages, rng, turns, q_tiles
+        self.together = together                  # a Q tile without keys takes part in the segment's barriers all the same
         self.slow = slow or {}                    # role -> factor of its delays
         self.now, self.events, self.order, self.blocked = 0.0, [], 0, []
         warps = 4 if q_tiles == 2 else 8
@@ -53,7 +54,7 @@ class Cta:
         self.s = [None] * q_tiles                 # whose scores S holds
         self.o = [None] * q_tiles
         self.q = [None] * q_tiles
-        self.dead = [None] * 8
+        self.dead, self.nan = [None] * 8, [None] * 8
         self.pipe = [0.0] * q_tiles               # when an issuer's last product ends
         self.finished = 0
         roles = [("issuer%d" % q, self.issuer(q)) for q in range(q_tiles)]
@@ -130,13 +131,15 @@ class Cta:
             n, na = seg[0], seg[1 + q]
             if n == 0:
                 continue
-            if na > 0:
+            if na > 0 or self.together:
                 ph = qph
                 yield lambda: self.b_q[q].passed(ph)
                 qph ^= 1
             yield lambda s=st, ph=kph: self.full[s].passed(ph)
             if na > 0:
                 scores(i, 0, st)
+            elif self.together:
+                self.commit(q, self.b_s[q])
             self.commit(q, self.empty[st])
             advance()
             for j in range(n):
@@ -162,13 +165,14 @@ class Cta:
                     advance()
 
     def softmax(self, q):
-        sph, tiles, turns = 0, 0, 0
+        sph, tiles, turns, seen = 0, 0, 0, 0
         for i, seg in enumerate(self.segments):
             n, na = seg[0], seg[1 + q]
             other = seg[2 - q] if self.Q == 2 else 0
             if na > 0:
                 yield 1500                        # query rows from memory
                 self.q[q] = i
+            if na > 0 or (n > 0 and self.together):
                 self.b_q[q].arrive()
             for j in range(na):
                 yield lambda ph=sph: self.b_s[q].passed(ph)
@@ -184,25 +188,29 @@ class Cta:
                 yield 900
                 self.written[q] += 1
                 self.b_p[q].arrive()
-            if na > 0:
+            if na > 0 or (n > 0 and self.together):
                 yield lambda ph=sph: self.b_s[q].passed(ph)
                 sph ^= 1
+            if na > 0:
                 yield 700
                 assert self.o[q] == (i, na - 1), "output overwritten"
+                assert self.nan[seen % 8] == seen, "notes of a segment overwritten"
             if seg[3]:
                 ph = self.soft_sync.phase
                 self.soft_sync.arrive()
                 yield lambda ph=ph: self.soft_sync.phase > ph
                 yield 1000
             tiles += n
+            seen += n > 0
             turns += other
 
     def expand(self, w):
-        issued, tiles = 0, 0
+        issued, tiles, seen = 0, 0, 0
         for i, seg in enumerate(self.segments):
             n = seg[0]
             if n == 0:
                 continue
+            self.nan[seen % 8] = seen
             ph = self.expand_sync.phase
             self.expand_sync.arrive()
             yield lambda ph=ph: self.expand_sync.phase > ph
@@ -219,6 +227,7 @@ class Cta:
                     yield 250
                     self.full[st].arrive()
             tiles += n
+            seen += 1
 
 
 def runs(segments, stages, seed, **kw):
@@ -320,6 +329,15 @@ def test_parity_alone_would_stall():
     # within one segment, and where every segment ends in a barrier, parity is enough
     assert all(runs([(40, 39, 40, True)], 5, seed, turns="parity") for seed in range(5))
     assert all(runs([(3, 3, 3, True)] * 8, 5, seed, turns="parity") for seed in range(10))
+
+
+def test_a_q_tile_without_keys_stays_with_the_others():
+    """Else the other one passes segments by the dozen while its last output is still being written."""
+    segs = [(1, 1, 1, False)] + [(1, 1, 0, False)] * 20
+    for seed in range(10):
+        assert runs(segs, 8, seed, slow={"soft1": 60.0})
+        with pytest.raises(AssertionError, match="notes of a segment"):
+            runs(segs, 8, seed, slow={"soft1": 60.0}, together=False)
 
 
 def test_one_q_tile():
