@@ -218,8 +218,9 @@ __device__ __forceinline__ void merge_warps(Acc<D, NT>& acc, float4 (&ml)[kWarps
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float4 x = ml[w][nt][lane & 3];
-      if (x.x != neg_inf()) l[0] += x.z * ex2_approx(x.x - mm[0]);
-      if (x.y != neg_inf()) l[1] += x.w * ex2_approx(x.y - mm[1]);
+      // without a reference: no key (l = 0), or scores that are all NaN (l = NaN, which the row's l becomes)
+      l[0] += x.x == neg_inf() ? x.z : x.z * ex2_approx(x.x - mm[0]);
+      l[1] += x.y == neg_inf() ? x.w : x.w * ex2_approx(x.y - mm[1]);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -624,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
             for (int d = 4; d < 32; d <<= 1) mm[nt][e] = fmaxf(mm[nt][e], __shfl_xor_sync(0xffffffffu, mm[nt][e], d));
         }
       };
+      // (0 times an l that is NaN, where every score was NaN, stays NaN)
       auto weight = [](float m, float mm) { return m == neg_inf() ? 0.f : ex2_approx(m - mm); };
       if (parts <= kAlone) {
         // few parts: warp 0's business alone; the others go on meanwhile

@@ -751,3 +751,51 @@ def test_more_requests_than_threads(ra, d, Hq, Hkv, R, rows):
     lens = [rng.choice([0, 1, 17, 64, rng.randrange(200)]) for _ in range(R)]
     c = Case(ra, R, lens, [rows if i % 5 else 0 for i in range(R)], Hq, Hkv, d, 16)
     run_units(ra, c, rows)
+
+
+# ------------------------------------------------------------------ rows that are not numbers
+
+def check_broken(ra, c, q, longest, causal=True):
+    """Query rows q instead of the case's own, which give the tolerance of the rows that stay numbers."""
+    sc = 1 / math.sqrt(c.d)
+    good, c.q = c.q, q
+    with np.errstate(invalid="ignore"):
+        want, wl = O.attention(f64(q), c.keys, c.values, c.lens, c.cu, causal, sc)
+    o, lse = ra.kv4_attention(q.cuda(), c.cache, c.table, c.lens_t, c.cu_t, causal=causal, o_fp32=True,
+                              max_q_len=longest, check=True)
+    c.q = good
+    c.compare(f64(o), f64(lse), want, wl, sc, True)
+    return want, wl
+
+
+# few rows: whole units, and units split over CTAs (long requests)
+ROWS = [(64, 2, 1, [17, 150, 1], [3, 5, 1]), (128, 4, 2, [17, 33, 1000, 0], [1, 2, 5, 3]), (256, 2, 1, [49, 200], [2, 9]),
+        (128, 4, 1, [4001], [1]), (256, 4, 1, [2500], [1])]
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", ROWS)
+def test_nan_query_rows(ra, d, Hq, Hkv, lens, qlens):
+    """A NaN in a query row: NaN in its output and LSE, and in no other row's."""
+    c = Case(ra, 101 + d, lens, qlens, Hq, Hkv, d, 16)
+    q = c.q.clone()
+    rows = list(range(0, c.cu[-1], 3))
+    for i in rows:
+        q[i, i % Hq, (7 * i) % d] = float("nan")
+    want, wl = check_broken(ra, c, q, max(qlens))
+    assert np.isnan(want).any() and np.isnan(wl).sum() == sum(not np.isneginf(wl[i % Hq, i]) for i in rows)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", ROWS)
+def test_nan_newest_key(ra, d, Hq, Hkv, lens, qlens):
+    """The newest key is NaN: alone in its tile (and part) in some cases, and the last row's score there the only one."""
+    rng = np.random.default_rng(3)
+    keys = []
+    for L in lens:
+        k = bf16(rng, L, Hkv, d)
+        if L:
+            k[L - 1, 0, 5] = float("nan")
+        keys.append(k)
+    c = Case(ra, 103 + d, lens, qlens, Hq, Hkv, d, 16, keys=keys)
+    want, wl = check_broken(ra, c, c.q, max(qlens))
+    assert np.isnan(wl).any()
+    check_broken(ra, c, c.q, max(qlens), causal=False)
