@@ -543,6 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         tc_fence_after();
       }
 
+      // A row whose scores were all NaN has no reference, but a sum that is NaN; with
+      // any reference its partial result makes the row NaN.
+      if (m_ref == neg_inf() && !(l_sum == 0.f)) m_ref = 0.f;
+
       // ---- output, or a partial result
       const bool direct = wk.whole();
       const int c0 = direct ? 0 : line.owner(wk.first);

@@ -768,12 +768,14 @@ def check_broken(ra, c, q, longest, causal=True):
     return want, wl
 
 
-# few rows: whole units, and units split over CTAs (long requests)
+# few rows and row tiles; whole units, and units split over CTAs (long requests)
 ROWS = [(64, 2, 1, [17, 150, 1], [3, 5, 1]), (128, 4, 2, [17, 33, 1000, 0], [1, 2, 5, 3]), (256, 2, 1, [49, 200], [2, 9]),
         (128, 4, 1, [4001], [1]), (256, 4, 1, [2500], [1])]
+TILES = [(64, 2, 1, [3001], [70]), (128, 4, 1, [128 * 39 + 1], [30]), (128, 8, 1, [1111, 5], [129, 7]), (256, 4, 1, [2500], [31]),
+         (128, 8, 8, [260] * 40, [100] * 40), (256, 8, 2, [130] * 80, [60] * 80)]
 
 
-@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", ROWS)
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", ROWS + TILES)
 def test_nan_query_rows(ra, d, Hq, Hkv, lens, qlens):
     """A NaN in a query row: NaN in its output and LSE, and in no other row's."""
     c = Case(ra, 101 + d, lens, qlens, Hq, Hkv, d, 16)
@@ -785,7 +787,7 @@ def test_nan_query_rows(ra, d, Hq, Hkv, lens, qlens):
     assert np.isnan(want).any() and np.isnan(wl).sum() == sum(not np.isneginf(wl[i % Hq, i]) for i in rows)
 
 
-@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", ROWS)
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", [x for x in ROWS + TILES if len(x[3]) < 10])
 def test_nan_newest_key(ra, d, Hq, Hkv, lens, qlens):
     """The newest key is NaN: alone in its tile (and part) in some cases, and the last row's score there the only one."""
     rng = np.random.default_rng(3)
