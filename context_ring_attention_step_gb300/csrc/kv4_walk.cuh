@@ -34,11 +34,13 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t w, int i, int j) {
 
 // The power of two that brings a row whose largest magnitude has the bf16 bits
 // `mx` to about 1 (`up`, applied to the row) and its inverse (returned, for the
-// softmax scale); 1 for a row of zeros or with an infinity or NaN.
+// softmax scale); 1 for a row of zeros.  A row with an infinity or NaN gets a
+// scale of NaN: its scores are infinite or NaN, and a softmax has no value then, even
+// where all of them are -inf (which would look like a row without keys).
 __device__ __forceinline__ float kv4_row_scale(uint32_t mx, float& up) {
   const int ex = mx == 0 || mx >= 0x7f80 ? 0 : min(max((int)(mx >> 7) - 127, -126), 126);
   up = __uint_as_float((uint32_t)(127 - ex) << 23);
-  return __uint_as_float((uint32_t)(127 + ex) << 23);
+  return mx >= 0x7f80 ? quiet_nan() : __uint_as_float((uint32_t)(127 + ex) << 23);
 }
 
 // What a CTA knows of a request.

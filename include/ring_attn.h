@@ -519,7 +519,8 @@ ra_status ra_kv4_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_h
  *   softmax_scale <= 0 selects 1/sqrt(head_dim).
  *   o [num_q_tokens, num_q_heads, head_dim]: bf16, or fp32 when o_is_fp32.
  *   lse fp32 [num_q_heads, num_q_tokens], natural log.
- * A row that sees no key gets o = 0 and lse = -inf.  Rows outside
+ * A row that sees no key gets o = 0 and lse = -inf; one that sees a key and has
+ * an infinity or a NaN in its query becomes NaN, o and lse.  Rows outside
  * [cu_q[0], cu_q[R]) are left as they were.  The workspace (device, 256-byte
  * aligned) must be zero before its first use (a call leaves it ready for the
  * next, of whatever shape, if it is large enough for it) and must not be shared

@@ -801,3 +801,21 @@ def test_nan_newest_key(ra, d, Hq, Hkv, lens, qlens):
     want, wl = check_broken(ra, c, c.q, max(qlens))
     assert np.isnan(wl).any()
     check_broken(ra, c, c.q, max(qlens), causal=False)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", ROWS + TILES)
+def test_infinite_queries(ra, d, Hq, Hkv, lens, qlens):
+    """An infinity in a query row: every score is infinite or NaN and the softmax has no value, also where all are -inf."""
+    rng = np.random.default_rng(4)
+    keys = []
+    for L in lens:
+        k = bf16(rng, L, Hkv, d)
+        k[:, :, 3] = 4.0                                         # no code is 0 there
+        keys.append(k)
+    c = Case(ra, 107 + d, lens, qlens, Hq, Hkv, d, 16, keys=keys)
+    q = c.q.clone()
+    rows = list(range(0, c.cu[-1], 2))
+    for i in rows:
+        q[i, i % Hq, 3 if i % 4 else 9] = float("-inf") if i % 3 else float("inf")
+    _, wl = check_broken(ra, c, q, max(qlens))
+    assert np.isnan(wl).sum() == sum(not np.isneginf(wl[i % Hq, i]) for i in rows)
