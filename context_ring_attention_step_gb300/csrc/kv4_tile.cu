@@ -404,7 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         }
         float up;
         sl2 = p.scale * kLog2e * kv4_row_scale(max(mx & 0xffffu, mx >> 16), up);
-        if (lim == 0) sl2 = 1.f;  // (it scales masked scores too, and a row without keys is not to become NaN)
+        // It scales masked scores (-inf) too: not with NaN in a row without keys, and not
+        // with a product that underflowed to 0 (2^-126 leaves scores that are as good as 0).
+        if (lim == 0) sl2 = 1.f;
+        if (sl2 < 0x1p-126f) sl2 = 0x1p-126f;
         auto cvt = [&](uint32_t x) { return pack_f16x2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up); };
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)

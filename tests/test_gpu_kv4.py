@@ -819,3 +819,12 @@ def test_infinite_queries(ra, d, Hq, Hkv, lens, qlens):
         q[i, i % Hq, 3 if i % 4 else 9] = float("-inf") if i % 3 else float("inf")
     _, wl = check_broken(ra, c, q, max(qlens))
     assert np.isnan(wl).sum() == sum(not np.isneginf(wl[i % Hq, i]) for i in rows)
+
+
+@pytest.mark.parametrize("n", [3, 70])                           # both kernels
+def test_scores_that_vanish(ra, n):
+    """A scale times a row's own power of two below the smallest number: equal weights for the keys a row sees."""
+    c = Case(ra, 109, [200], [n], 2, 1, 128, 16)
+    c.q = (c.q.float() * 2.0 ** -120).to(torch.bfloat16)
+    for scale in (1e-30, 1e-8, 1.0):
+        c.check(ra, scale=scale, max_q_len=n)
