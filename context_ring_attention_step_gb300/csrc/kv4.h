@@ -18,6 +18,10 @@ constexpr int kKv4Group = 16;              // elements sharing one scale
 constexpr float kKv4MaxScale = 10240.f;    // largest scale: 6 * 10240 is finite in fp16
 constexpr int kKv4NanScale = 0xff;         // scale byte of a group with a non-finite element
 constexpr int kKv4MaxLength = 1 << 30;     // cached tokens of a request (positions a few tiles on still fit 32 bits)
+// Status of a kernel that gave up on a pipeline wait: this plus the wait's site.  Above the
+// codes of the public header, so that it wins where both occur: rows are missing then.
+constexpr int kKv4GaveUp = 2000;
+static_assert(kKv4GaveUp > RA_KV4_BAD_FREE_COUNT, "the largest status wins");
 constexpr int kKv4MaxRequests = 4096;      // kv4_tables keeps per-request prefix sums in shared memory
 
 // One tile: K codes (8 D bytes), K scales (D), V codes (8 D), V scales (D).

@@ -296,7 +296,7 @@ ra_status ra_kv4_status(const void* status, void* stream_) {
     case RA_KV4_NO_PAGES: return fail(RA_ERR_WORKSPACE, "not enough free pages");
     case RA_KV4_BAD_FREE_COUNT: return fail(RA_ERR_INVALID_ARG, "the free count is negative or passes the number of pages");
   }
-  return fail(RA_ERR_TIMEOUT, "a kernel gave up on a pipeline wait (site %d)", word);
+  return fail(RA_ERR_TIMEOUT, "a kernel gave up on a pipeline wait (site %d)", word - ra::kKv4GaveUp);
 }
 
 }  // extern "C"

@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_dead + kSegs * 8);
   int* s_int = reinterpret_cast<int*>(tmem_slot + 1);  // abort, bad, last
   volatile uint32_t* s_turns = reinterpret_cast<uint32_t*>(s_int + 3);  // [2] warps' P tiles of Q tile 0 / 1 so far
+  // s_int[5]: where a wait was given up
   __shared__ long long s_sum[kThreads / 32], s_found[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
       mbar_init(b_full + 8 * i, C::kExpand);
       mbar_init(b_empty + 8 * i, kQt);
     }
-    s_int[0] = s_int[1] = s_int[2] = 0;
+    s_int[0] = s_int[1] = s_int[2] = s_int[5] = 0;
     s_turns[0] = s_turns[1] = 0;
     fence_mbar_init();
   }
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Abort ab{s_int, s_int + 1};
+  const Abort ab{s_int, s_int + 5};
   if (bad) atomicMax(s_int + 1, bad);
 
   // Register split: 512 threads x 128 at launch = 128 x 40 + 256 x 184 + 128 x 104.
@@ -547,6 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
         tc_fence_after();
       }
 
+      // After a wait that was given up the rows are not known: NaN, not zero.
+      if (!ok) l_sum = quiet_nan();
       // A row whose scores were all NaN has no reference, but a sum that is NaN; with
       // any reference its partial result makes the row NaN.
       if (m_ref == neg_inf() && !(l_sum == 0.f)) m_ref = 0.f;
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (tid == 0) kv4_end(p, s_int[1]);
+  if (tid == 0) kv4_end(p, s_int[5] ? kKv4GaveUp + s_int[5] : s_int[1]);
 }
 
 template <int D>

@@ -539,7 +539,8 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
  * Synchronise `stream` and read a status word (ra_kv4_tables' status, or the
  * start of ra_kv4_attention's workspace): RA_OK; RA_ERR_WORKSPACE for missing
  * pages; RA_ERR_INVALID_ARG for the other refusals; RA_ERR_TIMEOUT if a kernel
- * gave up on a pipeline wait.
+ * gave up on a pipeline wait (the rows it then could not compute are NaN; this
+ * status wins over the others).
  */
 ra_status ra_kv4_status(const void* status, void* stream);
 

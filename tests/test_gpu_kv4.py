@@ -828,3 +828,12 @@ def test_scores_that_vanish(ra, n):
     c.q = (c.q.float() * 2.0 ** -120).to(torch.bfloat16)
     for scale in (1e-30, 1e-8, 1.0):
         c.check(ra, scale=scale, max_q_len=n)
+
+
+def test_status_words(ra):
+    """A wait that was given up has a word above every other one (the largest wins), and names its site."""
+    for word, status, text in ((1001, 1, "page"), (1006, 1, "free count"), (2130, 5, "site 130)"), (2150, 5, "site 150)")):
+        with pytest.raises(ra.RingAttnError, match=text.replace(")", r"\)")) as e:
+            ra.kv4_status(torch.tensor([word, 0], dtype=torch.int32).cuda())
+        assert e.value.status == status
+    ra.kv4_status(torch.zeros(1, dtype=torch.int32).cuda())
