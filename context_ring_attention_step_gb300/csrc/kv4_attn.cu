@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, (AttnCfg<D, NT>::kPerSm)) kv4_attn_k
     auto ask = [&](int slot, int page, int tok) {
       const bool good = (uint32_t)page < (uint64_t)p.cache.num_pages;
       oks = oks << 1 | (good ? 1u : 0u);
-      if (!good) bad = RA_KV4_BAD_PAGE;
+      if (!good) bad = max(bad, (int)RA_KV4_BAD_PAGE);
       copy_tile<D>(smem_u32(ring) + slot, base + (int64_t)(good ? page : 0) * p.page_bytes + ((tok >> 4) & tiles_mask) * L::kBytes,
                    good && tok < t_stop, lane);
       copy_commit();

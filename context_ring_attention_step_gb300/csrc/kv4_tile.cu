@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tile_kernel(const Kv4AttnPara
           if (!ok) continue;
           const uint32_t dst = sKV + st * C::kTile + 2048 * kSubs * dw;
           if (kind == 0) {
-            if (dead) bad = RA_KV4_BAD_PAGE;
+            if (dead) bad = max(bad, (int)RA_KV4_BAD_PAGE);
             if (lane < kSubs) s_dead[((tiles + j) & (kSegs - 1)) * 8 + kSubs * dw + lane] = (dead >> lane) & 1;
 #pragma unroll
             for (int u = 0; u < kSubs; ++u) expand_k<D>(dst + 2048 * u, k[u], places);

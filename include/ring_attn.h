@@ -527,7 +527,7 @@ ra_status ra_kv4_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_h
  * by calls that may overlap.  Its first word is the status of the last call
  * (ra_kv4_status): keys on a page outside the cache are left out, a request
  * with a length out of range sees no key, one with offsets out of range has no
- * rows, and the status says so.  num_q_tokens * num_q_heads <= 2^30.
+ * rows, and the status says so (the largest code, where several hold).  num_q_tokens * num_q_heads <= 2^30.
  */
 ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_stride, int32_t num_q_tokens,
                            int32_t num_q_heads, const int32_t* block_table, int32_t table_width, int64_t table_stride,

@@ -837,3 +837,19 @@ def test_status_words(ra):
             ra.kv4_status(torch.tensor([word, 0], dtype=torch.int32).cuda())
         assert e.value.status == status
     ra.kv4_status(torch.zeros(1, dtype=torch.int32).cuda())
+
+
+@pytest.mark.parametrize("n", [1, 100])                          # both kernels
+def test_the_largest_status_wins(ra, n):
+    """Pages outside the cache in every CTA's part, and a request with a length out of range: the status is the length's."""
+    cache = ra.Kv4Cache(4, 16, 1, 128)
+    L = 600000
+    table = torch.full((2, L // 16), -1, dtype=torch.int32).cuda()
+    lens = torch.tensor([L, -1], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, n, n + 1], dtype=torch.int32).cuda()
+    q = torch.ones(n + 1, 1, 128, dtype=torch.bfloat16).cuda()
+    ws = ra.kv4_attention_workspace(cache, n + 1, 1, n)
+    o, lse = ra.kv4_attention(q, cache, table, lens, cu, max_q_len=n, workspace=ws)
+    with pytest.raises(ra.RingAttnError, match="length"):
+        ra.kv4_status(ws)
+    assert o.eq(0).all() and torch.isneginf(lse).all()
