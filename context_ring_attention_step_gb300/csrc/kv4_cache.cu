@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool alloc = p.free_pages != nullptr;
-  const int32_t count = alloc ? *p.free_count : 0;
+  const int32_t count = p.free_count ? *p.free_count : 0;
   if (tid == 0) s_bad = 0;
   __syncthreads();
 
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
     }
     if (tid == 0) {
       p.cu_new[R] = add;
-      if (alloc) *p.free_count_out = count + back - need;
+      if (p.free_count_out) *p.free_count_out = count + back - need;
       *p.status = code;
     }
   }

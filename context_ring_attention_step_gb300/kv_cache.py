@@ -149,7 +149,8 @@ def kv4_tables(kv_lens, new_lens, block_table, page_size, num_slots, free_pages=
     ``kv_lens`` [R] and ``new_lens`` [R] (int32): tokens cached before the step
     and tokens it adds, -1 for a request that leaves.  ``block_table`` [R, W] and
     ``free_pages`` [N] are updated in place; ``free_pages=None`` only maps (the
-    block table already holds the pages).  ``num_slots``: length of the slot map
+    block table already holds the pages; the free count is handed on, 0 if there is
+    none).  ``num_slots``: length of the slot map
     (-1 behind the last new token).  ``out`` may name ``kv_lens`` and
     ``free_count`` themselves as outputs.  A step that cannot be done (not
     enough pages, ...) changes nothing and says so in ``status``;
@@ -172,6 +173,7 @@ def kv4_tables(kv_lens, new_lens, block_table, page_size, num_slots, free_pages=
             raise ValueError("free_pages needs free_count")
         num_pages = free_pages.shape[0]
         free = _array("free_pages", free_pages, (num_pages,), _I32, dev)
+    if free_count is not None:
         count = _array("free_count", free_count, one, _I32, dev)
     o_lens, o_cu, o_slots, o_pos, o_count, o_status = out
     _launch(dev, lib.ra_kv4_tables, lens, new, R, table, width, stride, int(page_size), free, num_pages, count,

@@ -469,7 +469,8 @@ ra_status ra_kv4_cache_bytes(int64_t num_pages, int32_t page_size, int32_t num_k
  *     that left.  cu_new [R + 1]: prefix sums of the added tokens.
  *   slot_map int64 [num_slots], positions int32 [num_slots]: of the new tokens,
  *     request by request; -1 behind the last one.
- *   free_count_out [1] (may be free_count).
+ *   free_count_out [1] (may be free_count).  With free_pages NULL both may be
+ *     NULL, and the count (0 without free_count) is handed on.
  *   status int32 [1]: 0, or why the step was refused.  A refused step changes
  *     nothing: kv_lens_out = kv_lens, free_count_out = free_count, cu_new = 0,
  *     slots and positions -1.  Read it with ra_kv4_status.

@@ -853,3 +853,15 @@ def test_the_largest_status_wins(ra, n):
     with pytest.raises(ra.RingAttnError, match="length"):
         ra.kv4_status(ws)
     assert o.eq(0).all() and torch.isneginf(lse).all()
+
+
+def test_free_count_of_a_step_that_only_maps(ra):
+    """Without a free list the count is the caller's, or 0: never what the memory held."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+    for count, want in ((None, 0), (i32([5]), 5)):
+        out = ra.kv4_tables_out(2, 8)
+        for t in out:
+            t.fill_(-77)
+        step = ra.kv4_tables(i32([3, 0]), i32([1, 4]), i32([[2], [1]]), 16, 8, free_count=count, out=out, check=True)
+        assert int(step.free_count) == want
+        assert step.slot_map.tolist() == [35, 16, 17, 18, 19, -1, -1, -1]
