@@ -289,7 +289,7 @@ ra_status ra_kv4_status(const void* status, void* stream_) {
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   switch (word) {
     case 0: return RA_OK;
-    case RA_KV4_BAD_PAGE: return fail(RA_ERR_INVALID_ARG, "a block table entry is not a page of the cache");
+    case RA_KV4_BAD_PAGE: return fail(RA_ERR_INVALID_ARG, "a block table entry or free page is not a page of the cache");
     case RA_KV4_BAD_LENGTH: return fail(RA_ERR_INVALID_ARG, "a length is negative or passes the block table's row");
     case RA_KV4_BAD_OFFSET: return fail(RA_ERR_INVALID_ARG, "query offsets fall or pass the number of query tokens");
     case RA_KV4_TOO_MANY_TOKENS: return fail(RA_ERR_INVALID_ARG, "more new tokens than slots");

@@ -37,6 +37,8 @@ struct Counts {
 // and the new free count are the exception when they replace the old ones in
 // place: the grid is then one cluster, which waits until all have read them.
 // 262144 slots of 256 requests: 26 us as one cluster of 8 CTAs, 13 us as 256 CTAs.
+constexpr int kTablesCluster = 8;  // CTAs of the one cluster of a step in place
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesParams p) {
   extern __shared__ int32_t sm[];
@@ -150,7 +152,6 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
     if (tid == 0) {
       p.cu_new[R] = add;
       if (p.free_count_out) *p.free_count_out = count + back - need;
-      *p.status = code;
     }
   }
   // last index i with a[i] <= x (a non-decreasing, a[0] = 0, x < a[R])
@@ -170,7 +171,31 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
     const int r = find(s_back, i - count);
     return p.block_table[(size_t)r * p.table_stride + (i - count - s_back[r])];
   };
-  const int g0 = blockIdx.x * kThreads + tid, gn = gridDim.x * kThreads;
+  if (lead) {
+    // Pages given back, taken, or with place for new tokens that are none: the step is
+    // made, but its tokens there have no slot.
+    // (Taken pages that were not given back are a run of the free list.)
+    int none = 0;
+#pragma unroll 8
+    for (int32_t i = max(top - need, 0) + tid; i < count; i += kThreads) none |= p.free_pages[i];
+    if (alloc) {
+      for (int r = tid; r < R; r += kThreads)
+        if (s_cu[r + 1] > s_cu[r] && (s_len[r] & (P - 1)))
+          none |= p.block_table[(size_t)r * p.table_stride + (s_len[r] >> p.page_shift)];
+      for (int r = warp; r < R; r += kThreads / 32)
+#pragma unroll 4
+        for (int32_t i = lane; i < s_back[r + 1] - s_back[r]; i += 32)
+          none |= p.block_table[(size_t)r * p.table_stride + i];
+    }
+    none = __syncthreads_or(none < 0);
+    if (tid == 0) *p.status = code ? code : none ? RA_KV4_BAD_PAGE : 0;
+  }
+  // The first CTA of a grid without a cluster has done its share: 262144 slots of 256
+  // requests, 24 of them leaving and 32 new, take 10.2 us a call, 12.3 where it takes
+  // slots too.
+  const int others = gridDim.x > kTablesCluster ? gridDim.x - 1 : gridDim.x;
+  const int g0 = (blockIdx.x - (gridDim.x - others)) * kThreads + tid, gn = others * kThreads;
+  if (g0 < 0) return;
   for (int32_t i = g0; i < back; i += gn) p.free_pages[count + i] = free_page(count + i);
   for (int32_t i = g0; i < need; i += gn) {
     const int r = find(s_need, i);
@@ -392,8 +417,9 @@ cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream) {
   const bool small = p.num_requests <= 1024;
   const int64_t threads = small ? 256 : 1024;
   const int64_t want = std::max<int64_t>(1, (p.num_slots + 4 * threads - 1) / (4 * threads));
-  const int64_t most = in_place ? 8 : small ? 304 : 152;
-  cfg.gridDim = dim3((unsigned)std::min(want, most));
+  const int64_t most = in_place ? kTablesCluster : small ? 304 : 152;
+  const int64_t ctas = std::min(want, most);
+  cfg.gridDim = dim3((unsigned)(ctas > kTablesCluster ? ctas + 1 : ctas));
   cfg.blockDim = dim3((unsigned)threads);
   attr[0].val.clusterDim.x = in_place ? cfg.gridDim.x : 1;
   if (small) return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<256>, p);

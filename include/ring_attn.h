@@ -439,7 +439,7 @@ typedef struct ra_kv4_cache {
 
 /* Status words of the calls below. */
 typedef enum {
-  RA_KV4_BAD_PAGE = 1001,        /* a block table entry is not a page of the cache */
+  RA_KV4_BAD_PAGE = 1001,        /* a block table entry (or free page) is not a page of the cache */
   RA_KV4_BAD_LENGTH = 1002,      /* a length is negative, or passes the block table's row or 2^30 */
   RA_KV4_BAD_OFFSET = 1003,      /* query offsets fall or pass the number of query tokens */
   RA_KV4_TOO_MANY_TOKENS = 1004, /* more new tokens than slots */
@@ -474,6 +474,9 @@ ra_status ra_kv4_cache_bytes(int64_t num_pages, int32_t page_size, int32_t num_k
  *   status int32 [1]: 0, or why the step was refused.  A refused step changes
  *     nothing: kv_lens_out = kv_lens, free_count_out = free_count, cu_new = 0,
  *     slots and positions -1.  Read it with ra_kv4_status.
+ *     RA_KV4_BAD_PAGE is no refusal: the step was made, but with a free list a
+ *     page that it took, gave back or put tokens behind is negative, and the tokens
+ *     there have slot -1.
  * A page must occur only once in the free list and the block table together.
  */
 ra_status ra_kv4_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t num_requests, int32_t* block_table,

@@ -865,3 +865,25 @@ def test_free_count_of_a_step_that_only_maps(ra):
         step = ra.kv4_tables(i32([3, 0]), i32([1, 4]), i32([[2], [1]]), 16, 8, free_count=count, out=out, check=True)
         assert int(step.free_count) == want
         assert step.slot_map.tolist() == [35, 16, 17, 18, 19, -1, -1, -1]
+
+
+@pytest.mark.parametrize("big", [0, 20000])                      # one CTA, and many
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_that_are_none_are_reported(ra, big, in_place):
+    """A negative page that is given back, taken, or holds a request's last tokens: the step is made, and its status says so."""
+    W = big // 16 + 4
+    row = lambda *ids: list(ids) + [-9] * (W - len(ids))
+    base = dict(lens=[10, 20, 32, 0], new=[1, -1, 2, big], table=[row(0), row(1, 2), row(3, 4), row()],
+                free=list(range(10, 10 + W + 2)) + [-5, -5])
+    count = W + 2
+
+    def status(want, **change):
+        a = {**base, **change}
+        slots = sum(max(n, 0) for n in a["new"]) + 3
+        got = run_tables(ra, a["lens"], a["new"], a["table"], 16, slots, a["free"], count, in_place)
+        assert got == (want,) + O.tables(a["lens"], a["new"], a["table"], 16, slots, a["free"], count)
+    status(0)
+    status(1001, table=[row(0), row(1, -4), row(3, 4), row()])   # given back
+    status(1001, table=[row(-1), row(1, 2), row(3, 4), row()])   # the page of the newest tokens
+    status(0, table=[row(0), row(1, 2), row(-1, 4), row()])      # full pages are not looked at
+    status(1001, new=[1, 0, 2, big], free=base["free"][:W + 1] + [-1, -5, -5])   # taken
