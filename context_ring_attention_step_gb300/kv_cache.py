@@ -58,10 +58,6 @@ class Kv4Cache:
 Kv4Tables = collections.namedtuple("Kv4Tables", "kv_lens cu_new slot_map positions free_count status")
 
 
-def _library():
-    return _ra._lib or _ra.load_library()
-
-
 _I32, _I64, _BF16, _F32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
 _current_device = torch._C._cuda_getDevice
 
@@ -289,4 +285,5 @@ def kv4_status(status):
     """Synchronise and raise if the status word at the start of ``status`` (``Kv4Tables.status``,
     or the workspace of ``kv4_attention``) reports a refusal."""
     lib = _library()
+    _on_gpu("status", status.device)
     _launch(status.device, lib.ra_kv4_status, status.data_ptr())

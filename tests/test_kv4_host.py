@@ -159,3 +159,8 @@ def test_python_checks(ra):
     with pytest.raises(ValueError, match="GPU"):
         ra.kv4_tables(torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                       torch.zeros(2, 4, dtype=torch.int32), 64, 2)
+
+
+def test_status_must_be_on_a_gpu(ra):
+    with pytest.raises(ValueError, match="GPU"):
+        ra.kv4_status(torch.zeros(1, dtype=torch.int32))
