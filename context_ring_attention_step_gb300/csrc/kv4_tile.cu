@@ -40,7 +40,10 @@ constexpr int kKeys = 128;
 constexpr int kThreads = 512;
 constexpr int kFan = 8;  // partial results merged at once
 constexpr int kUnit = 1;  // what beginning a unit costs, in blocks of 128 keys
-constexpr int kTurnLimit = 1 << 12;  // polls of a wait for the other Q tile's turn
+// Polls of a wait for the other Q tile's turn.  In us, for 0, 6, 64 and 4096: one unit of many
+// key tiles (1024 tokens over 33792) 575, 548, 545, 542; several short units a CTA (16 parts of
+// 280 over 900, 32 / 8 heads) 181, 187, 225, 225: there the two are often a unit apart.
+constexpr int kTurnLimit = 6;
 constexpr int kSegs = 8;  // segments (and key tiles) that the expanding warps may be ahead, rounded up
 // P's reference as in kv4_attn.cu: the row's largest P is in (2^6, 2^7] when it
 // moves.  A tile whose P's add up to no more than 2^15 needs no look at its maximum.
