@@ -36,8 +36,9 @@ struct Counts {
 // entries and free pages are written only where none are read.  The new lengths
 // and the new free count are the exception when they replace the old ones in
 // place: the grid is then one cluster, which waits until all have read them.
-// 262144 slots of 256 requests: 26 us as one cluster of 8 CTAs, 13 us as 256 CTAs.
-constexpr int kTablesCluster = 8;  // CTAs of the one cluster of a step in place
+// 262144 slots of 256 requests, one call with cold caches: 42 us in place (one cluster of
+// 8 CTAs), 15 us as 257 CTAs.
+constexpr int kTablesCluster = 8;  // a grid of at most so many CTAs is one cluster; a step in place has no larger one
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesParams p) {
@@ -48,11 +49,12 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
   int32_t* s_need = s_cu + R + 1;     // [R + 1] pages taken before request r
   int32_t* s_back = s_need + R + 1;   // [R + 1] pages given back before request r
   __shared__ Counts s_warp[kThreads / 32];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_none;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const cg::cluster_group cluster = cg::this_cluster();
   const bool alloc = p.free_pages != nullptr;
   const int32_t count = p.free_count ? *p.free_count : 0;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_none = 0;
   __syncthreads();
 
   const int per = (R + kThreads - 1) / kThreads;
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
   bool gone[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) gone[i] = r0 + i < r1 && p.new_lens[r0 + i] < 0;
-  cg::this_cluster().sync();  // the cluster has read its inputs; this CTA's prefix sums are in place
+  cluster.sync();  // the cluster has read its inputs; this CTA's prefix sums are in place
 
   if (lead) {
     for (int r = r0; r < r1; ++r) {
@@ -171,31 +173,31 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
     const int r = find(s_back, i - count);
     return p.block_table[(size_t)r * p.table_stride + (i - count - s_back[r])];
   };
-  if (lead) {
-    // Pages given back, taken, or with place for new tokens that are none: the step is
-    // made, but its tokens there have no slot.
-    // (Taken pages that were not given back are a run of the free list.)
+  // Pages given back, taken, or with place for new tokens that are none: the step is
+  // made, but its tokens there have no slot, and the status says so.  A grid of more CTAs than a
+  // cluster leaves this to its first one, which then takes no slots: 262144 slots
+  // of 256 requests, 24 of them leaving and 32 new, take 10.2 us a call, 12.3 where it does.
+  const bool apart = gridDim.x > kTablesCluster;
+  if (lead || !apart) {
+    const int c0 = apart ? tid : blockIdx.x * kThreads + tid, cn = apart ? kThreads : gridDim.x * kThreads;
     int none = 0;
+    // (taken pages that were not given back are a run of the free list)
 #pragma unroll 8
-    for (int32_t i = max(top - need, 0) + tid; i < count; i += kThreads) none |= p.free_pages[i];
+    for (int32_t i = max(top - need, 0) + c0; i < count; i += cn) none |= p.free_pages[i];
     if (alloc) {
-      for (int r = tid; r < R; r += kThreads)
+      for (int r = c0; r < R; r += cn)
         if (s_cu[r + 1] > s_cu[r] && (s_len[r] & (P - 1)))
           none |= p.block_table[(size_t)r * p.table_stride + (s_len[r] >> p.page_shift)];
-      for (int r = warp; r < R; r += kThreads / 32)
+      for (int r = c0 >> 5; r < R; r += cn >> 5)
 #pragma unroll 4
         for (int32_t i = lane; i < s_back[r + 1] - s_back[r]; i += 32)
           none |= p.block_table[(size_t)r * p.table_stride + i];
     }
-    none = __syncthreads_or(none < 0);
-    if (tid == 0) *p.status = code ? code : none ? RA_KV4_BAD_PAGE : 0;
+    if (none < 0) atomicOr(apart ? &s_none : cluster.map_shared_rank(&s_none, 0), 1);
   }
-  // The first CTA of a grid without a cluster has done its share: 262144 slots of 256
-  // requests, 24 of them leaving and 32 new, take 10.2 us a call, 12.3 where it takes
-  // slots too.
-  const int others = gridDim.x > kTablesCluster ? gridDim.x - 1 : gridDim.x;
-  const int g0 = (blockIdx.x - (gridDim.x - others)) * kThreads + tid, gn = others * kThreads;
-  if (g0 < 0) return;
+  const int others = apart ? gridDim.x - 1 : gridDim.x;
+  const int gn = others * kThreads;
+  const int g0 = apart && lead ? 0x7fffffff : (blockIdx.x - (apart ? 1 : 0)) * kThreads + tid;
   for (int32_t i = g0; i < back; i += gn) p.free_pages[count + i] = free_page(count + i);
   for (int32_t i = g0; i < need; i += gn) {
     const int r = find(s_need, i);
@@ -242,6 +244,8 @@ __global__ void __launch_bounds__(kThreads) kv4_tables_kernel(const Kv4TablesPar
       }
     }
   }
+  cluster.sync();
+  if (lead && tid == 0) *p.status = code ? code : s_none ? RA_KV4_BAD_PAGE : 0;
 }
 
 // ------------------------------------------------------------------ store / load
@@ -421,7 +425,7 @@ cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream) {
   const int64_t ctas = std::min(want, most);
   cfg.gridDim = dim3((unsigned)(ctas > kTablesCluster ? ctas + 1 : ctas));
   cfg.blockDim = dim3((unsigned)threads);
-  attr[0].val.clusterDim.x = in_place ? cfg.gridDim.x : 1;
+  attr[0].val.clusterDim.x = ctas > kTablesCluster ? 1 : cfg.gridDim.x;
   if (small) return cudaLaunchKernelEx(&cfg, kv4_tables_kernel<256>, p);
   static Kv4SmemLimit limit;
   return limit.launch(reinterpret_cast<const void*>(kv4_tables_kernel<1024>),
