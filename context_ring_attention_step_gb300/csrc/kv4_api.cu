@@ -61,10 +61,13 @@ size_t page_bytes(int32_t page_size, int32_t Hkv, int32_t D) {
 // tile kernel, where a call can have them.  Its time hardly depends on the rows
 // up to 128 a request, the other's grows with each 24 (head_dim 256: 8) of them;
 // over 131072 cached tokens in 8 requests (8 heads at head_dim 128 and 64, 2 at
-// 256) they take, in us, at
-//    64 rows  193 / 158 / 118 (tiles), 162 / 126 / 118 (few rows)
-//    96 rows  198 / 160       (tiles), 202 / 175       (few rows)
-//   128 rows              154 (tiles),             206 (few rows).
+// 256) they take, in us,
+//    64 rows  179 / 117 / 100 (tiles), 150 /  98 / 100 (few rows)
+//    80 rows  184 / 119 / 108 (tiles), 193 / 125 / 122 (few rows)
+//    96 rows  185 / 121 / 116 (tiles), 193 / 125 / 144 (few rows)
+//   128 rows  190 / 126 / 137 (tiles), 282 / 177 / 187 (few rows),
+// in calls of one kind: in a call that has both, the few-rows kernel is sized for one
+// token (few_rows below), and 60 requests of 5 tokens over 4096 take 157 us instead of 110.
 constexpr int kTileMinRows = 96;
 bool has_tiles(int32_t G, int32_t max_q_len) { return (int64_t)G * max_q_len >= kTileMinRows; }
 // Rows that the other kernel's CTAs take: those of the longest request, or of

@@ -32,12 +32,13 @@
 //     tile, head) that spans CTAs leaves partial results in the workspace, and
 //     the CTA that brings the last one merges them (in the CTAs' order, so the
 //     result does not depend on which one that is).
-// What bounds it: with long caches the steady state reads 4.7 TB/s (4 x 131072
-// tokens, 8 heads, head_dim 128: 604 MB in 128 us), where the conversions (ALU
-// pipe 52 % of all cycles, two cycles each) and the multiplications (half rate)
-// leave little more; expanding and multiplying a 16-token tile alone takes 155 ns
-// of each scheduler, 66 % of what it then takes in all.  A single 131072-token
-// request (151 MB, 22 us at the measured 6.78 TB/s) takes 42 us: about 7 us until
+// What bounds it: with long caches the steady state reads 5.4 TB/s (4 x 131072
+// tokens, 8 heads, head_dim 128: 604 MB in 112 us).  No pipe is full (ALU 51 %,
+// issue 55 % of all cycles over 128 ragged requests): expanding and multiplying a
+// 16-token tile alone takes 155 ns of each scheduler, 66 % of what it then takes
+// in all, and with 12 warps an SM the fixed latencies between the steps of a tile
+// stay in the open.  A single 131072-token
+// request (151 MB, 22 us at the measured 6.78 TB/s) takes 41 us: about 7 us until
 // the first tiles are there, 25 to 30 of reading, 6 for the two merges.  128
 // ragged requests (579 MB): 117 us, 5.0 TB/s.
 #include <cuda_bf16.h>

@@ -8,10 +8,12 @@
 // expand it from registers into the swizzled shared-memory layout that the
 // tensor cores read, ahead of the products.
 // Measured: 1024 tokens over 33792 (32 query heads, 8 key/value heads, head_dim
-// 128) in 546 us, 1020 TFLOP/s; tensor pipe 42 to 51 % of all cycles.  Without
-// the expansion (timed once, results wrong) it would be 474 us, the rate of the ring
-// forward: the softmax of one Q tile beside the other's products sets the period,
-// and the expanding warps share its schedulers and the shared-memory bandwidth.
+// 128) in 555 us, 1010 TFLOP/s; tensor pipe 41 % of all cycles.  Without the
+// expansion (timed once, results wrong) it would be 474 us, the rate of the ring
+// forward, where the softmax of one Q tile beside the other's products sets the
+// period; the expanding warps share its schedulers and the shared-memory bandwidth.
+// A unit of few key tiles costs about 16 us besides them (query rows, first tiles
+// and output follow one another): 32 prompts of 256 tokens and 32 heads take 171 us.
 
 // Warp roles (512 threads):
 //   warps 0, 1    UMMA issuers of Q tiles 0 and 1 (warp 0 owns tensor memory)

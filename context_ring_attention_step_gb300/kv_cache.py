@@ -146,11 +146,11 @@ def kv4_tables(kv_lens, new_lens, block_table, page_size, num_slots, free_pages=
     and tokens it adds, -1 for a request that leaves.  ``block_table`` [R, W] and
     ``free_pages`` [N] are updated in place; ``free_pages=None`` only maps (the
     block table already holds the pages; the free count is handed on, 0 if there is
-    none).  ``num_slots``: length of the slot map
-    (-1 behind the last new token).  ``out`` may name ``kv_lens`` and
-    ``free_count`` themselves as outputs.  A step that cannot be done (not
-    enough pages, ...) changes nothing and says so in ``status``;
-    ``check=True`` synchronises and raises.
+    none).  ``num_slots``: length of the slot map (-1 behind the last new token).
+    ``out`` may name ``kv_lens`` and ``free_count`` themselves as outputs.  A step
+    that cannot be done (not enough pages, ...) changes nothing and says so in
+    ``status``; a step over pages that are none (negative) is made, and its status
+    says that.  ``check=True`` synchronises and raises.
     """
     lib = _library()
     dev, R = kv_lens.device, kv_lens.shape[0]
@@ -245,9 +245,14 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None,
     Request r brings rows ``cu_q[r]:cu_q[r+1]`` of ``q`` [Tq, Hq, d] (bf16, rows
     may be strided) and has ``kv_lens[r]`` cached tokens, the rows' own among
     them (``causal``: row i of n sees keys up to ``kv_lens[r] - n + i``).
-    ``max_q_len``: query tokens of the longest request (default Tq); it selects
-    the kernel variant.  Not differentiable.  ``check=True`` synchronises and
-    raises if the lengths, offsets or pages were out of range.
+    ``max_q_len``: query tokens of the longest request.  It selects the kernels,
+    so give it: the default, Tq, is right for one request, but lets a step of
+    single tokens launch the kernel of long requests too (128 of them over 2000
+    tokens: 75 us instead of 69) and makes the default workspace a large one.
+    ``scale`` <= 0 or None selects 1/sqrt(d).  Not differentiable.
+    ``check=True`` synchronises and raises if the lengths, offsets or pages were
+    out of range; without it, look at ``kv4_status(workspace)`` now and then: keys
+    on pages outside the cache are left out of the rows silently.
     """
     lib = _library()
     if q.requires_grad and torch.is_grad_enabled():
