@@ -953,3 +953,35 @@ def test_streams_and_graphs_over_many_units(ra):
                 with torch.cuda.stream(st):
                     run(i)
         check()
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", [
+    (64, 600, 300, [100, 33], [2, 1]), (128, 4096, 1, [70, 40], [3, 1]), (128, 300, 300, [200, 100], [110, 1]),
+    (64, 2, 1, [60 + i % 50 for i in range(5000)], [50 if i % 7 == 0 else 1 for i in range(5000)])])
+def test_many_heads_and_requests(ra, d, Hq, Hkv, lens, qlens):
+    run_units(ra, Case(ra, Hq, lens, qlens, Hq, Hkv, d, 16), max(qlens))
+
+
+@pytest.mark.parametrize("d,n,log", [(64, 1, 27), (128, 1, 28), (64, 100, 26)])
+def test_very_long_request(ra, d, n, log):
+    """2^26 to 2^28 cached tokens (a table that repeats seven pages).  An accumulator takes the L / (16 x 152) tiles of 16
+    keys of its part at most, each addition off by at most 2^-23 of the sum, in o and in l."""
+    rng = np.random.default_rng(log)
+    page, P, L = 256, 7, 1 << log
+    cache = ra.Kv4Cache(P, page, 1, d)
+    k, v = bf16(rng, P * page, 1, d), bf16(rng, P * page, 1, d)
+    ra.kv4_store(cache, k.cuda(), v.cuda(), torch.arange(P * page).cuda())
+    k, v = O.rounded(f64(k))[:, 0], O.rounded(f64(v))[:, 0]
+    table = (torch.arange(L // page, device="cuda") % P).int()[None]
+    q = bf16(rng, n, 1, d)
+    o, lse = ra.kv4_attention(q.cuda(), cache, table, torch.tensor([L], dtype=torch.int32).cuda(),
+                              torch.tensor([0, n], dtype=torch.int32).cuda(), causal=False, o_fp32=True, max_q_len=n, check=True)
+    times = np.array([(L // page - p + P - 1) // P for p in range(P)]).repeat(page)
+    s = f64(q)[:, 0] @ k.T / math.sqrt(d)
+    m = s.max(1, keepdims=True)
+    w = np.exp(s - m) * times
+    z = w.sum(1, keepdims=True)
+    e_s = math.sqrt(d) * 2.0 ** -23 * np.abs(f64(q)).max() * np.abs(k).sum(-1).max()
+    e = L / (16 * 152) * 2.0 ** -23 + 2.0 ** -11 + 2.0 ** -20 + 2 * e_s
+    assert np.abs(f64(o)[:, 0] - (w / z) @ v).max() <= 2 * e * np.abs(v).max()
+    assert np.abs(f64(lse)[0] - (m + np.log(z))[:, 0]).max() <= e
