@@ -26,6 +26,13 @@ ra_status cuda_fail(cudaError_t e, const char* what) { return fail(RA_ERR_CUDA, 
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Do `na` bytes at a and `nb` at b share any?  (Outputs that lie over what the call reads, or
+// over one another, are refused: CTAs would read what others have written.)
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
 constexpr size_t kHeader = 256;
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -140,7 +147,21 @@ ra_status ra_kv4_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t
   for (const void* w : words)
     if (!aligned(w, 4)) return fail(RA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
   if (!aligned(slot_map, 8)) return fail(RA_ERR_INVALID_ARG, "slot_map must be 8-byte aligned");
-  if (kv_lens_out == new_lens) return fail(RA_ERR_INVALID_ARG, "kv_lens_out may replace kv_lens, not new_lens");
+  // Arrays that are written, then those that are only read; an output may be the input
+  // that it replaces.
+  const size_t R4 = (size_t)num_requests * 4, table_bytes = ((size_t)(num_requests - 1) * table_stride + table_width) * 4;
+  const struct { const void* at; size_t bytes; const char* name; } arrays[] = {
+      {kv_lens_out, R4, "kv_lens_out"}, {cu_new, R4 + 4, "cu_new"}, {slot_map, (size_t)num_slots * 8, "slot_map"},
+      {positions, (size_t)num_slots * 4, "positions"}, {free_count_out, 4, "free_count_out"}, {status, 4, "status"},
+      {block_table, table_bytes, "block_table"}, {free_pages, (size_t)num_pages * 4, "free_pages"},
+      {kv_lens, R4, "kv_lens"}, {new_lens, R4, "new_lens"}, {free_count, 4, "free_count"}};
+  for (int i = 0; i < 8; ++i)
+    for (int j = i + 1; j < 11; ++j) {
+      if (arrays[i].at == arrays[j].at && ((i == 0 && j == 8) || (i == 4 && j == 10))) continue;
+      if (overlap(arrays[i].at, arrays[i].bytes, arrays[j].at, arrays[j].bytes))
+        return fail(RA_ERR_INVALID_ARG, "%s lies over %s (only kv_lens_out may be kv_lens, and free_count_out free_count)",
+                    arrays[i].name, arrays[j].name);
+    }
   ra::Kv4TablesParams p{kv_lens, new_lens, block_table, table_stride, table_width, num_requests,
                         page_shift(page_size), free_pages, num_pages, free_count, num_slots, kv_lens_out, cu_new,
                         slot_map, positions, free_count_out, status};
@@ -184,6 +205,10 @@ ra_status ra_kv4_load(const ra_kv4_cache* cache, const int64_t* slot_map, int64_
   const int64_t row = cache ? (int64_t)cache->num_kv_heads * cache->head_dim : 0;
   ra_status rs = check_rows(cache, k, row, v, row, slot_map, num_tokens, &p);
   if (rs != RA_OK || num_tokens == 0) return rs;
+  const size_t bytes = (size_t)num_tokens * row * 2;
+  if (overlap(k, bytes, v, bytes) || overlap(k, bytes, slot_map, (size_t)num_tokens * 8) ||
+      overlap(v, bytes, slot_map, (size_t)num_tokens * 8))
+    return fail(RA_ERR_INVALID_ARG, "k and v must not lie over one another or over slot_map");
   p.k_out = k;
   p.v_out = v;
   const cudaError_t e = ra::launch_kv4_load(cache->head_dim, p, reinterpret_cast<cudaStream_t>(stream));
@@ -241,6 +266,10 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
   if (num_q_tokens > 1 && (q_stride < row || q_stride % 8))
     return fail(RA_ERR_INVALID_ARG, "q row stride %lld: a multiple of 8 elements, at least %lld", (long long)q_stride,
                 (long long)row);
+  const size_t q_bytes = ((size_t)(num_q_tokens - 1) * (num_q_tokens > 1 ? q_stride : row) + row) * 2;
+  const size_t o_bytes = (size_t)num_q_tokens * row * (o_is_fp32 ? 4 : 2), lse_bytes = (size_t)num_q_tokens * num_q_heads * 4;
+  if (overlap(o, o_bytes, q, q_bytes) || overlap(lse, lse_bytes, q, q_bytes) || overlap(o, o_bytes, lse, lse_bytes))
+    return fail(RA_ERR_INVALID_ARG, "o and lse must not lie over q or over one another");
   if (!std::isfinite(softmax_scale)) return fail(RA_ERR_INVALID_ARG, "softmax_scale is not finite");
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -478,6 +478,8 @@ ra_status ra_kv4_cache_bytes(int64_t num_pages, int32_t page_size, int32_t num_k
  *     page that it took, gave back or put tokens behind is negative, and the tokens
  *     there have slot -1.
  * A page must occur only once in the free list and the block table together.
+ * No output lies over another array, but kv_lens_out may be kv_lens and
+ * free_count_out may be free_count.
  */
 ra_status ra_kv4_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t num_requests, int32_t* block_table,
                         int32_t table_width, int64_t table_stride, int32_t page_size, int32_t* free_pages,
@@ -500,7 +502,7 @@ ra_status ra_kv4_store(const ra_kv4_cache* cache, const void* k, int64_t k_strid
  * Read cached rows: k, v bf16 [num_tokens, num_kv_heads, head_dim] (dense)
  * receive the values in slots slot_map[t], exactly (6 significant bits fit
  * bf16); rows with a negative slot, or one outside the cache, become zero.
- * Slots may repeat.
+ * Slots may repeat.  k and v must not lie over one another.
  */
 ra_status ra_kv4_load(const ra_kv4_cache* cache, const int64_t* slot_map, int64_t num_tokens, void* k, void* v,
                       void* stream);
@@ -523,7 +525,7 @@ ra_status ra_kv4_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_h
  *   softmax_scale <= 0 selects 1/sqrt(head_dim).
  *   o [num_q_tokens, num_q_heads, head_dim]: bf16, or fp32 when o_is_fp32.
  *   lse fp32 [num_q_heads, num_q_tokens], natural log.
- * A row that sees no key gets o = 0 and lse = -inf; one that sees a key and has
+ * o and lse must not lie over q.  A row that sees no key gets o = 0 and lse = -inf; one that sees a key and has
  * an infinity or a NaN in its query becomes NaN, o and lse.  Rows outside
  * [cu_q[0], cu_q[R]) are left as they were.  The workspace (device, 256-byte
  * aligned) must be zero before its first use (a call leaves it ready for the

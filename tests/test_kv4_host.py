@@ -164,3 +164,34 @@ def test_python_checks(ra):
 def test_status_must_be_on_a_gpu(ra):
     with pytest.raises(ValueError, match="GPU"):
         ra.kv4_status(torch.zeros(1, dtype=torch.int32))
+
+
+def test_outputs_must_not_overlap(ra):
+    """Other CTAs read what one writes: refused, but for the lengths and the free count replaced in place."""
+    K, M = 1 << 10, 1 << 20
+
+    def tables(**change):
+        a = dict(lens=1 * M, new=2 * M, table=3 * M, free=4 * M, count=5 * M, out=6 * M, cu=7 * M, smap=8 * M, pos=9 * M,
+                 cout=10 * M, status=11 * M)
+        a.update(change)
+        return _status(ra, "ra_kv4_tables", a["lens"], a["new"], 4, a["table"], 8, 9, 64, a["free"], 10, a["count"], 16,
+                       a["out"], a["cu"], a["smap"], a["pos"], a["cout"], a["status"], None)
+    for change in (dict(out=2 * M), dict(out=1 * M + 4), dict(out=1 * M - 12), dict(cu=1 * M), dict(smap=9 * M - 8),
+                   dict(pos=3 * M + 34 * 4), dict(cout=1 * M + 8), dict(cout=11 * M), dict(status=7 * M + 16),
+                   dict(status=4 * M + 36), dict(free=3 * M + 24), dict(count=4 * M + 4)):
+        code, text = tables(**change)
+        assert code == 1 and "lies over" in text, change
+    load = lambda k, v, s: _status(ra, "ra_kv4_load", _cache_struct(ra), s, 3, k, v, None)
+    for k, v, s in ((M, M, K), (M, M + 3 * 512 - 16, K), (M, 2 * M, M + 8), (M, 2 * M, 2 * M + 8)):
+        code, text = load(k, v, s)
+        assert code == 1 and "lie over" in text
+    n = ctypes.c_size_t()
+    assert _status(ra, "ra_kv4_attention_workspace_bytes", 32, 8, 128, 1, ctypes.byref(n))[0] == 0
+
+    def attention(q=M, qs=5000, o=4 * M, lse=3 * M, f32=0):
+        return _status(ra, "ra_kv4_attention", _cache_struct(ra, heads=8), q, qs, 4, 32, 64, 8, 8, 64, 64, 4, 1, 1, 0.0, o,
+                       f32, lse, 4096, n.value, None)
+    for change in (dict(o=M), dict(o=M + 3 * 10000 + 8176), dict(o=M - 4 * 8192 + 16), dict(o=M - 4 * 8192 - 16, f32=1),
+                   dict(lse=M + 16), dict(lse=4 * M + 4 * 8192 - 4), dict(lse=4 * M - 508)):
+        code, text = attention(**change)
+        assert code == 1 and "lie over" in text, change
