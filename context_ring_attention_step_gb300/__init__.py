@@ -28,3 +28,12 @@ from .kv_cache import (  # noqa: F401
     kv4_tables,
     kv4_tables_out,
 )
+from .rope import (  # noqa: F401
+    QkNormRope,
+    Rotary,
+    qk_norm_rope,
+    qk_norm_rope_bwd,
+    qk_norm_rope_fwd,
+    qk_norm_rope_workspace,
+    rope_positions,
+)

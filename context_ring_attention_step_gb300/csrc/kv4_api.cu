@@ -24,14 +24,9 @@ ra_status fail(ra_status st, const char* fmt, ...) {
 }
 ra_status cuda_fail(cudaError_t e, const char* what) { return fail(RA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Do `na` bytes at a and `nb` at b share any?  (Outputs that lie over what the call reads, or
-// over one another, are refused: CTAs would read what others have written.)
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && na && nb && x < y + nb && y < x + na;
-}
+using ra::aligned;
+using ra::overlap;
+using ra::sm_count;
 
 constexpr size_t kHeader = 256;
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -81,18 +76,6 @@ bool has_tiles(int32_t G, int32_t max_q_len) { return (int64_t)G * max_q_len >= 
 // one token where the tile kernel takes the long ones.
 int64_t few_rows(int32_t G, int32_t max_q_len) {
   return has_tiles(G, max_q_len) ? G : (int64_t)G * max_q_len;
-}
-
-// SMs of the current device (a property of the hardware: asked once).
-cudaError_t sm_count(int* sms) {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
-  return e;
 }
 
 struct AttnLayout {

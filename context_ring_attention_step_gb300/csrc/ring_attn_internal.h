@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
+#include <cstddef>
 #include <cstdint>
 
 #include "../../include/ring_attn.h"
@@ -68,6 +70,27 @@ struct BwdParams {
   int* status;
   int32_t next_cta;    // CTAs resident at once (one per SM)
 };
+
+// SMs of the current device (a property of the hardware: asked once).
+inline cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
+}
+
+// Do `na` bytes at a and `nb` at b share any?  (Outputs that lie over what a call reads, or
+// over one another, are refused: CTAs would read what others have written.)
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Record `msg` as this thread's last error text and return `st`.
 ra_status set_last_error(ra_status st, const char* msg);

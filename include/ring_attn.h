@@ -396,6 +396,77 @@ ra_status ra_fwd_noalloc(const ra_plan* plan, const void* q, const void* k, cons
 ra_status ra_noalloc_status(void* stream);
 
 /* ------------------------------------------------------------------------
+ * Norms of queries and keys for each head, and the position rotation
+ * ------------------------------------------------------------------------
+ * What makes ra_fwd's q and k from a projection's output, in one pass.  No
+ * counterpart on the pages; a library convenience with ra_fwd's conventions
+ * (THD rows, bf16, fp32 inside and one rounding at the end).
+ *
+ * A row x of head_dim elements (one head of one token) at position p becomes
+ *   u = x w / sqrt(mean x^2 + eps)          (norm = 0: u = x)
+ *   y_a = u_a cos t - u_b sin t,  y_b = u_b cos t + u_a sin t,  t = p f_i
+ * for the pairs (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * interleaved, i < rotary_dim / 2; elements from rotary_dim on are y = u.
+ * The weights w [head_dim] are the heads' in common (fp32, or bf16 when
+ * weights_bf16; NULL: ones).  f_i is held as the turns per position in 2^-64
+ * (ra_rope_turns), so that p f_i loses nothing at any position.
+ *
+ * positions int32 [num_tokens], device: every token's place in its document
+ * (or, while generating, in its request: ra_kv4_tables writes them).  Rows at a
+ * negative position are no tokens: they become zero, and add nothing to a
+ * gradient.
+ */
+typedef struct ra_norm_rope {
+  int64_t num_tokens;      /* < 2^31 */
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;        /* 64, 128 or 256 */
+  int32_t rotary_dim;      /* 0: no rotation; a multiple of 16 (interleaved: of 2) up to head_dim */
+  int32_t interleaved;
+  int32_t norm;
+  float eps;
+  int32_t weights_bf16;
+  const int32_t* positions;
+  const uint64_t* turns;   /* device, [rotary_dim / 2] */
+  const void* q_weight;
+  const void* k_weight;
+} ra_norm_rope;
+
+/*
+ * Frequencies for ra_norm_rope, on the host: turns[i] (i < rotary_dim / 2) of
+ * the angles inv_freq[i] a position, or base^(-2 i / rotary_dim) where inv_freq
+ * is NULL; at most a turn (2 pi) a position.
+ */
+ra_status ra_rope_turns(int32_t rotary_dim, double base, const double* inv_freq, uint64_t* turns);
+
+/*
+ * q [num_tokens, num_q_heads, head_dim] and k [num_tokens, num_kv_heads,
+ * head_dim], bf16, rows *_stride elements apart (multiples of 8: slices of a
+ * fused projection's output go in, and come out, as they are).  q_out may be q
+ * and k_out k (same pointer and stride); nothing else may lie over an output.
+ */
+ra_status ra_qk_norm_rope_fwd(const ra_norm_rope* shape, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                              void* stream);
+
+/* Workspace bytes of ra_qk_norm_rope_bwd where it takes weight gradients. */
+ra_status ra_qk_norm_rope_workspace_bytes(int32_t head_dim, size_t* bytes);
+
+/*
+ * Gradients.  q, k: the forward's inputs; gq, gk: gradients of its results
+ * (bf16, or fp32 when g_is_fp32; strides multiples of 8 or 4); dq, dk: bf16.
+ * dq_weight, dk_weight fp32 [head_dim], or NULL where they are not wanted: sums
+ * over all tokens and heads, in an order that depends on the shape alone.  The
+ * workspace (256-byte aligned; its content does not matter) is only needed for
+ * those.  Outputs lie over nothing else.
+ */
+ra_status ra_qk_norm_rope_bwd(const ra_norm_rope* shape, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* gq, int64_t gq_stride, const void* gk, int64_t gk_stride,
+                              int32_t g_is_fp32, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                              float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
  * Key/value cache held in 4 bits, and attention over it
  * ------------------------------------------------------------------------
  * For generating tokens after a prompt: the prompt's keys and values (the
