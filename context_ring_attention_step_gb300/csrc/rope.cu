@@ -10,12 +10,12 @@
 //   dw = sum over tokens and heads of h r x,   dx = r (h w - r x mean(h w r x)).
 //
 // Both only move bytes: 4 D a row forward, 6 D backward.  Hence
-//   * a row lies on D / 8 lanes, one 16-byte word each; its sum of squares is a
-//     few shuffles, and so is the way to the other element of a pair (raw bf16,
-//     four words), so nothing passes through shared memory but the angles;
+//   * a row lies on D / 8 lanes, eight elements each: four neighbours and the other
+//     elements of their pairs, so that a pair never crosses lanes; the sum of squares is a
+//     few shuffles, and nothing passes through shared memory but the angles;
 //   * norm weight and angle make one coefficient of the own and one of the other
-//     element, taken once a token and used for all its heads:
-//     y = r (x cw + x' sw);
+//     element, taken once a token and used for all its heads: y_a = r (x_a ca + x_b sa).
+//     Arithmetic runs on pairs of fp32 numbers (one instruction for two);
 //   * the angle is the product of p and the frequency in turns as a 64-bit
 //     fixed-point fraction, where whole turns fall out exactly: at position 2^20
 //     an fp32 product would be off by 0.03 of a radian.
@@ -33,47 +33,65 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+// CTAs of 8 warps an SM, and rows (of 32 lanes) that a warp has on the way at once.  The grids
+// are as many CTAs as run at the same time.  32768 tokens of 40 heads (head_dim 128) take forward
+// 131, 106 and 107 us with 2, 3 and 4 CTAs of 4 rows; 65536 tokens backward 551 us as 3 x 1, 478
+// as 3 x 2, 395 as 2 x 2, 327 as 2 x 4: what is on the way counts, more than the warps do.
+constexpr int kFwdCtas = 3, kFwdRows = 4, kBwdCtas = 2, kBwdRows = 4;
 
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint64_t widen(uint32_t w) {  // two bf16 numbers
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float f2_sum(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return a + b;
+}
+__device__ __forceinline__ uint64_t f2_both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ uint64_t f2_neg(uint64_t x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t f2_swap(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return f2_pack(b, a);
+}
+__device__ __forceinline__ uint32_t narrow(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return pack_bf16x2(a, b);
+}
 
-// Eight elements of a row as a lane holds them: bf16 (four words) or fp32 (eight).
+// A lane's eight elements of a row, as they came: four at `a`, four at `b` (bf16, or fp32).
 template <bool kFp32>
 struct Vec {
-  uint32_t w[kFp32 ? 8 : 4];
-  __device__ __forceinline__ void load(const void* p, int64_t off) {
-    if (kFp32) {
-      const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + off);
-      const uint4 a = s[0], b = s[1];
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[kFp32 ? 4 : 0] = b.x; w[kFp32 ? 5 : 0] = b.y; w[kFp32 ? 6 : 0] = b.z; w[kFp32 ? 7 : 0] = b.w;
+  uint4 w;      // bf16: a in x, y, b in z, w
+  uint4 w2;     // fp32: a in w, b here
+  typedef typename std::conditional<kFp32, float, __nv_bfloat16>::type T;
+  __device__ __forceinline__ void load(const T* a, int b) {  // b: from there to the other four
+    if constexpr (kFp32) {
+      w = *reinterpret_cast<const uint4*>(a);
+      w2 = *reinterpret_cast<const uint4*>(a + b);
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + off);
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      const uint2 x = *reinterpret_cast<const uint2*>(a), y = *reinterpret_cast<const uint2*>(a + b);
+      w = make_uint4(x.x, x.y, y.x, y.y);
     }
   }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < (kFp32 ? 8 : 4); ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ float at(int i) const {
-    if (kFp32) return __uint_as_float(w[i % (kFp32 ? 8 : 4)]);
-    return i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1]);
-  }
-  // The other elements of the pairs; zero where an element is not rotated
-  // (mask), so that an infinity there does not meet the coefficient 0.
-  template <bool kInter>
-  __device__ __forceinline__ Vec partner(int from, const uint32_t (&mask)[4]) const {
-    Vec r;
-#pragma unroll
-    for (int i = 0; i < (kFp32 ? 8 : 4); ++i) {
-      if (!kInter) r.w[i] = __shfl_sync(0xffffffffu, w[i], from) & mask[kFp32 ? i >> 1 : i];
-      else if (kFp32) r.w[i] = w[i ^ 1] & mask[i >> 1];
-      else r.w[i] = __byte_perm(w[i], 0, 0x1032) & mask[i % 4];
+  __device__ __forceinline__ void clear() { w = w2 = make_uint4(0u, 0u, 0u, 0u); }
+  // fp32 pairs: elements a, a + 1; a + 2, a + 3; the same of b
+  __device__ __forceinline__ void get(uint64_t (&x)[4]) const {
+    if (kFp32) {
+      x[0] = f2_pack(__uint_as_float(w.x), __uint_as_float(w.y));
+      x[1] = f2_pack(__uint_as_float(w.z), __uint_as_float(w.w));
+      x[2] = f2_pack(__uint_as_float(w2.x), __uint_as_float(w2.y));
+      x[3] = f2_pack(__uint_as_float(w2.z), __uint_as_float(w2.w));
+    } else {
+      x[0] = widen(w.x); x[1] = widen(w.y); x[2] = widen(w.z); x[3] = widen(w.w);
     }
-    return r;
   }
 };
+__device__ __forceinline__ void store(__nv_bfloat16* a, int b, const uint64_t (&x)[4]) {
+  *reinterpret_cast<uint2*>(a) = make_uint2(narrow(x[0]), narrow(x[1]));
+  *reinterpret_cast<uint2*>(a + b) = make_uint2(narrow(x[2]), narrow(x[3]));
+}
 
 template <int D>
 __device__ __forceinline__ float row_sum(float v) {
@@ -102,9 +120,33 @@ __device__ __forceinline__ float row_scale(uint32_t top, float eps) {
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
+// The row times that power of two, and the power: what a row with a far sum is scaled by.
+template <int D>
+__device__ __forceinline__ float scale_row(uint64_t (&x)[4], float eps, bool far) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f2_unpack(x[i], a, b);
+    top = max(top, max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
+  }
+  const float down = row_scale(row_max<D>(top), eps);
+  if (!far) return 1.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], f2_both(down));
+  return down;
+}
+__device__ __forceinline__ float square_sum(const uint64_t (&x)[4]) {
+  uint64_t s = f2_mul(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = f2_fma(x[i], x[i], s);
+  return f2_sum(s);
+}
+
 // cos and sin of a token's angles, j = 0 .. rot / 2 - 1, by one warp.
 __device__ __forceinline__ void angles(const RopeParams& p, int32_t pos, float2* table, int lane) {
   __syncwarp();
+#pragma unroll 1
   for (int j = lane; j < p.rot / 2; j += 32) {
     const uint64_t turn = p.turns[j] * (uint64_t)(uint32_t)pos;
     float s, c;
@@ -114,167 +156,190 @@ __device__ __forceinline__ void angles(const RopeParams& p, int32_t pos, float2*
   __syncwarp();
 }
 
-// What a lane needs to know of its eight elements.
+// The elements of a row that a lane holds: a .. a + 3 and b .. b + 3.
+//   half layout: the first rot / 8 lanes hold pairs (i, i + rot / 2), the others
+//     neighbours behind the rotated part; interleaved: eight neighbours.
 template <int D, bool kInter>
 struct Lane {
-  int e0, from;       // first element; lane that holds the pairs' other elements (half layout)
-  uint32_t mask[4];   // all ones where a pair of elements (2i, 2i + 1 of the lane) is rotated
-  int first;          // angle of element 0 (half layout)
-  float sign;         // of the sine, half layout: - for the first half
+  int a, b;
+  bool turns;  // half layout: the lane's elements are rotated
   __device__ __forceinline__ Lane(const RopeParams& p, int lane) {
-    constexpr int LPR = D / 8;
-    const int ch = lane % LPR, half = p.rot / 16;
-    e0 = 8 * ch;
-    from = lane;
-    first = 0;
-    sign = 0.f;
+    const int l = lane % (D / 8);
+    turns = !kInter && 8 * l < p.rot;
+    a = turns ? 4 * l : 8 * l;
+    b = turns ? 4 * l + p.rot / 2 : 8 * l + 4;
+  }
+  // Cosines and sines of the pairs (half layout: c[0], c[1] for a .. a + 3 and again for
+  // b; interleaved: both elements of a pair alike).  Elements that are not rotated: 1 and 0.
+  __device__ __forceinline__ void angles_of(const RopeParams& p, const float2* table, uint64_t (&c)[4],
+                                            uint64_t (&s)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mask[i] = e0 + 2 * i < p.rot ? 0xffffffffu : 0u;
-    if (!kInter && e0 < p.rot) {
-      from = ch < half ? lane + half : lane - half;
-      first = e0 < p.rot / 2 ? e0 : e0 - p.rot / 2;
-      sign = ch < half ? -1.f : 1.f;
+    for (int i = 0; i < 4; ++i) {
+      if (kInter) {
+        const int e = (i < 2 ? a : b - 4) + 2 * i;  // (b = a + 4)
+        const float2 t = e < p.rot ? table[e >> 1] : make_float2(1.f, 0.f);
+        c[i] = f2_both(t.x);
+        s[i] = f2_pack(-t.y, t.y);
+      } else if (i < 2) {
+        float2 t = make_float2(1.f, 0.f), u = t;
+        if (turns) {
+          t = table[a + 2 * i];
+          u = table[a + 2 * i + 1];
+        }
+        c[i] = c[i + 2] = f2_pack(t.x, u.x);
+        s[i] = f2_pack(-t.y, -u.y);
+        s[i + 2] = f2_pack(t.y, u.y);
+      }
     }
   }
-  // cosine and signed sine of element i
-  __device__ __forceinline__ float2 turn(const float2* table, int i) const {
-    if (!mask[i >> 1]) return make_float2(1.f, 0.f);
-    if (kInter) {
-      const float2 t = table[(e0 + i) >> 1];
-      return make_float2(t.x, i & 1 ? t.y : -t.y);
+  // The other elements of the pairs; zero where nothing turns, so that an infinity there
+  // does not meet the coefficient 0.
+  __device__ __forceinline__ void others(const RopeParams& p, const uint64_t (&x)[4], uint64_t (&o)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (kInter) o[i] = a + 2 * i < p.rot ? f2_swap(x[i]) : 0ull;
+      else o[i] = turns ? x[i ^ 2] : 0ull;
     }
-    const float2 t = table[first + i];
-    return make_float2(t.x, sign * t.y);
+  }
+  __device__ __forceinline__ void weights(const float* w, uint64_t (&v)[4]) const {
+    const float4 x = *reinterpret_cast<const float4*>(w + a), y = *reinterpret_cast<const float4*>(w + b);
+    v[0] = f2_pack(x.x, x.y);
+    v[1] = f2_pack(x.z, x.w);
+    v[2] = f2_pack(y.x, y.y);
+    v[3] = f2_pack(y.z, y.w);
   }
 };
 
-// Weight of element e (the pair's other element is weighted too).
-__device__ __forceinline__ float weight(const RopeParams& p, const void* w, int e) {
-  if (!w) return 1.f;
-  return p.w_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[e]) : reinterpret_cast<const float*>(w)[e];
-}
-template <int D, bool kInter>
-__device__ __forceinline__ int other(const RopeParams& p, const Lane<D, kInter>& ln, int i) {
-  if (!ln.mask[i >> 1]) return ln.e0 + i;
-  if (kInter) return ln.e0 + (i ^ 1);
-  return ln.e0 + i + (ln.sign < 0.f ? p.rot / 2 : -(p.rot / 2));
+// Both weights as fp32, ones where there is none.
+template <int D>
+__device__ __forceinline__ void read_weights(const RopeParams& p, float (&w)[2][D]) {
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const void* src = i < D ? p.w[0] : p.w[1];
+    const int e = i % D;
+    w[i / D][e] = !src      ? 1.f
+                  : p.w_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src)[e])
+                             : reinterpret_cast<const float*>(src)[e];
+  }
+  __syncthreads();
 }
 
-// Work of one warp at a time: row groups (32 / (D / 8) neighbouring heads, one pass of the
-// lanes) of one token.  Either all of its heads, the queries' first, or, where the tokens
+// Work of one warp at a time: one token, either all of its heads, or, where the tokens
 // alone would not fill the GPU, a share of one side's.
 struct Item {
   int64_t t;
-  int side, h, h1;  // side and first head; end of the heads on this side
-  bool both;        // goes on to the keys
+  int h0[2], h1[2];  // heads of either side
 };
 template <int RPW>
 __device__ __forceinline__ Item item_of(const RopeParams& p, int64_t it) {
   const int n = p.parts[0] + p.parts[1];
-  if (n == 0) return Item{it, 0, 0, p.H[0], true};
-  const int64_t t = it / n;
-  int part = (int)(it - t * n);
-  const int side = part >= p.parts[0];
-  if (side) part -= p.parts[0];
-  const int H = side ? p.H[1] : p.H[0], parts = side ? p.parts[1] : p.parts[0];
-  const int per = ((H + RPW - 1) / RPW + parts - 1) / parts * RPW;
-  return Item{t, side, min(part * per, H), min((part + 1) * per, H), false};
+  if (n == 0) return Item{it, {0, 0}, {p.H[0], p.H[1]}};
+  Item c{it / n, {0, 0}, {0, 0}};
+  const int part = (int)(it - c.t * n);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int k = part - (s ? p.parts[0] : 0);
+    if (k < 0 || k >= p.parts[s]) continue;
+    const int per = ((p.H[s] + RPW - 1) / RPW + p.parts[s] - 1) / p.parts[s] * RPW;
+    c.h0[s] = min(k * per, p.H[s]);
+    c.h1[s] = min(k * per + per, p.H[s]);
+  }
+  return c;
 }
-// On by n heads; false at the end.
-__device__ __forceinline__ bool advance(const RopeParams& p, Item& c, int n) {
-  c.h += n;
-  if (c.h < c.h1) return true;
-  if (!c.both || c.side) return false;
-  c.side = 1;
-  c.h = 0;
-  c.h1 = p.H[1];
-  return true;
+
+template <typename T>
+__device__ __forceinline__ T* at(const RopeRows& r, int64_t off) { return reinterpret_cast<T*>(r.p) + off; }
+
+// `n` heads of zeros.
+template <int D>
+__device__ __forceinline__ void zero_heads(__nv_bfloat16* y, int db, int n, int row) {
+  const uint64_t z[4] = {};
+  for (int h = row; h < n; h += 256 / D) store(y + h * D, db, z);
 }
 
 // ------------------------------------------------------------------ forward
 
+// One row (and those of the warp's other lanes) from x to y; `in`: it is one of the heads.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeParams p) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
+__device__ __forceinline__ void fwd_row(const RopeParams& p, const Lane<D, kInter>& ln, const Vec<false>& v,
+                                        const uint64_t (&ca)[4], const uint64_t (&sa)[4], __nv_bfloat16* y, bool in) {
+  uint64_t x[4], o[4];
+  v.get(x);
+  uint64_t r2 = f2_both(1.f);
+  if (p.norm) {
+    float ss = row_sum<D>(square_sum(x)), e = p.eps;
+    const bool far = in && far_out(ss, p.eps);
+    if (__any_sync(0xffffffffu, far)) {
+      const float down = scale_row<D>(x, p.eps, far);
+      const float s2 = row_sum<D>(square_sum(x));
+      if (far) {
+        ss = s2;
+        e = p.eps * down * down;
+      }
+    }
+    r2 = f2_both(rsqrtf(fmaf(ss, 1.f / D, e)));
+  }
+  ln.others(p, x, o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = f2_mul(f2_fma(x[i], ca[i], f2_mul(o[i], sa[i])), r2);
+  if (in) store(y, ln.b - ln.a, x);
+}
+
+template <int D, bool kInter>
+__global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const RopeParams p) {
+  constexpr int RPW = 256 / D, U = kFwdRows;  // rows of a warp at once, and how often before it waits for them
   extern __shared__ float2 s_angles[];
+  __shared__ __align__(16) float s_w[2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float2* table = s_angles + warp * (p.rot / 2);
   const Lane<D, kInter> ln(p, lane);
-  const int row = lane / LPR;
+  const int row = lane / (D / 8), db = ln.b - ln.a;
   const int64_t items = p.T * max(1, p.parts[0] + p.parts[1]);
+  read_weights<D>(p, s_w);
   for (int64_t it = blockIdx.x * (int64_t)kWarps + warp; it < items; it += gridDim.x * (int64_t)kWarps) {
-    Item c = item_of<RPW>(p, it);
+    const Item c = item_of<RPW>(p, it);
     const int32_t pos = p.pos[c.t];
-    auto load = [&](Vec<false> (&v)[U], const Item& at) {
-      const RopeRows x = at.side ? p.x[1] : p.x[0];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = at.h + u * RPW + row;
-        if (h < at.h1 && pos >= 0) v[u].load(x.p, at.t * x.stride + (int64_t)h * D + ln.e0);
-        else v[u].clear();
-      }
-    };
-    Vec<false> next[U];
-    load(next, c);  // on the way while the angles are taken
     if (pos >= 0 && p.rot > 0) angles(p, pos, table, lane);
-    float cw[8], sw[8];
-    int side = -1;
 #pragma unroll 1
-    for (bool more = true; more;) {
-      if (c.side != side) {
-        side = c.side;
-        const void* w = side ? p.w[1] : p.w[0];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 a = pos >= 0 ? ln.turn(table, i) : make_float2(0.f, 0.f);
-          cw[i] = a.x * weight(p, w, ln.e0 + i);
-          sw[i] = a.y * weight(p, w, other(p, ln, i));
-        }
+    for (int side = 0; side < 2; ++side) {
+      const int h0 = side ? c.h0[1] : c.h0[0], n = (side ? c.h1[1] : c.h1[0]) - h0;
+      if (n <= 0) continue;
+      const RopeRows& xr = side ? p.x[1] : p.x[0];
+      const RopeRows& yr = side ? p.y[1] : p.y[0];
+      const __nv_bfloat16* x = at<__nv_bfloat16>(xr, c.t * xr.stride + h0 * D + ln.a);
+      __nv_bfloat16* y = at<__nv_bfloat16>(yr, c.t * yr.stride + h0 * D + ln.a);
+      if (pos < 0) {
+        zero_heads<D>(y, db, n, row);
+        continue;
       }
-      Vec<false> v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = next[u];
-      const Item at = c;
-      more = advance(p, c, U * RPW);
-      if (more) load(next, c);
-      const RopeRows y = side ? p.y[1] : p.y[0];
-      const int64_t yo = at.t * y.stride + ln.e0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (at.h + u * RPW >= at.h1) break;
-        const int h = at.h + u * RPW + row;
-        float r = 1.f;
-        if (p.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[u].at(i), v[u].at(i), ss);
-          ss = row_sum<D>(ss);
-          r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-          const bool far = h < at.h1 && far_out(ss, p.eps);
-          if (__any_sync(0xffffffffu, far)) {
-            uint32_t top = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[u].at(i)) & 0x7fffffffu);
-            const float down = row_scale(row_max<D>(top), p.eps);
-            float s2 = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s2 = fmaf(v[u].at(i) * down, v[u].at(i) * down, s2);
-            s2 = row_sum<D>(s2);
-            if (far) r = rsqrtf(fmaf(s2, 1.f / D, p.eps * down * down)) * down;
-          }
-        }
-        const Vec<false> o = v[u].template partner<kInter>(ln.from, ln.mask);
-        uint32_t w[4];
+      uint64_t ca[4], sa[4];  // coefficients of the own and of the pair's other element
+      {
+        uint64_t w[4], wo[4];
+        ln.weights(s_w[side], w);
+        ln.others(p, w, wo);
+        ln.angles_of(p, table, ca, sa);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // (r first: the row times its coefficients alone may overflow, or lose small numbers)
-          const float a = fmaf(v[u].at(2 * i) * r, cw[2 * i], o.at(2 * i) * r * sw[2 * i]);
-          const float b = fmaf(v[u].at(2 * i + 1) * r, cw[2 * i + 1], o.at(2 * i + 1) * r * sw[2 * i + 1]);
-          w[i] = pos >= 0 ? pack_bf16x2(a, b) : 0u;
+          ca[i] = f2_mul(ca[i], w[i]);
+          sa[i] = f2_mul(sa[i], wo[i]);
         }
-        if (h < at.h1)
-          *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(y.p) + yo + (int64_t)h * D) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      x += row * D;
+      y += row * D;
+      int h = 0;
+#pragma unroll 1
+      for (; h + U * RPW <= n; h += U * RPW, x += U * RPW * D, y += U * RPW * D) {
+        Vec<false> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u].load(x + u * RPW * D, db);
+#pragma unroll
+        for (int u = 0; u < U; ++u) fwd_row<D, kInter>(p, ln, v[u], ca, sa, y + u * RPW * D, true);
+      }
+#pragma unroll 1
+      for (; h < n; h += RPW, x += RPW * D, y += RPW * D) {
+        Vec<false> v;
+        v.clear();
+        if (h + row < n) v.load(x, db);
+        fwd_row<D, kInter>(p, ln, v, ca, sa, y, h + row < n);
       }
     }
   }
@@ -282,151 +347,137 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeParams p) 
 
 // ------------------------------------------------------------------ backward
 
-template <int D, bool kInter, bool kFp32>
-__global__ void __launch_bounds__(kThreads, 2) rope_bwd_kernel(const RopeParams p) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 2;
-  extern __shared__ float2 s_angles[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <int D, bool kInter, bool kFp32, bool kNorm>
+__device__ __forceinline__ void bwd_row(const RopeParams& p, const Lane<D, kInter>& ln, const Vec<false>& v,
+                                        const Vec<kFp32>& g, const uint64_t (&cs)[4], const uint64_t (&sn)[4],
+                                        const uint64_t (&w)[4], uint64_t (&dw)[4], __nv_bfloat16* y, bool in) {
+  uint64_t x[4], d[4], o[4];
+  g.get(d);
+  ln.others(p, d, o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = f2_fma(d[i], cs[i], f2_mul(o[i], sn[i]));  // h
+  if (kNorm) {
+    v.get(x);
+    uint64_t hw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hw[i] = f2_mul(d[i], w[i]);
+    auto product = [&]() {
+      uint64_t s = f2_mul(hw[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) s = f2_fma(hw[i], x[i], s);
+      return f2_sum(s);
+    };
+    float ss = row_sum<D>(square_sum(x)), dot = row_sum<D>(product()), e = p.eps, down = 1.f;
+    const bool far = in && far_out(ss, p.eps);
+    if (__any_sync(0xffffffffu, far)) {
+      // as forward: r is the scaled row's then, and r x that of the row itself
+      down = scale_row<D>(x, p.eps, far);
+      const float s2 = row_sum<D>(square_sum(x)), d2 = row_sum<D>(product());
+      if (far) {
+        ss = s2;
+        dot = d2;
+        e = p.eps * down * down;
+      }
+    }
+    const float r = rsqrtf(fmaf(ss, 1.f / D, e));
+    const float mean = dot * r * (1.f / D);  // of h w r x
+    const uint64_t r2 = f2_both(r), m2 = f2_both(-mean), rd = f2_both(r * down);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t n = f2_mul(x[i], r2);
+      if (in) dw[i] = f2_fma(d[i], n, dw[i]);
+      d[i] = f2_mul(f2_fma(n, m2, hw[i]), rd);
+    }
+  }
+  if (in) store(y, ln.b - ln.a, d);
+}
+
+template <int D, bool kInter, bool kFp32, bool kNorm>
+__global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const RopeParams p) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = kBwdRows;
+  typedef typename Vec<kFp32>::T G;
+  extern __shared__ __align__(16) float2 s_angles[];
+  __shared__ __align__(16) float s_w[2][D];
+  // a lane's sums of the weights' gradients: in registers for one side of a token only
+  __shared__ __align__(16) uint64_t s_dw[2][4][kNorm ? kThreads : 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float2* table = s_angles + warp * (p.rot / 2);
   const Lane<D, kInter> ln(p, lane);
-  const int row = lane / LPR;
+  const int row = lane / LPR, db = ln.b - ln.a;
   const int64_t items = p.T * max(1, p.parts[0] + p.parts[1]);
-  float dwq[8], dwk[8];  // sums of the weights' gradients
+  if (kNorm) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
-
+    for (int i = 0; i < 4; ++i) s_dw[0][i][tid] = s_dw[1][i][tid] = 0ull;
+  }
+  read_weights<D>(p, s_w);
   for (int64_t it = blockIdx.x * (int64_t)kWarps + warp; it < items; it += gridDim.x * (int64_t)kWarps) {
-    Item c = item_of<RPW>(p, it);
+    const Item c = item_of<RPW>(p, it);
     const int32_t pos = p.pos[c.t];
-    auto load = [&](Vec<false> (&v)[U], Vec<kFp32> (&g)[U], const Item& at) {
-      const RopeRows x = at.side ? p.x[1] : p.x[0], gr = at.side ? p.g[1] : p.g[0];
+    uint64_t cs[4], sn[4];
+    if (pos >= 0) {
+      if (p.rot > 0) angles(p, pos, table, lane);
+      ln.angles_of(p, table, cs, sn);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = at.h + u * RPW + row;
-        const bool in = h < at.h1 && pos >= 0;
-        if (in && p.norm) v[u].load(x.p, at.t * x.stride + (int64_t)h * D + ln.e0);
-        else v[u].clear();
-        if (in) g[u].load(gr.p, at.t * gr.stride + (int64_t)h * D + ln.e0);
-        else g[u].clear();
-      }
-    };
-    Vec<false> v_next[U];
-    Vec<kFp32> g_next[U];
-    load(v_next, g_next, c);
-    if (pos >= 0 && p.rot > 0) angles(p, pos, table, lane);
-    float cs[8], sn[8];  // of the rotation by -t
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 a = pos >= 0 ? ln.turn(table, i) : make_float2(0.f, 0.f);
-      cs[i] = a.x;
-      sn[i] = -a.y;
+      for (int i = 0; i < 4; ++i) sn[i] = f2_neg(sn[i]);  // back, by -t
     }
-    float w[8];
-    int side = -1;
 #pragma unroll 1
-    for (bool more = true; more;) {
-      if (c.side != side) {
-        side = c.side;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = weight(p, side ? p.w[1] : p.w[0], ln.e0 + i);
+    for (int side = 0; side < 2; ++side) {
+      const int h0 = side ? c.h0[1] : c.h0[0], n = (side ? c.h1[1] : c.h1[0]) - h0;
+      if (n <= 0) continue;
+      const RopeRows& xr = side ? p.x[1] : p.x[0];
+      const RopeRows& gr = side ? p.g[1] : p.g[0];
+      const RopeRows& yr = side ? p.y[1] : p.y[0];
+      __nv_bfloat16* y = at<__nv_bfloat16>(yr, c.t * yr.stride + h0 * D + ln.a);
+      if (pos < 0) {
+        zero_heads<D>(y, db, n, row);
+        continue;
       }
-      Vec<false> v[U];
-      Vec<kFp32> g[U];
+      y += row * D;
+      const __nv_bfloat16* x = at<__nv_bfloat16>(xr, c.t * xr.stride + (h0 + row) * D + ln.a);
+      const G* g = at<G>(gr, c.t * gr.stride + (h0 + row) * D + ln.a);
+      uint64_t w[4], dw[4] = {};
+      ln.weights(s_w[side], w);
+      int h = 0;
+#pragma unroll 1
+      for (; h + U * RPW <= n; h += U * RPW, x += U * RPW * D, g += U * RPW * D, y += U * RPW * D) {
+        Vec<false> v[U];
+        Vec<kFp32> gv[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        v[u] = v_next[u];
-        g[u] = g_next[u];
-      }
-      const Item at = c;
-      more = advance(p, c, U * RPW);
-      if (more) load(v_next, g_next, c);
-      const RopeRows y = side ? p.y[1] : p.y[0];
-      const int64_t yo = at.t * y.stride + ln.e0;
-      float dw[8] = {};
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (at.h + u * RPW >= at.h1) break;
-        const Vec<kFp32> o = g[u].template partner<kInter>(ln.from, ln.mask);
-        const int h = at.h + u * RPW + row;
-        const bool in = h < at.h1 && pos >= 0;
-        float d[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = fmaf(g[u].at(i), cs[i], o.at(i) * sn[i]);
-        if (p.norm) {
-          float ss = 0.f, dot = 0.f, down = 1.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ss = fmaf(v[u].at(i), v[u].at(i), ss);
-            dot = fmaf(d[i] * w[i], v[u].at(i), dot);
-          }
-          ss = row_sum<D>(ss);
-          dot = row_sum<D>(dot);
-          float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-          const bool far = in && far_out(ss, p.eps);
-          if (__any_sync(0xffffffffu, far)) {
-            // as forward; the row itself is scaled (`down`), and r is the scaled row's
-            uint32_t top = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[u].at(i)) & 0x7fffffffu);
-            const float dn = row_scale(row_max<D>(top), p.eps);
-            float s2 = 0.f, d2 = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float xs = v[u].at(i) * dn;
-              s2 = fmaf(xs, xs, s2);
-              d2 = fmaf(d[i] * w[i], xs, d2);
-            }
-            s2 = row_sum<D>(s2);
-            d2 = row_sum<D>(d2);
-            if (far) {
-              r = rsqrtf(fmaf(s2, 1.f / D, p.eps * dn * dn));
-              dot = d2;
-              down = dn;
-            }
-          }
-          const float mean = dot * r * (1.f / D);  // of h w r x
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float n = v[u].at(i) * down * r;
-            if (in) dw[i] = fmaf(d[i], n, dw[i]);
-            d[i] = fmaf(-n, mean, d[i] * w[i]) * r * down;
-          }
+        for (int u = 0; u < U; ++u) {
+          if (kNorm) v[u].load(x + u * RPW * D, db);
+          gv[u].load(g + u * RPW * D, db);
         }
-        if (h < at.h1) {
-          uint4 out = make_uint4(0u, 0u, 0u, 0u);
-          if (pos >= 0)
-            out = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
-                             pack_bf16x2(d[6], d[7]));
-          *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(y.p) + yo + (int64_t)h * D) = out;
-        }
-      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dwq[i] += side ? 0.f : dw[i];
-        dwk[i] += side ? dw[i] : 0.f;
+        for (int u = 0; u < U; ++u)
+          bwd_row<D, kInter, kFp32, kNorm>(p, ln, v[u], gv[u], cs, sn, w, dw, y + u * RPW * D, true);
+      }
+#pragma unroll 1
+      for (; h < n; h += RPW, x += RPW * D, g += RPW * D, y += RPW * D) {
+        const bool in = h + row < n;
+        Vec<false> v;
+        Vec<kFp32> gv;
+        v.clear();
+        gv.clear();
+        if (in && kNorm) v.load(x, db);
+        if (in) gv.load(g, db);
+        bwd_row<D, kInter, kFp32, kNorm>(p, ln, v, gv, cs, sn, w, dw, y, in);
+      }
+      if (kNorm) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_dw[side][i][tid] = f2_add(s_dw[side][i][tid], dw[i]);
       }
     }
   }
-  if (!p.partials) return;
-  // this CTA's sums, in a fixed order: rows of a warp, then the warps
-  __shared__ float s_dw[kWarps][D];
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = side ? dwk[i] : dwq[i];
-#pragma unroll
-      for (int d = LPR; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-      if (row == 0) s_dw[warp][ln.e0 + i] = v;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < D; e += kThreads) {
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) v += s_dw[k][e];
-      p.partials[((size_t)blockIdx.x * 2 + side) * D + e] = v;
-    }
+  if (!kNorm || !p.partials) return;
+  // this CTA's sums, always in the same order: the lanes that hold the same elements, warp by warp
+  __syncthreads();
+  for (int i = tid; i < 2 * D / 2; i += kThreads) {
+    const int side = i / (D / 2), j = i % (D / 2) % 4, l = i % (D / 2) / 4;  // pair j of lane l of a row
+    uint64_t v = 0ull;
+    for (int k = l; k < kThreads; k += LPR) v = f2_add(v, s_dw[side][j][k]);
+    const Lane<D, kInter> o(p, l);
+    float* dst = p.partials + ((size_t)blockIdx.x * 2 + side) * D + (j < 2 ? o.a : o.b - 4) + 2 * j;
+    f2_unpack(v, dst[0], dst[1]);
   }
 }
 
@@ -448,27 +499,29 @@ __global__ void __launch_bounds__(256) rope_dw_kernel(const float* partials, int
   }
 }
 
-// A token's heads on one warp (parts 0) where the tokens alone fill the GPU, else each side's
-// shared out over some.
-int64_t share_out(RopeParams& p, int D, int sms) {
+// CTAs for this many tokens: a token's heads go to one warp (parts 0) where the tokens alone
+// fill the GPU, else each side's are shared out over some.
+unsigned share_out(RopeParams& p, int D, int sms, int per_sm) {
   const int rows_at_once = 256 / D;
-  const int64_t want = (int64_t)sms * 32;  // warps
+  const int64_t want = (int64_t)sms * per_sm * kWarps;  // warps that run at once
+  int64_t items = p.T;
   p.parts[0] = p.parts[1] = 0;
-  if (p.T >= want) return p.T;
-  const int g0 = (p.H[0] + rows_at_once - 1) / rows_at_once, g1 = (p.H[1] + rows_at_once - 1) / rows_at_once;
-  const int64_t warps = std::max<int64_t>(2, want / std::max<int64_t>(1, p.T));
-  const int per = (int)std::max<int64_t>(1, (g0 + g1 + warps - 1) / warps);  // row groups of a warp
-  p.parts[0] = (g0 + per - 1) / per;
-  p.parts[1] = (g1 + per - 1) / per;
-  return p.T * (p.parts[0] + p.parts[1]);
+  if (p.T < want) {
+    const int g0 = (p.H[0] + rows_at_once - 1) / rows_at_once, g1 = (p.H[1] + rows_at_once - 1) / rows_at_once;
+    const int64_t warps = std::max<int64_t>(2, want / std::max<int64_t>(1, p.T));
+    const int per = (int)std::max<int64_t>(1, (g0 + g1 + warps - 1) / warps);  // rows (of 32 lanes) of a warp
+    p.parts[0] = (g0 + per - 1) / per;
+    p.parts[1] = (g1 + per - 1) / per;
+    items *= p.parts[0] + p.parts[1];
+  }
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)sms * per_sm));
 }
 
 }  // namespace
 
 cudaError_t launch_rope_fwd(int D, bool interleaved, RopeParams p, int sms, cudaStream_t stream) {
   if (p.T == 0) return cudaSuccess;
-  const int64_t items = share_out(p, D, sms);
-  const unsigned ctas = (unsigned)std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)sms * 8);
+  const unsigned ctas = share_out(p, D, sms, kFwdCtas);
   const size_t smem = (size_t)kWarps * (p.rot / 2) * sizeof(float2);
   auto go = [&](auto kern) {
     kern<<<ctas, kThreads, smem, stream>>>(p);
@@ -482,22 +535,27 @@ cudaError_t launch_rope_fwd(int D, bool interleaved, RopeParams p, int sms, cuda
 
 cudaError_t launch_rope_bwd(int D, bool interleaved, bool g_fp32, RopeParams p, int sms, float* dw[2],
                             cudaStream_t stream) {
-  const int64_t items = share_out(p, D, sms);
-  const unsigned ctas = (unsigned)std::max<int64_t>(
-      1, std::min<int64_t>({(items + kWarps - 1) / kWarps, (int64_t)sms * 4, (int64_t)kRopeMaxCtas}));
+  sms = std::min(sms, kRopeMaxCtas / kBwdCtas);
+  const unsigned ctas = share_out(p, D, sms, kBwdCtas);
   const size_t smem = (size_t)kWarps * (p.rot / 2) * sizeof(float2);
   auto go = [&](auto kern) {
     kern<<<ctas, kThreads, smem, stream>>>(p);
     return cudaGetLastError();
   };
-  auto pick = [&](auto inter) {
-    constexpr bool I = decltype(inter)::value;
-    if (D == 64) return g_fp32 ? go(rope_bwd_kernel<64, I, true>) : go(rope_bwd_kernel<64, I, false>);
-    if (D == 128) return g_fp32 ? go(rope_bwd_kernel<128, I, true>) : go(rope_bwd_kernel<128, I, false>);
-    if (D == 256) return g_fp32 ? go(rope_bwd_kernel<256, I, true>) : go(rope_bwd_kernel<256, I, false>);
-    return cudaErrorInvalidValue;
+  auto pick = [&](auto inter, auto fp32, auto norm) {
+    constexpr bool I = decltype(inter)::value, F = decltype(fp32)::value, N = decltype(norm)::value;
+    return D == 64    ? go(rope_bwd_kernel<64, I, F, N>)
+           : D == 128 ? go(rope_bwd_kernel<128, I, F, N>)
+           : D == 256 ? go(rope_bwd_kernel<256, I, F, N>)
+                      : cudaErrorInvalidValue;
   };
-  cudaError_t e = interleaved ? pick(std::true_type{}) : pick(std::false_type{});
+  auto with_norm = [&](auto inter, auto fp32) {
+    return p.norm ? pick(inter, fp32, std::true_type{}) : pick(inter, fp32, std::false_type{});
+  };
+  auto with_type = [&](auto inter) {
+    return g_fp32 ? with_norm(inter, std::true_type{}) : with_norm(inter, std::false_type{});
+  };
+  const cudaError_t e = interleaved ? with_type(std::true_type{}) : with_type(std::false_type{});
   if (e != cudaSuccess || !p.partials) return e;
   rope_dw_kernel<<<2 * D / 32, 256, 0, stream>>>(p.partials, (int)ctas, D, dw[0], dw[1]);
   return cudaGetLastError();

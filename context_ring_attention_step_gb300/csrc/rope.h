@@ -33,7 +33,7 @@ struct RopeParams {
   float* partials;        // backward: [CTAs][2][D] sums of the weights' gradients, or null
 };
 
-constexpr int kRopeMaxCtas = 640;
+constexpr int kRopeMaxCtas = 320;  // of a backward pass: what its workspace holds
 cudaError_t launch_rope_fwd(int D, bool interleaved, RopeParams p, int sms, cudaStream_t stream);
 cudaError_t launch_rope_bwd(int D, bool interleaved, bool g_fp32, RopeParams p, int sms, float* dw[2],
                             cudaStream_t stream);

@@ -55,9 +55,9 @@ ra_status check_shape(const ra_norm_rope* r, ra::RopeParams* p) {
     return fail(RA_ERR_INVALID_ARG, "num_tokens %lld outside [0, 2^31)", (long long)r->num_tokens);
   if (r->num_q_heads < 1 || r->num_q_heads > 65536 || r->num_kv_heads < 1 || r->num_kv_heads > 65536)
     return fail(RA_ERR_INVALID_ARG, "num_q_heads %d, num_kv_heads %d outside [1, 65536]", r->num_q_heads, r->num_kv_heads);
-  if (r->rotary_dim < 0 || r->rotary_dim > r->head_dim || r->rotary_dim % (r->interleaved ? 2 : 16))
+  if (r->rotary_dim < 0 || r->rotary_dim > r->head_dim || r->rotary_dim % (r->interleaved ? 2 : 8))
     return fail(RA_ERR_UNSUPPORTED, "rotary_dim %d: a multiple of %d up to head_dim %d", r->rotary_dim,
-                r->interleaved ? 2 : 16, r->head_dim);
+                r->interleaved ? 2 : 8, r->head_dim);
   if (r->norm && !(r->eps >= 0.f && std::isfinite(r->eps))) return fail(RA_ERR_INVALID_ARG, "eps must be finite and not negative");
   if (!r->norm && (r->q_weight || r->k_weight)) return fail(RA_ERR_INVALID_ARG, "weights need the norm");
   if (r->num_tokens > 0 && !r->positions) return fail(RA_ERR_INVALID_ARG, "positions is NULL");

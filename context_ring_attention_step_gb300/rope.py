@@ -20,6 +20,7 @@ current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -29,12 +30,8 @@ from .kv_cache import _array, _launch, _library, _on_gpu
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-class _Shape(ctypes.Structure):
-    _fields_ = [("num_tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("weights_bf16", ctypes.c_int32),
-                ("positions", ctypes.c_void_p), ("turns", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
-                ("k_weight", ctypes.c_void_p)]
+# ra_norm_rope, field by field
+_pack_shape = struct.Struct("=qiiiiiifiQQQQ").pack
 
 
 class Rotary:
@@ -66,6 +63,7 @@ class Rotary:
         bits = [t - (1 << 64) if t >> 63 else t for t in turns[:n]]
         self.turns = torch.tensor(bits, dtype=torch.int64).to(device)
         self.device = self.turns.device
+        self.address = self.turns.data_ptr() if n else 0
 
 
 def rope_positions(cu_seqlens, device="cuda"):
@@ -79,55 +77,50 @@ def rope_positions(cu_seqlens, device="cuda"):
     return (t - start).to(device)
 
 
-def _strided(name, t, shape, dtype, device):
-    """(pointer, row stride) of a [T, heads, dim] tensor whose rows are dense."""
+def _strided(name, t, T, heads, dim, dtype, device):
+    """(pointer, row stride) of a [T, heads, dim] tensor whose rows are dense.
+
+    (One expression for the common case: a step makes several of these checks.)"""
+    s = t.stride()
+    if t.dtype is dtype and t.get_device() == device.index and t.shape == (T, heads, dim) and s[2] == 1 and s[1] == dim:
+        return t.data_ptr(), s[0] if T > 1 else heads * dim
     if t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    row = shape[1] * shape[2]
-    if shape[0] == 0:
-        return 0, row
-    s = t.stride()
-    if s[2] != 1 or (shape[1] > 1 and s[1] != shape[2]):
+    if t.shape != (T, heads, dim):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (T, heads, dim)))
+    if T > 0 and (s[2] != 1 or (heads > 1 and s[1] != dim)):
         raise ValueError("%s: the heads of a row must lie one after the other (strides %s)" % (name, tuple(s)))
-    return t.data_ptr(), s[0] if shape[0] > 1 else row
+    return t.data_ptr(), s[0] if T > 1 else heads * dim
 
 
 def _shape_of(q, k, positions, rotary, q_weight, k_weight, eps):
-    """(the call's shape block, device); the tensors' shapes are checked against one another."""
+    """(the call's shape block, tokens, query heads, key heads, device); the shapes are checked against one another."""
     dev, D = q.device, rotary.head_dim
-    _on_gpu("q", dev)
+    if dev.type != "cuda":
+        _on_gpu("q", dev)
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != D or k.shape[2] != D:
         raise ValueError("q and k have shapes %s and %s, expected [T, heads, %d]" % (tuple(q.shape), tuple(k.shape), D))
     if rotary.device != dev:
         raise ValueError("rotary is on %s, expected %s" % (rotary.device, dev))
-    T = q.shape[0]
-    norm = eps is not None
-    c = _Shape(T, q.shape[1], k.shape[1], D, rotary.rotary_dim, int(rotary.interleaved), int(norm),
-               float(eps) if norm else 0.0, 0, _array("positions", positions, (T,), _I32, dev),
-               rotary.turns.data_ptr() if rotary.rotary_dim else 0, 0, 0)
-    if not norm and not (q_weight is None and k_weight is None):
-        raise ValueError("q_weight and k_weight need the norm (eps)")
-    wt = q_weight.dtype if q_weight is not None else k_weight.dtype if k_weight is not None else _F32
-    if wt is not _F32 and wt is not _BF16:
-        raise ValueError("weights have dtype %s, expected %s or %s" % (wt, _F32, _BF16))
-    c.weights_bf16 = int(wt is _BF16)
-    if q_weight is not None:
-        c.q_weight = _array("q_weight", q_weight, (D,), wt, dev)
-    if k_weight is not None:
-        c.k_weight = _array("k_weight", k_weight, (D,), wt, dev)
-    return c, dev
-
-
-def _pair(out, q, k, names, dev):
-    """The two bf16 results, allocated where the caller owns none, and their pointers and strides."""
-    if out is None:
-        out = (torch.empty(q.shape, dtype=_BF16, device=dev), torch.empty(k.shape, dtype=_BF16, device=dev))
-    a, b = out
-    return a, b, _strided(names[0], a, q.shape, _BF16, dev), _strided(names[1], b, k.shape, _BF16, dev)
+    T, Hq, _ = q.shape
+    Hkv = k.shape[1]
+    qw = kw = bf16 = 0
+    if q_weight is not None or k_weight is not None:
+        if eps is None:
+            raise ValueError("q_weight and k_weight need the norm (eps)")
+        wt = (k_weight if q_weight is None else q_weight).dtype
+        if wt is not _F32 and wt is not _BF16:
+            raise ValueError("weights have dtype %s, expected %s or %s" % (wt, _F32, _BF16))
+        bf16 = wt is _BF16
+        if q_weight is not None:
+            qw = _array("q_weight", q_weight, (D,), wt, dev)
+        if k_weight is not None:
+            kw = _array("k_weight", k_weight, (D,), wt, dev)
+    c = _pack_shape(T, Hq, Hkv, D, rotary.rotary_dim, rotary.interleaved, eps is not None, eps or 0.0, bf16,
+                    _array("positions", positions, (T,), _I32, dev), rotary.address, qw, kw)
+    return c, T, Hq, Hkv, dev
 
 
 def qk_norm_rope_fwd(q, k, positions, rotary, q_weight=None, k_weight=None, eps=1e-6, out=None):
@@ -137,12 +130,16 @@ def qk_norm_rope_fwd(q, k, positions, rotary, q_weight=None, k_weight=None, eps=
     ``eps=None`` leaves the norm out.  ``out=(q_out, k_out)`` writes into
     caller-owned tensors (rows may be strided); they may be q and k themselves.
     """
-    lib = _library()
-    c, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
-    qp, qs = _strided("q", q, q.shape, _BF16, dev)
-    kp, ks = _strided("k", k, k.shape, _BF16, dev)
-    qo, ko, (qop, qos), (kop, kos) = _pair(out, q, k, ("q_out", "k_out"), dev)
-    _launch(dev, lib.ra_qk_norm_rope_fwd, ctypes.addressof(c), qp, qs, kp, ks, qop, qos, kop, kos)
+    c, T, Hq, Hkv, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
+    D = rotary.head_dim
+    qp, qs = _strided("q", q, T, Hq, D, _BF16, dev)
+    kp, ks = _strided("k", k, T, Hkv, D, _BF16, dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=dev), torch.empty((T, Hkv, D), dtype=_BF16, device=dev)
+    qo, ko = out
+    qop, qos = _strided("q_out", qo, T, Hq, D, _BF16, dev)
+    kop, kos = _strided("k_out", ko, T, Hkv, D, _BF16, dev)
+    _launch(dev, _library().ra_qk_norm_rope_fwd, c, qp, qs, kp, ks, qop, qos, kop, kos)
     return qo, ko
 
 
@@ -163,29 +160,37 @@ def qk_norm_rope_bwd(q, k, gq, gk, positions, rotary, q_weight=None, k_weight=No
     projection's gradient); the weights' are fp32 [d], None where there is no
     weight or ``weight_grads`` is false.
     """
-    lib = _library()
-    c, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
-    qp, qs = _strided("q", q, q.shape, _BF16, dev)
-    kp, ks = _strided("k", k, k.shape, _BF16, dev)
+    c, T, Hq, Hkv, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
+    D = rotary.head_dim
+    qp, qs = _strided("q", q, T, Hq, D, _BF16, dev)
+    kp, ks = _strided("k", k, T, Hkv, D, _BF16, dev)
     gt = gq.dtype
     if gt is not _BF16 and gt is not _F32:
         raise ValueError("gq has dtype %s, expected %s or %s" % (gt, _BF16, _F32))
-    gqp, gqs = _strided("gq", gq, q.shape, gt, dev)
-    gkp, gks = _strided("gk", gk, k.shape, gt, dev)
-    dq, dk, (dqp, dqs), (dkp, dks) = _pair(out, q, k, ("dq", "dk"), dev)
-    grads = [None, None]
-    ws, ws_bytes = 0, 0
+    gqp, gqs = _strided("gq", gq, T, Hq, D, gt, dev)
+    gkp, gks = _strided("gk", gk, T, Hkv, D, gt, dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=dev), torch.empty((T, Hkv, D), dtype=_BF16, device=dev)
+    dq, dk = out
+    dqp, dqs = _strided("dq", dq, T, Hq, D, _BF16, dev)
+    dkp, dks = _strided("dk", dk, T, Hkv, D, _BF16, dev)
+    dqw = dkw = None
+    dqwp = dkwp = ws = ws_bytes = 0
     if weight_grads and not (q_weight is None and k_weight is None):
-        grads = [None if w is None else torch.empty(rotary.head_dim, dtype=_F32, device=dev) for w in (q_weight, k_weight)]
+        if q_weight is not None:
+            dqw = torch.empty(D, dtype=_F32, device=dev)
+            dqwp = dqw.data_ptr()
+        if k_weight is not None:
+            dkw = torch.empty(D, dtype=_F32, device=dev)
+            dkwp = dkw.data_ptr()
         if workspace is None:
-            workspace = qk_norm_rope_workspace(rotary.head_dim, dev)
+            workspace = qk_norm_rope_workspace(D, dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on %s" % dev)
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    dqw, dkw = (0 if g is None else g.data_ptr() for g in grads)
-    _launch(dev, lib.ra_qk_norm_rope_bwd, ctypes.addressof(c), qp, qs, kp, ks, gqp, gqs, gkp, gks, int(gt is _F32), dqp,
-            dqs, dkp, dks, dqw, dkw, ws, ws_bytes)
-    return dq, dk, grads[0], grads[1]
+    _launch(dev, _library().ra_qk_norm_rope_bwd, c, qp, qs, kp, ks, gqp, gqs, gkp, gks, gt is _F32, dqp, dqs, dkp, dks,
+            dqwp, dkwp, ws, ws_bytes)
+    return dq, dk, dqw, dkw
 
 
 class QkNormRope(torch.autograd.Function):

@@ -421,7 +421,7 @@ typedef struct ra_norm_rope {
   int32_t num_q_heads;
   int32_t num_kv_heads;
   int32_t head_dim;        /* 64, 128 or 256 */
-  int32_t rotary_dim;      /* 0: no rotation; a multiple of 16 (interleaved: of 2) up to head_dim */
+  int32_t rotary_dim;      /* 0: no rotation; a multiple of 8 (interleaved: of 2) up to head_dim */
   int32_t interleaved;
   int32_t norm;
   float eps;

@@ -98,6 +98,7 @@ SHAPES = [  # T, Hq, Hkv, d, rotary_dim, interleaved, norm, weights
     (50, 4, 2, 128, 0, False, True, torch.float32),
     (77, 6, 2, 64, 64, True, False, None),
     (77, 6, 2, 128, 96, False, False, None),
+    (78, 3, 2, 64, 24, False, True, torch.bfloat16),
     (5003, 4, 2, 64, 16, False, True, torch.float32),
     (4999, 17, 1, 128, 128, False, True, torch.float32),
 ]

@@ -97,13 +97,28 @@ A = 1 << 40          # addresses that are never touched
 ROWS = 4
 
 
+class _Shape(ctypes.Structure):
+    """ra_norm_rope as the header has it."""
+
+    _fields_ = [("num_tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("weights_bf16", ctypes.c_int32),
+                ("positions", ctypes.c_void_p), ("turns", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
 def shape_block(ra, **kw):
-    from context_ring_attention_step_gb300.rope import _Shape
     v = dict(num_tokens=ROWS, num_q_heads=2, num_kv_heads=1, head_dim=64, rotary_dim=64, interleaved=0, norm=1, eps=1e-6,
              weights_bf16=0, positions=A + (9 << 20), turns=A + (10 << 20), q_weight=A + (11 << 20),
              k_weight=A + (12 << 20))
     v.update(kw)
     return _Shape(*[v[n] for n, _ in _Shape._fields_])
+
+
+def test_the_packed_shape_is_the_structure(ra):
+    from context_ring_attention_step_gb300.rope import _pack_shape
+    values = (7, 6, 5, 64, 32, 1, 1, 0.5, 1, 11, 22, 33, 44)
+    assert _pack_shape(*values) == bytes(_Shape(*values))
 
 
 def fwd_args(**kw):
@@ -115,7 +130,7 @@ def fwd_args(**kw):
 @pytest.mark.parametrize("kw,status,word", [
     (dict(head_dim=80), 2, "head_dim"), (dict(num_tokens=-1), 1, "num_tokens"), (dict(num_tokens=1 << 31), 1, "num_tokens"),
     (dict(num_q_heads=0), 1, "num_q_heads"), (dict(num_kv_heads=70000), 1, "num_kv_heads"),
-    (dict(rotary_dim=24), 2, "rotary_dim"), (dict(rotary_dim=33, interleaved=1), 2, "rotary_dim"),
+    (dict(rotary_dim=20), 2, "rotary_dim"), (dict(rotary_dim=33, interleaved=1), 2, "rotary_dim"),
     (dict(rotary_dim=128), 2, "rotary_dim"), (dict(eps=-1.0), 1, "eps"), (dict(eps=float("nan")), 1, "eps"),
     (dict(norm=0), 1, "weights need the norm"), (dict(positions=None), 1, "positions"), (dict(turns=None), 1, "turns"),
     (dict(positions=A + 2), 1, "aligned"), (dict(q_weight=A + 2), 1, "aligned")])
