@@ -27,6 +27,7 @@ from .kv_cache import (  # noqa: F401
     kv4_store,
     kv4_tables,
     kv4_tables_out,
+    kv4_weights,
 )
 from .rope import (  # noqa: F401
     QkNormRope,

@@ -159,6 +159,16 @@ struct Kv4AttnParams {
   float* partials;  // two slots per CTA: [0] of a unit that an earlier CTA began, [1] of one that this CTA began
 };
 
+// The weights that cached tokens receive (kv4_weights.cu): the queries, tables and
+// lengths as for attention, of which nothing is written but the status.
+struct Kv4WeightsParams {
+  Kv4AttnParams a;
+  const float* lse;         // [Hq, Tq], of the rows' attention
+  const int32_t* new_lens;  // [R] tokens at a request's end whose sums begin at zero, or null
+  float* weights;           // [num_pages, page size]
+};
+cudaError_t launch_kv4_weights(int D, int sms, const Kv4WeightsParams& p, cudaStream_t stream);
+
 cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_store(int D, const Kv4RowsParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_load(int D, const Kv4RowsParams& p, cudaStream_t stream);

@@ -295,6 +295,78 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
   return RA_OK;
 }
 
+ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_stride, int32_t num_q_tokens,
+                         int32_t num_q_heads, const int32_t* block_table, int32_t table_width, int64_t table_stride,
+                         const int32_t* kv_lens, const int32_t* cu_q, int32_t num_requests, int32_t max_q_len,
+                         int32_t causal, float softmax_scale, const float* lse, const int32_t* new_lens,
+                         float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+  ra::Kv4WeightsParams w{};
+  ra::Kv4AttnParams& p = w.a;
+  ra_status rs = check_cache(cache, &p.cache);
+  if (rs != RA_OK) return rs;
+  const int32_t D = cache->head_dim, Hkv = cache->num_kv_heads;
+  rs = check_heads(num_q_heads, Hkv, D, max_q_len);
+  if (rs != RA_OK) return rs;
+  if (num_q_tokens < 0 || num_requests < 0)
+    return fail(RA_ERR_INVALID_ARG, "num_q_tokens %d, num_requests %d must not be negative", num_q_tokens, num_requests);
+  if ((int64_t)num_q_tokens * num_q_heads > (int64_t(1) << 30))
+    return fail(RA_ERR_INVALID_ARG, "%d query tokens of %d heads: more than 2^30 rows in one call", num_q_tokens, num_q_heads);
+  if (table_width < 1 || table_stride < table_width)
+    return fail(RA_ERR_INVALID_ARG, "table_width %d, table_stride %lld: need 1 <= width <= stride", table_width,
+                (long long)table_stride);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < kHeader)
+    return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes: need %zu, 256-byte aligned", workspace ? workspace_bytes : 0,
+                kHeader);
+  if (!std::isfinite(softmax_scale)) return fail(RA_ERR_INVALID_ARG, "softmax_scale is not finite");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (num_requests == 0) {
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int32_t), st);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, "status reset");
+  }
+  if ((num_q_tokens > 0 && (!q || !lse)) || !block_table || !kv_lens || !cu_q || !weights)
+    return fail(RA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(cu_q, 4) ||
+      !aligned(new_lens, 4) || !aligned(weights, 4))
+    return fail(RA_ERR_INVALID_ARG, "q must be 16-byte aligned, the other arrays 4-byte aligned");
+  const int64_t row = (int64_t)num_q_heads * D;
+  if (num_q_tokens > 1 && (q_stride < row || q_stride % 8))
+    return fail(RA_ERR_INVALID_ARG, "q row stride %lld: a multiple of 8 elements, at least %lld", (long long)q_stride,
+                (long long)row);
+  const size_t slots4 = (size_t)cache->num_pages * cache->page_size * 4, R4 = (size_t)num_requests * 4;
+  const struct { const void* at; size_t bytes; const char* name; } reads[] = {
+      {q, num_q_tokens > 0 ? ((size_t)(num_q_tokens - 1) * (num_q_tokens > 1 ? q_stride : row) + row) * 2 : 0, "q"},
+      {lse, (size_t)num_q_tokens * num_q_heads * 4, "lse"},
+      {block_table, ((size_t)(num_requests - 1) * table_stride + table_width) * 4, "block_table"},
+      {kv_lens, R4, "kv_lens"}, {cu_q, R4 + 4, "cu_q"}, {new_lens, R4, "new_lens"}, {workspace, kHeader, "the workspace"},
+      {cache->pages, (size_t)cache->num_pages * page_bytes(cache->page_size, Hkv, D), "the cache"}};
+  for (const auto& x : reads)
+    if (overlap(weights, slots4, x.at, x.bytes)) return fail(RA_ERR_INVALID_ARG, "weights lie over %s", x.name);
+  p.q = q;
+  p.q_stride = q_stride;
+  p.Tq = num_q_tokens;
+  p.Hq = num_q_heads;
+  p.R = num_requests;
+  p.causal = causal != 0;
+  p.block_table = block_table;
+  p.table_stride = table_stride;
+  p.table_width = table_width;
+  p.kv_lens = kv_lens;
+  p.cu_q = cu_q;
+  p.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D);
+  p.page_bytes = (int64_t)page_bytes(cache->page_size, Hkv, D);
+  p.status = reinterpret_cast<int32_t*>(workspace);
+  p.found = p.status + 1;
+  p.ended = p.status + 2;
+  w.lse = lse;
+  w.new_lens = new_lens;
+  w.weights = weights;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  e = ra::launch_kv4_weights(D, sms, w, st);
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache weights launch");
+}
+
 ra_status ra_kv4_status(const void* status, void* stream_) {
   if (!status) return fail(RA_ERR_INVALID_ARG, "status is NULL");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_);

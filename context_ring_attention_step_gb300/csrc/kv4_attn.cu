@@ -46,6 +46,7 @@
 
 #include "kv4.cuh"
 #include "kv4.h"
+#include "kv4_mma.cuh"
 #include "kv4_walk.cuh"
 #include "tc.cuh"
 
@@ -65,12 +66,6 @@ constexpr int KB = 16 * kWarps;  // keys of one block: a tile a warp
 constexpr float kHeadroom = 7.f;
 constexpr float kMaxExp = 15.f;
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
 // Transpose of an 8 x 8 matrix of 16-bit elements held one row a quad.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -79,28 +74,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 // One warp's tile in registers.
 template <int D>
-struct TileRegs {
-  uint4 k[D / 64], v[D / 64];
-  uint32_t ks[D == 256 ? 2 : 1], vs[D == 256 ? 2 : 1];
+struct TileRegs : KeyRegs<D> {
+  uint4 v[D / 64];
+  uint32_t vs[D == 256 ? 2 : 1];
 };
-
-// Asynchronous copies of a lane's own words into its warp's ring; `n` bytes (all
-// or none: then zeros) are read.  A lane reads back only what it copied itself, so
-// that waiting for its own copies is all the synchronisation there is.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, uint32_t n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const uint8_t* src, uint32_t n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {  // all but the last N groups are there
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 template <int D>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* tile, bool in, int lane) {
@@ -141,23 +118,6 @@ __device__ __forceinline__ void load_tile(TileRegs<D>& t, const uint8_t* tile, i
   }
 }
 
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-// Word `i` of the run of K codes that a lane holds for token r + 8 h.
-template <int D>
-__device__ __forceinline__ uint32_t k_word(const TileRegs<D>& t, int h, int i) {
-  if (D == 64) return word(t.k[0], 2 * h + i);
-  if (D == 128) return word(t.k[h], i);
-  return word(t.k[(2 * h + (i >> 2)) % (D / 64)], i & 3);
-}
-// Its scale of group g, in both halves.
-template <int D>
-__device__ __forceinline__ uint32_t k_scale2(const TileRegs<D>& t, int h, int g) {
-  if (D == 64) return scale_both(t.ks[0], h);
-  if (D == 128) return scale_both(t.ks[0], 2 * h + g);
-  return scale_both(t.ks[h % (D == 256 ? 2 : 1)], g);
-}
 // Word `i` of the run of V codes that a lane holds for token 2c + e + 8 h.
 template <int D>
 __device__ __forceinline__ uint32_t v_word(const TileRegs<D>& t, int h, int e, int i) {

@@ -139,21 +139,19 @@ struct Kv4Line {
   }
 };
 
-// Cut the line for this grid; `wk` receives the place where this CTA's part
-// begins (when it has one).  All threads of the CTA; s_sum has one entry a warp.
-template <int RT, int KB, int KU, bool kTiles, int kThreads>
-__device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long long* s_sum, long long* s_found,
-                                                 Kv4Walk& wk, int& bad) {
+// Cut the line for this grid: `work(r)` places for each of R requests.  `r` and `base`
+// receive the request that holds the first place of this CTA's part (when it has one) and
+// the places before that request.  All threads of the CTA; s_sum has one entry a warp.
+template <int kThreads, typename F>
+__device__ __forceinline__ Kv4Line kv4_cut(int R, F work, long long* s_sum, long long* s_found, int& r, long long& base) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) s_found[0] = -1;
   long long mine = 0, total = 0;  // work of request `tid`; of all
-  for (int i = tid; i < p.R; i += kThreads) {
-    const Kv4Request q = kv4_request<RT, KB, kTiles>(p, i);
-    const long long w = kv4_request_work<KU>(q, p.cache.Hkv);
+  for (int i = tid; i < R; i += kThreads) {
+    const long long w = work(i);
     if (i == tid) mine = w;
     total += w;
-    bad = max(bad, q.bad);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
@@ -170,14 +168,11 @@ __device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long lo
   line.rest = line.total - line.size * line.cut;
   line.begin = idle ? 0 : line.size * blockIdx.x + min((long long)blockIdx.x, line.rest);
   line.end = idle ? 0 : line.begin + line.size + (blockIdx.x < line.rest ? 1 : 0);
-  wk.pos = line.begin;
-  wk.base = 0;
-  wk.r = 0;
+  base = 0;
+  r = 0;
   if (idle) return line;
-  for (int r0 = 0; r0 < p.R; r0 += kThreads) {
-    const long long w = r0 == 0           ? mine
-                        : r0 + tid < p.R ? kv4_request_work<KU>(kv4_request<RT, KB, kTiles>(p, r0 + tid), p.cache.Hkv)
-                                         : 0;
+  for (int r0 = 0; r0 < R; r0 += kThreads) {
+    const long long w = r0 == 0 ? mine : r0 + tid < R ? work(r0 + tid) : 0;
     long long x = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -187,7 +182,7 @@ __device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long lo
     __syncthreads();
     if (lane == 31) s_sum[warp] = x;
     __syncthreads();
-    long long before = wk.base, chunk = 0;
+    long long before = base, chunk = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
       if (i < warp) before += s_sum[i];
@@ -199,12 +194,26 @@ __device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long lo
     }
     __syncthreads();
     if (s_found[0] >= 0) {
-      wk.r = (int)s_found[0];
-      wk.base = s_found[1];
+      r = (int)s_found[0];
+      base = s_found[1];
       break;
     }
-    wk.base += chunk;
+    base += chunk;
   }
+  return line;
+}
+
+// The same for attention's units; `wk` receives the place where this CTA's part begins.
+template <int RT, int KB, int KU, bool kTiles, int kThreads>
+__device__ __forceinline__ Kv4Line kv4_find_part(const Kv4AttnParams& p, long long* s_sum, long long* s_found,
+                                                 Kv4Walk& wk, int& bad) {
+  auto work = [&](int i) {
+    const Kv4Request q = kv4_request<RT, KB, kTiles>(p, i);
+    bad = max(bad, q.bad);
+    return kv4_request_work<KU>(q, p.cache.Hkv);
+  };
+  const Kv4Line line = kv4_cut<kThreads>(p.R, work, s_sum, s_found, wk.r, wk.base);
+  wk.pos = line.begin;
   return line;
 }
 

@@ -286,6 +286,46 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None,
     return o, lse
 
 
+def kv4_weights(q, cache, block_table, kv_lens, cu_q, lse, weights, new_lens=None, causal=True, scale=None,
+                max_q_len=None, workspace=None, check=False):
+    """Add to ``weights`` the attention weight that every cached token receives from the query rows.
+
+    ``q``, ``block_table``, ``kv_lens``, ``cu_q``, ``causal``, ``scale`` and
+    ``max_q_len`` as for ``kv4_attention``, and ``lse`` [Hq, Tq] from it:
+    ``weights[slot] += sum of exp(scale q . k - lse)`` over the rows and query
+    heads that see the slot's token.  ``weights``: fp32 [num_pages * page_size],
+    updated in place (and returned).  ``new_lens`` [R] (int32): the sums of a
+    request's last tokens, as many as the step added, begin at zero.
+    ``workspace``: that of ``kv4_attention`` will do.  ``check=True`` synchronises
+    and raises if lengths, offsets or pages were out of range.
+    """
+    lib = _library()
+    if q.requires_grad and torch.is_grad_enabled():
+        raise ValueError("kv4_weights has no gradient: call it under torch.no_grad()")
+    dev, R = cache.device, kv_lens.shape[0]
+    if q.dim() != 3:
+        raise ValueError("q has shape %s, expected [T, heads, %d]" % (tuple(q.shape), cache.head_dim))
+    _on_gpu("cache", dev)
+    T, Hq, D = q.shape
+    qp, qs = _rows("q", q, Hq, cache.head_dim, dev)
+    table, width, stride = _table(block_table, R, dev)
+    lens = _array("kv_lens", kv_lens, (R,), _I32, dev)
+    cu = _array("cu_q", cu_q, (R + 1,), _I32, dev)
+    new = None if new_lens is None else _array("new_lens", new_lens, (R,), _I32, dev)
+    if workspace is None:
+        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    _launch(dev, lib.ra_kv4_weights, cache._ref, qp, qs, T, Hq, table, width, stride, lens, cu, R,
+            max(1, int(T if max_q_len is None else max_q_len)), int(bool(causal)), float(scale) if scale else 0.0,
+            _array("lse", lse, (Hq, T), _F32, dev), new,
+            _array("weights", weights, (cache.num_pages * cache.page_size,), _F32, dev), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    if check:
+        kv4_status(workspace)
+    return weights
+
+
 def kv4_status(status):
     """Synchronise and raise if the status word at the start of ``status`` (``Kv4Tables.status``,
     or the workspace of ``kv4_attention``) reports a refusal."""

@@ -613,6 +613,34 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The attention weight that every cached token receives from the call's query
+ * rows, added to a running sum:
+ *   weights[slot(j)] += sum over query heads h and rows i that see key j of
+ *                       exp(softmax_scale q_ih . k_j - lse[h][i]).
+ * Queries, tables, lengths, masks, max_q_len and softmax_scale as in
+ * ra_kv4_attention, whose lse this is (fp32 [num_q_heads, num_q_tokens]).
+ *   weights fp32 [num_pages * page_size], a sum for every slot.  Slots of no
+ *     request's cached tokens stay as they are.  It lies over nothing that the
+ *     call reads.
+ *   new_lens int32 [R], or NULL: the sums of a request's last new_lens[r]
+ *     tokens begin at zero with this call, whatever their slots held (a negative
+ *     number counts as 0, one above the length as all).  Requests without query
+ *     rows take part in that.  What ra_kv4_tables took, for the step that stored them.
+ * Calls of several layers may share one array: new_lens in the first of them.
+ * A row whose lse is -inf sees no key; one that is NaN, or whose query is not
+ * finite, makes the sums of all keys it sees NaN.  A slot must not belong to two
+ * requests (or twice to one): its sum would miss one's share.  The order of the additions
+ * is fixed.  Keys on pages outside the cache are left out.
+ * The workspace (at least 256 bytes, 256-byte aligned) must be zero before its
+ * first use, may be that of ra_kv4_attention, and receives the status as there.
+ */
+ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_stride, int32_t num_q_tokens,
+                         int32_t num_q_heads, const int32_t* block_table, int32_t table_width, int64_t table_stride,
+                         const int32_t* kv_lens, const int32_t* cu_q, int32_t num_requests, int32_t max_q_len,
+                         int32_t causal, float softmax_scale, const float* lse, const int32_t* new_lens,
+                         float* weights, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream` and read a status word (ra_kv4_tables' status, or the
  * start of ra_kv4_attention's workspace): RA_OK; RA_ERR_WORKSPACE for missing
  * pages; RA_ERR_INVALID_ARG for the other refusals; RA_ERR_TIMEOUT if a kernel
