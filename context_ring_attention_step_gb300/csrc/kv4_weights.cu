@@ -15,6 +15,7 @@
 // multiplication.  A tile is expanded once for all row tiles; those lie in shared
 // memory in the order of the operand registers.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,6 +29,10 @@
 namespace ra {
 namespace {
 
+#ifndef WP
+#define WP 4
+#define WH 1
+#endif
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int KB = 16 * kWarps;  // keys of one block: a tile a warp
@@ -35,28 +40,32 @@ constexpr int kExpandCost = 3;   // expanding a tile, in row tiles
 
 template <int D>
 struct WeightsCfg {
-  static constexpr int kPerSm = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kPerSm = D == 64 ? 4 : D == 128 ? WP : 2;
   static constexpr int kTile = 9 * D;                  // bytes of a tile's keys: codes, then scales
   static constexpr int kSlots = D == 256 ? 6 : 8;      // ring of each warp
+  static constexpr int kHeads = D == 256 ? 1 : WH;     // heads whose products are mixed
   static constexpr int kQTile = 16 * D;                // bytes of eight rows in fp16
-  static constexpr int kCap = D == 64 ? 28 : D == 128 ? 16 : 12;  // row tiles in shared memory at once
+  static constexpr int kCap = D == 64 ? 28 : D == 128 ? (WP == 3 ? 16 : 8) : 12;  // row tiles in shared memory at once
   static constexpr int kRing = kWarps * kSlots * kTile;
   static constexpr int kSmem = kRing + kCap * (kQTile + 8 * 12);
   static_assert(kSmem <= (220 / kPerSm - 1) * 1024, "CTAs on an SM");
   static_assert(Kv4Layout<D>::kKCodes == 0 && Kv4Layout<D>::kKScales == 8 * D, "keys lie at a tile's start");
 };
 
+// Copy a lane's words of a tile's keys: codes from `k`, scales from `s` (the lane's own),
+// to the tile's place in the ring (`dst`; at head_dim 64 two lanes share a word of scales,
+// and both copy it).
 template <int D>
-__device__ __forceinline__ void copy_keys(uint32_t dst, const uint8_t* tile, bool in, int lane) {
-  using L = Kv4Layout<D>;
+__device__ __forceinline__ void copy_keys(uint32_t dst, const uint8_t* k, const uint8_t* s, int lane) {
+  constexpr int kS = Kv4Layout<D>::kKScales;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) copy16(dst + 512 * i + 16 * lane, tile + 512 * i + 16 * lane, in ? 16 : 0);
-  if (D == 256) {
-    copy8(dst + L::kKScales + 8 * lane, tile + L::kKScales + 8 * lane, in ? 8 : 0);
-  } else {  // at head_dim 64 two lanes share a word, and both copy it
-    const int k = D == 64 ? 2 * lane & ~3 : 4 * lane;
-    copy4(dst + L::kKScales + k, tile + L::kKScales + k, in ? 4 : 0);
-  }
+  for (int i = 0; i < D / 64; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * i + 16 * lane), "l"(k + 512 * i) : "memory");
+  if (D == 256)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + kS + 8 * lane), "l"(s) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + kS + (D == 64 ? 2 * lane & ~3 : 4 * lane)), "l"(s)
+                 : "memory");
 }
 template <int D>
 __device__ __forceinline__ void load_keys(KeyRegs<D>& t, const uint8_t* tile, int lane) {
@@ -127,7 +136,8 @@ __global__ void __launch_bounds__(kThreads, (WeightsCfg<D>::kPerSm)) kv4_weights
   const int r8 = lane >> 2, c4 = lane & 3;
   const int G = p.Hq / p.cache.Hkv, P = 1 << p.cache.page_shift;
   const uint8_t* ring = s_dyn + warp * S * C::kTile;
-  uint4* s_q = reinterpret_cast<uint4*>(s_dyn + C::kRing);                      // [kCap][D / 32][32]
+  const uint32_t ring_at = smem_u32(ring);
+  uint4* s_q = reinterpret_cast<uint4*>(s_dyn + C::kRing);                                // [kCap][D / 32][32]
   float2* s_row = reinterpret_cast<float2*>(s_dyn + C::kRing + C::kCap * C::kQTile);  // [kCap][8] scale, - lse (log2)
   int* s_lim = reinterpret_cast<int*>(s_row + 8 * C::kCap);                      // [kCap][8] keys that the row sees
   if (tid == 0) s_bad = 0;
@@ -210,83 +220,121 @@ __global__ void __launch_bounds__(kThreads, (WeightsCfg<D>::kPerSm)) kv4_weights
         __syncthreads();
         const int lim_min = s_lim_min;
 
-        // ---- this warp's (tile, head) pairs, S - 1 of them under way
-        const uint32_t ring_at = smem_u32(ring);
-        int ai = b0, ah = 0, page = page_of(b0), page_next = page_of(b0 + 1), slot_ask = 0;
-        auto ask = [&]() {
-          if (ai < e1 && nh > 0) {
-            const bool good = (uint32_t)page < (uint64_t)p.cache.num_pages;
-            const size_t tile = ((size_t)(h0 + ah) << (p.cache.page_shift - 4)) + (((ai * KB + 16 * warp) & (P - 1)) >> 4);
-            copy_keys<D>(ring_at + slot_ask, p.cache.pages + (int64_t)(good ? page : 0) * p.page_bytes + tile * L::kBytes,
-                         good, lane);
-            if (++ah == nh) {
-              ah = 0;
-              ++ai;
-              page = page_next;
-              page_next = page_of(ai + 1);
-            }
-          }
+        // ---- this warp's (tile, head) pairs, S - 1 of them under way in the warp's ring
+        const size_t head_bytes = (size_t)L::kBytes << (p.cache.page_shift - 4);
+        int ai = b0, ah = 0, page = page_of(b0), page_next = page_of(b0 + 1);
+        const uint8_t *kp, *sp;
+        auto aim = [&]() {  // at the first head of tile `ai`; a page that is none: somewhere in the cache
+          const uint8_t* tile = p.cache.pages + (int64_t)((uint32_t)page < (uint64_t)p.cache.num_pages ? page : 0) * p.page_bytes +
+                                h0 * head_bytes + (((ai * KB + 16 * warp) & (P - 1)) >> 4) * L::kBytes;
+          kp = tile + 16 * lane;
+          sp = tile + L::kKScales + (D == 64 ? 2 * lane & ~3 : (D / 32) * lane);
+        };
+        aim();
+        uint32_t slot_ask = 0;
+        auto ask = [&]() {  // (behind the last tile: that again, unused)
+          copy_keys<D>(ring_at + slot_ask, kp, sp, lane);
           copy_commit();
           slot_ask = slot_ask == (S - 1) * C::kTile ? 0 : slot_ask + C::kTile;
+          if (++ah < nh) {
+            kp += head_bytes;
+            sp += head_bytes;
+          } else if (ai + 1 < e1) {
+            ah = 0;
+            ++ai;
+            page = page_next;
+            page_next = page_of(ai + 1);
+            aim();
+          }
         };
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) ask();
-        int slot = 0, mine = page_of(b0);
-#pragma unroll 1
-        for (int i = b0; i < e1; ++i) {
-          const int tok = i * KB + 16 * warp;
+        int i = b0, mine = page;
+        float sum0 = 0.f, sum1 = 0.f, old = 0.f;
+        float* dst = nullptr;
+        // lanes c4 < 2 hand in token r8 + 8 c4 of the tile
+        const int off = r8 + 8 * (c4 & 1);
+        auto begin = [&]() {
           const bool good = (uint32_t)mine < (uint64_t)p.cache.num_pages;
           if (!good) bad = max(bad, (int)RA_KV4_BAD_PAGE);
-          // lanes c4 < 2 hand in token r8 + 8 c4 of the tile
-          const int out = tok + r8 + 8 * (c4 & 1);
-          float* dst = wp.weights + ((int64_t)(good ? mine : 0) << p.cache.page_shift) + (out & (P - 1));
-          const bool writes = good && c4 < 2 && out < rq.L;
-          float old = 0.f;
-          if (writes && !(first && out >= job.fresh)) old = *dst;
+          const int out = i * KB + 16 * warp + off;
+          dst = good && c4 < 2 && out < rq.L ? wp.weights + ((int64_t)mine << p.cache.page_shift) + (out & (P - 1)) : nullptr;
+          const bool fresh = out >= job.fresh;
+          old = dst && !(first && fresh) ? *dst : 0.f;
+          if (nh == 0 && !fresh) dst = nullptr;
           mine = page_of(i + 1);
-          const bool masked = tok + 16 > lim_min;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll 1
-          for (int hh = 0; hh < nh; ++hh) {
-            copy_wait<S - 2>();
-            KeyRegs<D> keys;
-            load_keys<D>(keys, ring + slot, lane);
-            ask();
-            slot = slot == (S - 1) * C::kTile ? 0 : slot + C::kTile;
-            uint32_t a[D / 16][4];
-            expand_keys<D>(keys, a);
-#pragma unroll 1
-            for (int t = 0; t < nt; ++t) {
-              const int k = hh * nt + t;
-              const uint4* q = s_q + k * (D / 32) * 32 + lane;
-              float c[2][4] = {};
-#pragma unroll
-              for (int j = 0; j < D / 32; ++j) {
-                const uint4 w = q[32 * j];
-                const uint32_t x[2] = {w.x, w.y}, y[2] = {w.z, w.w};
-                mma16816(c[0], a[2 * j], x);
-                mma16816(c[1], a[2 * j + 1], y);
-              }
-              const float4 row = *reinterpret_cast<const float4*>(s_row + 8 * k + 2 * c4);
-              float e[4];
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                e[v] = ex2_approx(fmaf(c[0][v] + c[1][v], v & 1 ? row.z : row.x, v & 1 ? row.w : row.y));
-              if (masked) {
-                const int2 lim = *reinterpret_cast<const int2*>(s_lim + 8 * k + 2 * c4);
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  if (tok + r8 + 8 * (v >> 1) >= (v & 1 ? lim.y : lim.x)) e[v] = 0.f;
-              }
-              sum0 += e[0] + e[1];
-              sum1 += e[2] + e[3];
-            }
-          }
+          sum0 = sum1 = 0.f;
+        };
+        auto end = [&]() {
           sum0 += __shfl_xor_sync(0xffffffffu, sum0, 1);
           sum1 += __shfl_xor_sync(0xffffffffu, sum1, 1);
           sum0 += __shfl_xor_sync(0xffffffffu, sum0, 2);
           sum1 += __shfl_xor_sync(0xffffffffu, sum1, 2);
-          if (writes && (nh > 0 || out >= job.fresh)) *dst = old + (c4 == 0 ? sum0 : sum1);
+          if (dst) *dst = old + (c4 == 0 ? sum0 : sum1);
+        };
+        // a tile's keys of N neighbouring heads against all rows of those
+        int slot = 0;
+        auto products = [&](auto heads, int hh) {
+          constexpr int N = decltype(heads)::value;
+          const int tok = i * KB + 16 * warp;
+          const bool masked = tok + 16 > lim_min;
+          copy_wait<S - 1 - N>();
+          uint32_t a[N][D / 16][4];
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            KeyRegs<D> keys;
+            load_keys<D>(keys, ring + slot, lane);
+            slot = slot == (S - 1) * C::kTile ? 0 : slot + C::kTile;
+            expand_keys<D>(keys, a[n]);
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) ask();
+          const uint4* q = s_q + hh * nt * D + lane;
+          const float2* rows = s_row + hh * nt * 8 + 2 * c4;
+#pragma unroll 1
+          for (int t = 0; t < nt; ++t, q += D, rows += 8) {
+            float e[N][4];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              float c[2][4] = {};
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) {
+                const uint4 w = q[n * nt * D + 32 * j];
+                const uint32_t x[2] = {w.x, w.y}, y[2] = {w.z, w.w};
+                mma16816(c[0], a[n][2 * j], x);
+                mma16816(c[1], a[n][2 * j + 1], y);
+              }
+              const float4 row = *reinterpret_cast<const float4*>(rows + n * nt * 8);
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                e[n][v] = ex2_approx(fmaf(c[0][v] + c[1][v], v & 1 ? row.z : row.x, v & 1 ? row.w : row.y));
+            }
+            if (masked) {
+#pragma unroll
+              for (int n = 0; n < N; ++n) {
+                const int2 lim = *reinterpret_cast<const int2*>(s_lim + ((hh + n) * nt + t) * 8 + 2 * c4);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  if (tok + r8 + 8 * (v >> 1) >= (v & 1 ? lim.y : lim.x)) e[n][v] = 0.f;
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              sum0 += e[n][0] + e[n][1];
+              sum1 += e[n][2] + e[n][3];
+            }
+          }
+        };
+        if (nh > 0 && i < e1) {
+#pragma unroll
+          for (int u = 0; u < S - 1; ++u) ask();
+        }
+#pragma unroll 1
+        for (; i < e1; ++i) {
+          begin();
+          int hh = 0;
+#pragma unroll 1
+          for (; hh + C::kHeads <= nh; hh += C::kHeads) products(std::integral_constant<int, C::kHeads>{}, hh);
+          if (C::kHeads > 1 && hh < nh) products(std::integral_constant<int, 1>{}, hh);
+          end();
         }
         copy_wait<0>();
         first = false;
