@@ -4,6 +4,7 @@
 // documented in ring_attn.h.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <atomic>
 #include <cstddef>
@@ -168,6 +169,10 @@ struct Kv4WeightsParams {
   float* weights;           // [num_pages, page size]
 };
 cudaError_t launch_kv4_weights(int D, int sms, const Kv4WeightsParams& p, cudaStream_t stream);
+// For many rows (kv4_wtile.cu), one CTA an SM: `tq` maps the query tensor [Tq, Hq, D] in boxes of 64
+// dims, `heads` heads and `tokens` tokens, as kv4_wtile_box says for groups of G heads.
+void kv4_wtile_box(int D, int G, int* heads, int* tokens);
+cudaError_t launch_kv4_wtile(int D, int ctas, const Kv4WeightsParams& p, const CUtensorMap& tq, cudaStream_t stream);
 
 cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_store(int D, const Kv4RowsParams& p, cudaStream_t stream);

@@ -78,6 +78,10 @@ int64_t few_rows(int32_t G, int32_t max_q_len) {
   return has_tiles(G, max_q_len) ? G : (int64_t)G * max_q_len;
 }
 
+// The same for the weights of cached tokens.
+constexpr int kWeightsTileRows = 64;
+static_assert(2 * 256 * ra::kKv4MaxSms <= 2 * ra::kKv4MaxSms * 8 * (64 + 16), "attention's workspace holds the tile kernel's sums");
+
 struct AttnLayout {
   size_t tickets, partials, total;
 };
@@ -314,9 +318,10 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
   if (table_width < 1 || table_stride < table_width)
     return fail(RA_ERR_INVALID_ARG, "table_width %d, table_stride %lld: need 1 <= width <= stride", table_width,
                 (long long)table_stride);
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < kHeader)
+  const AttnLayout l = attn_layout(D, num_q_heads / Hkv, max_q_len);  // (more than is needed here, for any shape)
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total)
     return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes: need %zu, 256-byte aligned", workspace ? workspace_bytes : 0,
-                kHeader);
+                l.total);
   if (!std::isfinite(softmax_scale)) return fail(RA_ERR_INVALID_ARG, "softmax_scale is not finite");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (num_requests == 0) {
@@ -337,7 +342,7 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
       {q, num_q_tokens > 0 ? ((size_t)(num_q_tokens - 1) * (num_q_tokens > 1 ? q_stride : row) + row) * 2 : 0, "q"},
       {lse, (size_t)num_q_tokens * num_q_heads * 4, "lse"},
       {block_table, ((size_t)(num_requests - 1) * table_stride + table_width) * 4, "block_table"},
-      {kv_lens, R4, "kv_lens"}, {cu_q, R4 + 4, "cu_q"}, {new_lens, R4, "new_lens"}, {workspace, kHeader, "the workspace"},
+      {kv_lens, R4, "kv_lens"}, {cu_q, R4 + 4, "cu_q"}, {new_lens, R4, "new_lens"}, {workspace, l.total, "the workspace"},
       {cache->pages, (size_t)cache->num_pages * page_bytes(cache->page_size, Hkv, D), "the cache"}};
   for (const auto& x : reads)
     if (overlap(weights, slots4, x.at, x.bytes)) return fail(RA_ERR_INVALID_ARG, "weights lie over %s", x.name);
@@ -363,8 +368,26 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  e = ra::launch_kv4_weights(D, sms, w, st);
-  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache weights launch");
+  p.tickets = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) + l.tickets);
+  p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + l.partials);
+  const int32_t G = num_q_heads / Hkv;
+  const bool tiles = num_q_tokens > 0 && (int64_t)G * max_q_len >= kWeightsTileRows;
+  if (!tiles || num_requests > 1) {  // (a single long request is the tile kernel's, whatever its real length)
+    p.split_rows = tiles ? kWeightsTileRows : 0;
+    e = ra::launch_kv4_weights(D, sms, w, st);
+    if (e != cudaSuccess) return cuda_fail(e, "cache weights launch");
+    p.status_kept = 1;
+  }
+  if (tiles) {
+    CUtensorMap tq;
+    int heads = 0, tokens = 0;
+    ra::kv4_wtile_box(D, G, &heads, &tokens);
+    if (!ra::encode_query_rows(&tq, q, num_q_tokens, num_q_heads, D, num_q_tokens > 1 ? q_stride : row, heads, tokens))
+      return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad tensor)");
+    e = ra::launch_kv4_wtile(D, std::min(sms, ra::kKv4MaxSms), w, tq, st);
+    if (e != cudaSuccess) return cuda_fail(e, "cache weights launch (row tiles)");
+  }
+  return RA_OK;
 }
 
 ra_status ra_kv4_status(const void* status, void* stream_) {

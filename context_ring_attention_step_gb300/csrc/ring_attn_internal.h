@@ -95,6 +95,10 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 // Record `msg` as this thread's last error text and return `st`.
 ra_status set_last_error(ra_status st, const char* msg);
 
+// bf16 rows [T, H, D], `stride` elements apart, as a 3-D map {D, H, T}; box {64, heads, tokens},
+// 128-byte swizzle.
+bool encode_query_rows(CUtensorMap* m, const void* base, int T, int H, int D, int64_t stride, int heads, int tokens);
+
 // Kernel launch wrappers (return the launch error).
 cudaError_t launch_fwd_fused(int head_dim, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const FwdParams& p, int num_items, cudaStream_t stream);

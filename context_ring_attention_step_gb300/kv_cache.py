@@ -296,7 +296,7 @@ def kv4_weights(q, cache, block_table, kv_lens, cu_q, lse, weights, new_lens=Non
     heads that see the slot's token.  ``weights``: fp32 [num_pages * page_size],
     updated in place (and returned).  ``new_lens`` [R] (int32): the sums of a
     request's last tokens, as many as the step added, begin at zero.
-    ``workspace``: that of ``kv4_attention`` will do.  ``check=True`` synchronises
+    ``workspace``: as for ``kv4_attention``, one for both.  ``check=True`` synchronises
     and raises if lengths, offsets or pages were out of range.
     """
     lib = _library()
@@ -312,12 +312,13 @@ def kv4_weights(q, cache, block_table, kv_lens, cu_q, lse, weights, new_lens=Non
     lens = _array("kv_lens", kv_lens, (R,), _I32, dev)
     cu = _array("cu_q", cu_q, (R + 1,), _I32, dev)
     new = None if new_lens is None else _array("new_lens", new_lens, (R,), _I32, dev)
+    longest = max(1, int(T if max_q_len is None else max_q_len))
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+        workspace = kv4_attention_workspace(cache, T, Hq, longest)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     _launch(dev, lib.ra_kv4_weights, cache._ref, qp, qs, T, Hq, table, width, stride, lens, cu, R,
-            max(1, int(T if max_q_len is None else max_q_len)), int(bool(causal)), float(scale) if scale else 0.0,
+            longest, int(bool(causal)), float(scale) if scale else 0.0,
             _array("lse", lse, (Hq, T), _F32, dev), new,
             _array("weights", weights, (cache.num_pages * cache.page_size,), _F32, dev), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())

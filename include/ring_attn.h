@@ -627,12 +627,12 @@ ra_status ra_kv4_attention(const ra_kv4_cache* cache, const void* q, int64_t q_s
  *     number counts as 0, one above the length as all).  Requests without query
  *     rows take part in that.  What ra_kv4_tables took, for the step that stored them.
  * Calls of several layers may share one array: new_lens in the first of them.
- * A row whose lse is -inf sees no key; one that is NaN, or whose query is not
- * finite, makes the sums of all keys it sees NaN.  A slot must not belong to two
+ * A row whose lse is -inf sees no key; one whose lse is NaN (as it is where the query
+ * has an infinity or a NaN) makes the sums of all keys it sees NaN.  A slot must not belong to two
  * requests (or twice to one): its sum would miss one's share.  The order of the additions
  * is fixed.  Keys on pages outside the cache are left out.
- * The workspace (at least 256 bytes, 256-byte aligned) must be zero before its
- * first use, may be that of ra_kv4_attention, and receives the status as there.
+ * The workspace is one for ra_kv4_attention with the same arguments (of the same size, and
+ * they may share it), and receives the status as there.
  */
 ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_stride, int32_t num_q_tokens,
                          int32_t num_q_heads, const int32_t* block_table, int32_t table_width, int64_t table_stride,

@@ -245,7 +245,7 @@ def test_refused_contents_are_reported_and_stay_in_bounds(ra):
         guard = torch.full((c.N * c.page + 2048,), 7.5, device="cuda")
         w = guard[1024:1024 + c.N * c.page]
         w.copy_(c.before)
-        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        ws = ra.kv4_attention_workspace(c.cache, 6, 4)
         ra.kv4_weights(c.q.cuda(), c.cache, c.table, c.lens_t, c.cu_t, lse, w, workspace=ws)
         with pytest.raises(ra.RingAttnError) as e:
             ra.kv4_status(ws)
@@ -300,7 +300,7 @@ def test_results_repeat_on_streams_and_in_graphs(ra):
             runs.append(w)
     torch.cuda.synchronize()
     assert all(torch.equal(w, want) for w in runs)
-    w, ws, lens = c.before.cuda(), torch.zeros(256, dtype=torch.uint8, device="cuda"), c.lens_t.clone()
+    w, ws, lens = c.before.cuda(), ra.kv4_attention_workspace(c.cache, 5, 16, 2), c.lens_t.clone()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         ra.kv4_weights(q, c.cache, c.table, lens, c.cu_t, lse, w, new_lens=new, max_q_len=2, workspace=ws)
@@ -333,3 +333,151 @@ def test_refusals(ra):
         ra.kv4_weights(**dict(ok, workspace=torch.zeros(128, dtype=torch.uint8, device="cuda")))
     with pytest.raises(ra.RingAttnError, match="multiple"):
         ra.kv4_weights(**dict(ok, q=torch.zeros(2, 3, 64, dtype=torch.bfloat16, device="cuda"), lse=lse[:3].contiguous()))
+
+
+# ------------------------------------------------------------------ many rows: the tile kernel
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", [
+    (128, 8, 2, [300], [40]), (64, 2, 2, [1000], [130]), (256, 4, 2, [700], [50]),
+    (128, 15, 3, [257, 900], [33, 100]), (64, 7, 1, [2000, 129, 128], [64, 20, 128]),
+    (256, 28, 4, [513, 90], [31, 90]), (128, 32, 8, [5000], [64])])
+def test_prompt_parts(ra, d, Hq, Hkv, lens, qlens, causal):
+    Case(ra, d + Hq, lens, qlens, Hq, Hkv, d, 32).check(ra, causal, max_q_len=max(qlens))
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,n", [(128, 160, 1, 3), (256, 130, 2, 2), (64, 129, 1, 1), (256, 65, 1, 4), (128, 127, 1, 5)])
+def test_large_groups(ra, d, Hq, Hkv, n):
+    """Query tiles that hold a part of one token's heads, or one token and little else."""
+    Case(ra, Hq, [400, 90], [n, n], Hq, Hkv, d, 16).check(ra, max_q_len=n)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", [(128, 80, 40, [200], [40]), (64, 64, 64, [256, 17], [70, 64]),
+                                                 (256, 24, 24, [130], [128]), (128, 16, 16, [1500, 3], [100, 2])])
+def test_blocks_of_many_ctas(ra, d, Hq, Hkv, lens, qlens):
+    """Few blocks of keys with many heads: their sums come from several CTAs."""
+    Case(ra, Hq + d, lens, qlens, Hq, Hkv, d, 64).check(ra, max_q_len=max(qlens))
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 8, 2), (128, 32, 8), (256, 16, 8)])
+def test_prompt_parts_among_single_tokens(ra, d, Hq, Hkv):
+    lens = [700, 1, 300, 64, 2000, 0, 90, 512]
+    qlens = [1, 1, 200, 5, 16, 0, 0, 333]
+    c = Case(ra, 9 + d, lens, qlens, Hq, Hkv, d, 64)
+    c.check(ra, max_q_len=333)
+    c.check(ra, False, max_q_len=333)
+
+
+def test_many_requests_of_many_rows(ra):
+    rng = np.random.default_rng(6)
+    lens = [int(x) for x in rng.integers(1, 700, 300)]
+    qlens = [int(min(n, x)) for n, x in zip(lens, rng.integers(0, 120, 300))]
+    Case(ra, 27, lens, qlens, 4, 2, 64, 16).check(ra, max_q_len=120)
+
+
+def test_one_request_without_rows(ra):
+    """A call that names a long request and brings none: only the new tokens' sums change."""
+    c = Case(ra, 8, [1000], [0], 4, 2, 128, 16)
+    c.new = [600]
+    w = c.before.cuda()
+    z, q = torch.zeros(4, 80).cuda(), torch.zeros(80, 4, 128, dtype=torch.bfloat16).cuda()
+    ra.kv4_weights(q, c.cache, c.table, c.lens_t, c.cu_t, z, w, new_lens=i32(c.new), check=True)
+    want = c.before.clone()
+    want[torch.tensor(c.slots[0][400:])] = 0
+    assert torch.equal(w.cpu(), want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_and_keys_that_are_no_numbers_in_tiles(ra, d):
+    lens, qlens = [600, 300], [90, 70]
+    rng = np.random.default_rng(d)
+    keys = [torch.tensor(rng.standard_normal((n, 2, d)), dtype=torch.float32).to(torch.bfloat16) for n in lens]
+    keys[0][599, 1, 3] = float("nan")                            # the newest token: seen by the last row alone
+    keys[0][17, 0, 50] = float("inf")
+    keys[1][299, 0, 0] = float("nan")
+    c = Case(ra, 2, lens, qlens, 4, 2, d, 16, keys=keys)
+    z = torch.full((4, 160), 3.0).cuda()
+    z[2, 0] = z[1, 89] = float("-inf")
+    z[3, 159] = float("-inf")                                    # the only rows that see request 1's newest key: those of head 0 to 2
+    z[0, 30] = float("nan")                                      # request 0, row 30: sees 541 keys
+    c.q[95, 1, 7] = float("nan")                                 # request 1, row 5: sees 236
+    q = f64(c.q)
+    want = E.weights(q, c.keys, c.lens, c.cu, f64(z), True, 1 / math.sqrt(d))
+    w = c.run(ra, z, new=False, check=True)
+    for r in range(2):
+        assert np.array_equal(np.isnan(f64(w)[c.slots[r]]), np.isnan(want[r]))
+    assert np.isnan(want[0]).nonzero()[0].tolist() == list(range(541)) + [599]
+    assert np.isnan(want[1]).nonzero()[0].tolist() == list(range(236)) + [299]
+    c.compare(w, z, new=False)
+    # a request whose rows have no softmax at all adds nothing, whatever its keys are
+    z[:, 90:] = float("-inf")
+    w = c.run(ra, z, new=False, check=True)
+    assert np.array_equal(f64(w)[c.slots[1]], f64(c.before)[c.slots[1]])
+
+
+def test_bad_pages_lengths_and_offsets_in_tiles(ra):
+    def fresh():
+        return Case(ra, 43, [800, 100, 900], [70, 1, 80], 4, 2, 64, 16, spare=3)
+
+    lse = fresh().lse(ra)
+    ref = f64(fresh().run(ra, lse, new=False, max_q_len=80))
+    for what in ("page", "far page", "length", "offset"):
+        c = fresh()
+        if what == "page":
+            c.table[2, 30] = -1
+        elif what == "far page":
+            c.table[2, 30] = 1 << 30
+        elif what == "length":
+            c.lens_t[2] = 1 << 20
+        else:
+            c.cu_t[3] = 200
+        w, ws = c.before.cuda(), ra.kv4_attention_workspace(c.cache, 151, 4, 80)
+        ra.kv4_weights(c.q.cuda(), c.cache, c.table, c.lens_t, c.cu_t, lse, w, max_q_len=80, workspace=ws)
+        with pytest.raises(ra.RingAttnError) as e:
+            ra.kv4_status(ws)
+        assert e.value.status == 1
+        got, want = f64(w), ref.copy()
+        if "page" in what:
+            want[c.slots[2][480:496]] = f64(c.before)[c.slots[2][480:496]]
+        else:
+            want[c.slots[2]] = f64(c.before)[c.slots[2]]
+        assert np.array_equal(got, want)
+        ra.kv4_weights(c.q.cuda(), fresh().cache, fresh().table, fresh().lens_t, fresh().cu_t, lse, w, max_q_len=80, workspace=ws)
+        ra.kv4_status(ws)
+
+
+def test_strided_queries_and_graphs_in_tiles(ra):
+    c = Case(ra, 33, [900, 333], [64, 40], 8, 2, 128, 32)
+    lse = c.lse(ra)
+    wide = torch.randn(104, 12, 128).to(torch.bfloat16).cuda()
+    wide[:, 2:10] = c.q.cuda()
+    want = c.check(ra, lse=lse, q=wide[:, 2:10], max_q_len=64)
+    want = c.run(ra, lse, max_q_len=64)
+    q, new, lens, cu = c.q.cuda(), i32(c.new), c.lens_t.clone(), c.cu_t.clone()
+    w, ws = c.before.cuda(), ra.kv4_attention_workspace(c.cache, 104, 8, 64)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ra.kv4_weights(q, c.cache, c.table, lens, cu, lse, w, new_lens=new, max_q_len=64, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(w, want)
+    for n0, n1, L in ((1, 3, 500), (0, 0, 0), (30, 40, 901)):    # rows and lengths change between replays
+        cu.copy_(i32([0, n0, n0 + n1]))
+        lens[0] = L
+        w.copy_(c.before)
+        graph.replay()
+        alone = c.before.cuda()
+        ra.kv4_weights(q, c.cache, c.table, lens, cu, lse, alone, new_lens=new, max_q_len=64)
+        torch.cuda.synchronize()
+        assert torch.equal(w, alone)
+        ra.kv4_status(ws)
+
+
+def test_both_kernels_agree(ra):
+    """The same rows by either kernel (max_q_len selects): fp32 sums in another order."""
+    c = Case(ra, 71, [3000, 40], [70, 40], 8, 2, 128, 64)
+    lse = c.lse(ra)
+    a, b = c.run(ra, lse, max_q_len=70), c.run(ra, lse, max_q_len=1)
+    c.compare(a, lse)
+    c.compare(b, lse)
+    assert torch.allclose(a, b, rtol=2e-5, atol=1e-7)
