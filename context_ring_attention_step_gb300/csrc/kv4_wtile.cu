@@ -5,10 +5,11 @@
 // Here products and exponentials dominate: 2 D flops and one exponential a row and
 // key.  Keys are the rows of S^T = K Q^T, so that a thread owns a key: it adds up
 // the exponentials of a row of tensor memory, and nothing is exchanged between
-// threads.  A unit is 256 keys (head_dim 256: 128) of one request and head; K stays in
-// shared memory, expanded once, while the head's query rows stream past, 128 (64) at a time,
-// straight from the query tensor (TMA).  Both are bf16: codes times scales have 6
-// significant bits.
+// threads.  A unit is 256 keys (head_dim 256: 128) of one request and head.  The keys lie in
+// tensor memory as the products' A operand, expanded once, while the head's query rows stream past,
+// 128 (64) at a time, straight from the query tensor (TMA): from shared memory both operands
+// would be read at 128 bytes a clock, all there is.  Both are bf16: codes times scales
+// have 6 significant bits.
 //
 // Warp roles (512 threads):
 //   warp 0        UMMA issuer (owns tensor memory)
@@ -16,8 +17,8 @@
 //   warps 2, 3    the tiles' log-sum-exps and key limits, tiles in turn
 //   warps 4-11    exponentials and sums: a thread is a key; at head_dim 256 warps
 //                 4-7 take the first half of a tile's rows and 8-11 the second
-//   warps 12-15   cache tiles -> bf16 keys
-// Tensor memory (512 columns): two buffers of S^T, 256 columns each.
+//   warps 12-15   cache -> bf16 keys: a thread is a key here too
+// Tensor memory (512 columns): the keys (D / 2 columns for 128 of them), then a ring of S^T tiles.
 // Items (block of keys, head) lie on one line that the CTAs cut evenly; of a block
 // whose heads went to several CTAs the one that brings the last sum adds them, in
 // the CTAs' order.
@@ -43,13 +44,14 @@ struct WTile {
   static constexpr int kKeys = 128 * kKeyTiles;
   static constexpr int kN = D == 256 ? 64 : 128;      // query rows of a tile
   static constexpr int kCols = kN * kKeyTiles / 2;    // columns of a thread
-  static constexpr int kKTile = 128 * D * 2;
-  static constexpr int kKBytes = kKeyTiles * kKTile;  // of one of the two stages
+  static constexpr int kKCols = D / 2;                // tensor memory columns of 128 keys
+  static constexpr int kSRing = D == 256 ? 4 : 3;     // S^T tiles (128 keys x kN rows) in tensor memory
+  static constexpr int kSOff = kKeyTiles * kKCols;
+  static_assert(kSOff + kSRing * kN <= 512, "tensor memory");
   static constexpr int kQTile = kN * D * 2;
-  static constexpr int kQStages = D == 64 ? 4 : 2;
-  static constexpr int kQOff = 2 * kKBytes;
-  static constexpr int kLseOff = kQOff + kQStages * kQTile;
-  static constexpr int kLseStage = 8 * kN + 16;       // - lse (log2), limits, their smallest
+  static constexpr int kQStages = D == 64 ? 8 : 6;
+  static constexpr int kLseOff = kQStages * kQTile;
+  static constexpr int kLseStage = 8 * kN + 16;       // - lse (log2), limits, the smallest and the largest of them
   static constexpr int kPartOff = kLseOff + kLseStages * kLseStage;
   static constexpr int kBarOff = kPartOff + 512;      // (half sums of 128 keys: head_dim 256)
   static constexpr int kSmem = kBarOff + 512 + 1024;  // barriers, alignment slack
@@ -59,78 +61,73 @@ struct WTile {
 
 __device__ __forceinline__ void keys_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// One lane's share of a 16-token cache tile's keys.
+// One token's keys of one head: the codes in order (8 dims a word), and the scales' bytes.
 template <int D>
-struct Words {
-  uint4 w[D / 64];
-  uint32_t s, s1;  // scales (s1: the second word, head_dim 256)
+struct KeyWords {
+  uint32_t w[D / 8];
+  uint32_t s[D / 64];  // scales of groups 4 i .. 4 i + 3
 };
+// From the cache tile that holds token t (of 16).  A token's codes are D / 2 bytes in whole words of
+// 16 bytes (head_dim 64: of 8), its scales D / 64 of every 4, or neighbouring bytes (Kv4Layout).
 template <int D>
-__device__ __forceinline__ void load_words(Words<D>& t, const uint8_t* tile, int lane) {
+__device__ __forceinline__ void load_key(KeyWords<D>& k, const uint8_t* tile, int t) {
   using L = Kv4Layout<D>;
+  const int r = t & 7, h = t >> 3;
+  if (D == 64) {
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) t.w[i] = __ldg(reinterpret_cast<const uint4*>(tile + L::kKCodes + 512 * i + 16 * lane));
-  if (D == 256) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(tile + L::kKScales) + lane);
-    t.s = x.x;
-    t.s1 = x.y;
-  } else if (D == 64) {
-    t.s = __ldg(reinterpret_cast<const uint16_t*>(tile + L::kKScales) + lane);
+    for (int g = 0; g < 4; ++g) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(tile + (4 * r + g) * 16 + h * 8));
+      k.w[2 * g] = x.x;
+      k.w[2 * g + 1] = x.y;
+    }
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(tile + L::kKScales + 8 * r));  // [group][h]
+    k.s[0] = __byte_perm(x.x, x.y, h ? 0x7531 : 0x6420);
+  } else if (D == 128) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(tile + h * 512 + (4 * r + c) * 16));
+      k.w[4 * c] = x.x;
+      k.w[4 * c + 1] = x.y;
+      k.w[4 * c + 2] = x.z;
+      k.w[(4 * c + 3) % (D / 8)] = x.w;
+    }
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(tile + L::kKScales + 16 * r));  // [quarter][h][2]
+    k.s[0] = __byte_perm(x.x, x.y, h ? 0x7632 : 0x5410);
+    k.s[D == 128 ? 1 : 0] = __byte_perm(x.z, x.w, h ? 0x7632 : 0x5410);
   } else {
-    t.s = __ldg(reinterpret_cast<const uint32_t*>(tile + L::kKScales) + lane);
-  }
-}
-// Eight codes and their scale byte (of a word) -> 16 bytes of bf16.
-__device__ __forceinline__ void expand8(uint32_t addr, uint32_t codes, uint32_t scales, int i) {
-  const uint4 v = kv4_expand_half(codes, (scales >> (8 * i)) & 0xffu);
-  st_shared_v4(addr, v.x, v.y, v.z, v.w);
-}
-// Lane 4 r + c of a cache tile holds tokens r and r + 8 and dims [c D/4, (c+1) D/4).  Where
-// its 16-byte chunks go in a tile of 128-byte-swizzled rows (64 dims a row, the next 64
-// 16 KB on); cache tile `sub` lies 2048 sub bytes on, tokens 8 to 15 of it 1024.  At
-// head_dim 128 lanes with c >= 2 write their chunks in another order (2 before 0), so that
-// the eight lanes of a shared-memory pass touch eight different chunks.
-template <int D>
-struct Places {
-  uint32_t k[D / 32];
-  bool turn;
-  __device__ __forceinline__ explicit Places(int lane) {
-    const int r = lane >> 2, c = lane & 3;
-    turn = D == 128 && c >= 2;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int ch = D == 64 ? 2 * c + i : D == 256 ? i : 4 * (c & 1) + (turn ? i ^ 2 : i);
-      k[i] = (D == 64 ? 0 : D == 256 ? c * 16384 : (c >> 1) * 16384) + r * 128 + ((ch ^ r) << 4);
-    }
-  }
-};
-template <int D>
-__device__ __forceinline__ void expand_keys(uint32_t base, const Words<D>& t, const Places<D>& pl) {
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (D == 64) {
-      expand8(base + pl.k[0] + 1024 * h, h ? t.w[0].z : t.w[0].x, t.s, h);
-      expand8(base + pl.k[1] + 1024 * h, h ? t.w[0].w : t.w[0].y, t.s, h);
-    } else if (D == 256) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 w = t.w[(2 * h + (i >> 2)) % (D / 64)];
-        expand8(base + pl.k[i % (D / 32)] + 1024 * h, (i & 3) == 0 ? w.x : (i & 3) == 1 ? w.y : (i & 3) == 2 ? w.z : w.w,
-                h ? t.s1 : t.s, i >> 1);
+      for (int i = 0; i < 2; ++i) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(tile + (2 * h + i) * 512 + (4 * r + c) * 16));
+        k.w[(8 * c + 4 * i) % (D / 8)] = x.x;
+        k.w[(8 * c + 4 * i + 1) % (D / 8)] = x.y;
+        k.w[(8 * c + 4 * i + 2) % (D / 8)] = x.z;
+        k.w[(8 * c + 4 * i + 3) % (D / 8)] = x.w;
       }
-    } else {
-      const uint4 w = t.w[h % (D / 64)];
-      const bool sw = pl.turn;
-      const int a = 2 * h + (sw ? 1 : 0), b = 2 * h + (sw ? 0 : 1);
-      expand8(base + pl.k[0] + 1024 * h, sw ? w.z : w.x, t.s, a);
-      expand8(base + pl.k[1] + 1024 * h, sw ? w.w : w.y, t.s, a);
-      expand8(base + pl.k[D == 128 ? 2 : 0] + 1024 * h, sw ? w.x : w.z, t.s, b);
-      expand8(base + pl.k[D == 128 ? 3 : 0] + 1024 * h, sw ? w.y : w.w, t.s, b);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(tile + L::kKScales + 32 * r + 16 * i));  // [quarter][h][4]
+      k.s[(2 * i) % (D / 64)] = h ? x.y : x.x;
+      k.s[(2 * i + 1) % (D / 64)] = h ? x.w : x.z;
     }
+  }
+}
+// Expand them into this thread's row of tensor memory, 32 columns (64 dims) at a time.
+template <int D>
+__device__ __forceinline__ void expand_key(uint32_t taddr, const KeyWords<D>& k) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    uint32_t o[32];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint4 v = kv4_expand_half(k.w[8 * i + j], (k.s[i] >> (8 * (j >> 1))) & 0xffu);
+      o[4 * j] = v.x;
+      o[4 * j + 1] = v.y;
+      o[4 * j + 2] = v.z;
+      o[4 * j + 3] = v.w;
+    }
+    tmem_st32(taddr + 32 * i, o);
   }
 }
 
@@ -197,22 +194,22 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
   const Kv4AttnParams& p = wp.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sK = smem_u32(smem), sQ = sK + C::kQOff;
+  const uint32_t sQ = smem_u32(smem);
   auto lse_of = [&](int s) { return reinterpret_cast<float*>(smem + C::kLseOff + s * C::kLseStage); };
-  auto lim_of = [&](int s) { return reinterpret_cast<int*>(lse_of(s) + N); };  // [N], then the smallest
+  auto lim_of = [&](int s) { return reinterpret_cast<int*>(lse_of(s) + N); };  // [N], then the smallest and the largest
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  const uint32_t b_kfull = smem_u32(bars);            // [2] keys expanded (4 warps)
+  const uint32_t b_kfull = smem_u32(bars);            // [2] a tile's keys expanded (4 warps)
   const uint32_t b_kempty = smem_u32(bars + 2);       // [2]
   const uint32_t b_qfull = smem_u32(bars + 4);        // [QS]
-  const uint32_t b_qempty = smem_u32(bars + 8);       // [QS]
-  const uint32_t b_lfull = smem_u32(bars + 12);       // [LS]
-  const uint32_t b_lempty = smem_u32(bars + 12 + LS); // [LS] (8 warps)
-  const uint32_t b_sfull = smem_u32(bars + 12 + 2 * LS);   // [2] S^T ready
-  const uint32_t b_sempty = smem_u32(bars + 14 + 2 * LS);  // [2] (8 warps)
-  const uint32_t b_drain = smem_u32(bars + 16 + 2 * LS);
-  int* s_int = reinterpret_cast<int*>(bars + 17 + 2 * LS);  // abort, bad, last, where a wait was given up
+  const uint32_t b_qempty = smem_u32(bars + 12);      // [QS]
+  const uint32_t b_lfull = smem_u32(bars + 20);       // [LS]
+  const uint32_t b_lempty = smem_u32(bars + 20 + LS); // [LS] (8 warps)
+  const uint32_t b_sfull = smem_u32(bars + 20 + 2 * LS);   // [kSRing] an S^T tile ready
+  const uint32_t b_sempty = smem_u32(bars + 24 + 2 * LS);  // [kSRing] (the warps that read it)
+  const uint32_t b_drain = smem_u32(bars + 28 + 2 * LS);
+  int* s_int = reinterpret_cast<int*>(bars + 29 + 2 * LS);  // abort, bad, last, where a wait was given up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_int + 4);
-  static_assert((17 + 2 * LS) * 8 + 20 <= 512, "barriers");
+  static_assert(QS <= 8 && (29 + 2 * LS) * 8 + 20 <= 512, "barriers");
   __shared__ long long s_sum[kThreads / 32], s_found[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -222,8 +219,10 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_kfull + 8 * i, 4);
       mbar_init(b_kempty + 8 * i, 1);
+    }
+    for (int i = 0; i < C::kSRing; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
-      mbar_init(b_sempty + 8 * i, 8);
+      mbar_init(b_sempty + 8 * i, 8 / C::kKeyTiles);
     }
     for (int i = 0; i < QS; ++i) {
       mbar_init(b_qfull + 8 * i, 1);
@@ -278,32 +277,32 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
-      const uint64_t d0 = sdesc_sw128(sK, 0, 1024);
-      uint32_t g = 0, item = 0;
+      const uint64_t d0 = sdesc_sw128(sQ, 0, 1024);
+      uint32_t qs = 0, qph = 0, sb = 0, sph = 0, item = 0;  // stages and their parities
       bool ok = true;
       while (ok && wk.next()) {
+        const int tiles = wk.job.tiles;
         for (long long x = wk.x0; x < wk.x1 && ok; ++x, ++item) {
-          const uint32_t ks = item & 1;
-          if (!(ok = mbar_wait(b_kfull + 8 * ks, (item >> 1) & 1, ab, 160))) break;
-          for (int t = 0; t < wk.job.tiles; ++t, ++g) {
-            const uint32_t qs = g % QS, sb = g & 1;
-            if (!(ok = mbar_wait(b_qfull + 8 * qs, (g / QS) & 1, ab, 161))) break;
-            if (!(ok = mbar_wait(b_sempty + 8 * sb, ((g >> 1) & 1) ^ 1, ab, 162))) break;
-            tc_fence_after();
-            const uint64_t b = opaque(d0);
-            const uint64_t dq = sdesc_at(b, (uint32_t)(C::kQOff + qs * C::kQTile), 0);
+          for (int t = 0; t < tiles; ++t) {
+            if (!(ok = mbar_wait(b_qfull + 8 * qs, qph, ab, 161))) break;
+            const uint64_t dq = sdesc_at(opaque(d0), (uint32_t)(qs * C::kQTile), 0);
 #pragma unroll
             for (int kt = 0; kt < C::kKeyTiles; ++kt) {
-              const uint64_t dk = sdesc_at(b, (uint32_t)(ks * C::kKBytes + kt * C::kKTile), 0);
+              if (t == 0 && !(ok = mbar_wait(b_kfull + 8 * kt, item & 1, ab, 160))) break;
+              if (!(ok = mbar_wait(b_sempty + 8 * sb, sph ^ 1, ab, 162))) break;
+              tc_fence_after();
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                umma_ss(tmem + sb * 256 + kt * 128, sdesc_at(dk, (kk >> 2) * 16384 + (kk & 3) * 32, 16),
+                umma_ts(tmem + C::kSOff + sb * N, tmem + kt * C::kKCols + kk * 8,
                         sdesc_at(dq, (kk >> 2) * (N * 128) + (kk & 3) * 32, 16), C::kIdesc, kk > 0);
+              umma_commit(b_sfull + 8 * sb);
+              if (t + 1 == tiles) umma_commit(b_kempty + 8 * kt);
+              if (++sb == C::kSRing) { sb = 0; sph ^= 1; }
             }
-            umma_commit(b_sfull + 8 * sb);
+            if (!ok) break;
             umma_commit(b_qempty + 8 * qs);
+            if (++qs == QS) { qs = 0; qph ^= 1; }
           }
-          umma_commit(b_kempty + 8 * ks);
         }
       }
       if (!ok) {  // let issued MMAs finish before tensor memory is released
@@ -316,18 +315,23 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       uint32_t g = 0;
       bool ok = true;
       while (ok && wk.next()) {
+        const int tiles = wk.job.tiles;
+        int head = (int)(wk.x0 % Hkv);
         for (long long x = wk.x0; x < wk.x1 && ok; ++x) {
-          const int head = (int)(x % Hkv);
-          for (int t = 0; t < wk.job.tiles; ++t, ++g) {
+          int tok = wk.job.rq.b, part = 0;
+          for (int t = 0; t < tiles; ++t, ++g) {
             const uint32_t qs = g % QS;
             if (!(ok = mbar_wait(b_qempty + 8 * qs, ((g / QS) & 1) ^ 1, ab, 163))) break;
             mbar_expect_tx(b_qfull + 8 * qs, bytes);
-            const int h = head * G + (t % tl.per_token) * N;
-            const int tok = wk.job.rq.b + (tl.per_token > 1 ? t / tl.per_token : t * tl.tokens);
 #pragma unroll
             for (int s = 0; s < D / 64; ++s)
-              tma_load_3d(sQ + qs * C::kQTile + s * (N * 128), &tq, b_qfull + 8 * qs, 64 * s, h, tok);
+              tma_load_3d(sQ + qs * C::kQTile + s * (N * 128), &tq, b_qfull + 8 * qs, 64 * s, head * G + part * N, tok);
+            if (++part == tl.per_token) {
+              part = 0;
+              tok += tl.tokens;
+            }
           }
+          if (++head == Hkv) head = 0;
         }
       }
       if (!ok)  // copies under way land before the CTA's shared memory is given up
@@ -336,6 +340,16 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       // ---------------------------------------------------------- log-sum-exps and limits
       // (values of the next tile are on their way while this one's wait for their place)
       constexpr int V = N / 32;
+      // where this lane's columns lie in a tile: token and head of the group (a tile of a part
+      // of one token: head alone), past any of both for columns that are none
+      int col_tok[V], col_head[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = lane + 32 * i;
+        col_tok[i] = tl.per_token > 1 ? 0 : c / G;
+        col_head[i] = tl.per_token > 1 ? c : c - col_tok[i] * G;
+        if (tl.per_token == 1 && c >= tl.tokens * G) col_head[i] = 0x40000000;
+      }
       float v[V];
       int lim[V];
       uint32_t g = 0, held = 0;  // `held`: the tile in v and lim
@@ -345,7 +359,7 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
         ok = mbar_wait(b_lempty + 8 * ls, ((held / LS) & 1) ^ 1, ab, 164);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        int least = 0x7fffffff;
+        int least = 0x7fffffff, most = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           // rows that are none, or have no softmax (lse = -inf: they see no key), see no key here
@@ -354,38 +368,47 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
           lse_of(ls)[lane + 32 * i] = dead ? neg_inf() : -v[i] * kLog2e;
           lim_of(ls)[lane + 32 * i] = lim[i];
           least = min(least, lim[i]);
+          most = max(most, lim[i]);
         }
         least = __reduce_min_sync(0xffffffffu, least);
-        if (lane == 0) lim_of(ls)[N] = least;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) *reinterpret_cast<int2*>(lim_of(ls) + N) = make_int2(least, most);
         __syncwarp();
         if (lane == 0) mbar_arrive(b_lfull + 8 * ls);
       };
       while (ok && wk.next()) {
         const Kv4Request& rq = wk.job.rq;
+        const int tiles = wk.job.tiles, n = rq.n, top = p.causal ? rq.L - n + 1 : rq.L;
+        const float* lse = wp.lse + rq.b;
+        int head = (int)(wk.x0 % Hkv);
         for (long long x = wk.x0; x < wk.x1 && ok; ++x) {
-          const int head = (int)(x % Hkv);
-          for (int t = 0; t < wk.job.tiles && ok; ++t, ++g) {
-            if ((g & 1) != (uint32_t)(warp - 2)) continue;
-            float nv[V];
-            int nl[V];
+          int tok0 = 0, part = 0;  // the tile's first token, and which part of a token
+          for (int t = 0; t < tiles && ok; ++t, ++g) {
+            if ((g & 1) == (uint32_t)(warp - 2)) {
+              float nv[V];
+              int nl[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const int c = lane + 32 * i;
-              const int gi = tl.per_token > 1 ? (t % tl.per_token) * N + c : c % G;
-              const int tok = tl.per_token > 1 ? t / tl.per_token : t * tl.tokens + c / G;
-              const bool valid = gi < G && tok < rq.n && (tl.per_token > 1 || c < tl.tokens * G);
-              nv[i] = valid ? __ldg(wp.lse + (size_t)(head * G + gi) * p.Tq + rq.b + tok) : neg_inf();
-              nl[i] = valid ? kv4_key_limit(p, rq, tok * G) : 0;
-            }
-            if (have) put();
+              for (int i = 0; i < V; ++i) {
+                const int gi = part * N + col_head[i], tok = tok0 + col_tok[i];
+                const bool valid = gi < G && tok < n;
+                nv[i] = valid ? __ldg(lse + (size_t)(head * G + gi) * p.Tq + tok) : neg_inf();
+                nl[i] = valid ? max(0, min(rq.L, p.causal ? top + tok : top)) : 0;
+              }
+              if (have) put();
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              v[i] = nv[i];
-              lim[i] = nl[i];
+              for (int i = 0; i < V; ++i) {
+                v[i] = nv[i];
+                lim[i] = nl[i];
+              }
+              held = g;
+              have = true;
             }
-            held = g;
-            have = true;
+            if (++part == tl.per_token) {
+              part = 0;
+              tok0 += tl.tokens;
+            }
           }
+          if (++head == Hkv) head = 0;
         }
       }
       if (have && ok) put();
@@ -397,12 +420,37 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
     const int gp = (warp - 4) >> 2, row = tid - 128 * (1 + gp);
     const int key_t = C::kKeyTiles == 2 ? 128 * gp + row : row;  // key of the block
     const int col0 = C::kKeyTiles == 2 ? 0 : NC * gp;
-    const uint32_t tS = tmem_addr(tmem, (uint32_t)(warp & 3) * 32, C::kKeyTiles == 2 ? 128 * gp : col0);
+    const uint32_t tS = tmem_addr(tmem, (uint32_t)(warp & 3) * 32, C::kSOff + col0);
     const float c1 = p.scale * kLog2e;
     const uint64_t c2 = f2_pack(c1, c1);
-    uint32_t g = 0;
+    uint32_t g = 0, sb = C::kKeyTiles == 2 ? gp : 0, sph = 0;  // tiles so far; this thread's next S^T tile and its parity
     bool ok = true;
     float acc = 0.f;
+    uint64_t sum_a, sum_b;
+    auto columns = [&](const uint32_t (&s)[32], const float4* nl) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 m = nl[i];
+        float e[4];
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2, f2_pack(m.x, m.y)), e[0], e[1]);
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), c2, f2_pack(m.z, m.w)), e[2], e[3]);
+        sum_a = f2_add(sum_a, f2_pack(ex2_approx(e[0]), ex2_approx(e[1])));
+        sum_b = f2_add(sum_b, f2_pack(ex2_approx(e[2]), ex2_approx(e[3])));
+      }
+    };
+    auto masked_columns = [&](const uint32_t (&s)[32], const float4* nl, const int4* lim, int key) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 m = nl[i];
+        const int4 l = lim[i];
+        const float e0 = ex2_approx(fmaf(__uint_as_float(s[4 * i]), c1, m.x));
+        const float e1 = ex2_approx(fmaf(__uint_as_float(s[4 * i + 1]), c1, m.y));
+        const float e2 = ex2_approx(fmaf(__uint_as_float(s[4 * i + 2]), c1, m.z));
+        const float e3 = ex2_approx(fmaf(__uint_as_float(s[4 * i + 3]), c1, m.w));
+        sum_a = f2_add(sum_a, f2_pack(key < l.x ? e0 : 0.f, key < l.y ? e1 : 0.f));
+        sum_b = f2_add(sum_b, f2_pack(key < l.z ? e2 : 0.f, key < l.w ? e3 : 0.f));
+      }
+    };
     while (wk.next()) {
       const Job& job = wk.job;
       for (long long x = wk.x0; x < wk.x1; ++x) {
@@ -410,49 +458,62 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
         const int key = blk * C::kKeys + key_t, key_end = (key & ~127) + 128;
         if (head == 0 || x == wk.x0) acc = 0.f;
         for (int t = 0; t < job.tiles; ++t, ++g) {
-          const uint32_t ls = g % LS, sb = g & 1;
-          if (ok) ok = mbar_wait(b_lfull + 8 * ls, (g / LS) & 1, ab, 165) && mbar_wait(b_sfull + 8 * sb, (g >> 1) & 1, ab, 166);
+          const uint32_t ls = g % LS;
+          if (ok) ok = mbar_wait(b_lfull + 8 * ls, (g / LS) & 1, ab, 165);
+          if (ok) ok = mbar_wait(b_sfull + 8 * sb, sph, ab, 166);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          uint32_t s[NC / 32][32];
-#pragma unroll
-          for (int c = 0; c < NC / 32; ++c) tmem_ld32(tS + sb * 256 + 32 * c, s[c]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < NC / 32; ++c) reg_fence32(s[c]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_sempty + 8 * sb);
           const float4* nl = reinterpret_cast<const float4*>(lse_of(ls) + col0);
-          uint64_t sum_a = 0, sum_b = 0;
-          if (key_end <= lim_of(ls)[N]) {
-#pragma unroll
-            for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 m = nl[8 * c + i];
-                float e[4];
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c][4 * i]), __uint_as_float(s[c][4 * i + 1])), c2, f2_pack(m.x, m.y)), e[0], e[1]);
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c][4 * i + 2]), __uint_as_float(s[c][4 * i + 3])), c2, f2_pack(m.z, m.w)), e[2], e[3]);
-                sum_a = f2_add(sum_a, f2_pack(ex2_approx(e[0]), ex2_approx(e[1])));
-                sum_b = f2_add(sum_b, f2_pack(ex2_approx(e[2]), ex2_approx(e[3])));
-              }
+          const int4* lim = reinterpret_cast<const int4*>(lim_of(ls) + col0);
+          const int2 ends = *reinterpret_cast<const int2*>(lim_of(ls) + N);
+          const bool whole = key_end <= ends.x, none = key_end - 128 >= ends.y;  // all rows see all keys; none does any
+          auto release = [&]() {  // all columns are in registers: the S^T tile may be written again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_sempty + 8 * sb);
+          };
+          sum_a = sum_b = 0;
+          if (none) {
+            release();
+          } else if constexpr (NC == 32) {
+            uint32_t s[32];
+            tmem_ld32(tS + sb * N, s);
+            tmem_ld_wait();
+            reg_fence32(s);
+            release();
+            if (whole) columns(s, nl);
+            else masked_columns(s, nl, lim, key);
           } else {
-            const int4* lim = reinterpret_cast<const int4*>(lim_of(ls) + col0);
-#pragma unroll
-            for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 m = nl[8 * c + i];
-                const int4 l = lim[8 * c + i];
-                const float e0 = ex2_approx(fmaf(__uint_as_float(s[c][4 * i]), c1, m.x));
-                const float e1 = ex2_approx(fmaf(__uint_as_float(s[c][4 * i + 1]), c1, m.y));
-                const float e2 = ex2_approx(fmaf(__uint_as_float(s[c][4 * i + 2]), c1, m.z));
-                const float e3 = ex2_approx(fmaf(__uint_as_float(s[c][4 * i + 3]), c1, m.w));
-                sum_a = f2_add(sum_a, f2_pack(key < l.x ? e0 : 0.f, key < l.y ? e1 : 0.f));
-                sum_b = f2_add(sum_b, f2_pack(key < l.z ? e2 : 0.f, key < l.w ? e3 : 0.f));
-              }
+            // half of the columns are on their way while the other half is worked on
+            uint32_t s[2][32], u[2][32];
+            tmem_ld32(tS + sb * N, s[0]);
+            tmem_ld32(tS + sb * N + 32, s[1]);
+            tmem_ld_wait();
+            reg_fence32(s[0]);
+            reg_fence32(s[1]);
+            tmem_ld32(tS + sb * N + 64, u[0]);
+            tmem_ld32(tS + sb * N + 96, u[1]);
+            if (whole) {
+              columns(s[0], nl);
+              columns(s[1], nl + 8);
+            } else {
+              masked_columns(s[0], nl, lim, key);
+              masked_columns(s[1], nl + 8, lim + 8, key);
+            }
+            tmem_ld_wait();
+            reg_fence32(u[0]);
+            reg_fence32(u[1]);
+            release();
+            if (whole) {
+              columns(u[0], nl + 16);
+              columns(u[1], nl + 24);
+            } else {
+              masked_columns(u[0], nl + 16, lim + 16, key);
+              masked_columns(u[1], nl + 24, lim + 24, key);
+            }
           }
+          sb += C::kKeyTiles;
+          if (sb >= C::kSRing) { sb -= C::kSRing; sph ^= 1; }
           __syncwarp();
           if (lane == 0) mbar_arrive(b_lempty + 8 * ls);
           float a0, a1, a2, a3;
@@ -520,61 +581,66 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // ------------------------------------------------------------ expansion
-    using L = Kv4Layout<D>;
-    constexpr int kSubs = C::kKeys / 64;  // cache tiles of a block that a warp takes
-    const int dw = warp - 12;
-    const Places<D> places(lane);
+    // Key tile by key tile: while one is expanded for the next head, the products of this
+    // head's last query tile go on with the other.
+    constexpr int kT = C::kKeyTiles;
+    const int row = 32 * (warp & 3) + lane;  // key of a key tile
+    const uint32_t tK = tmem_addr(tmem, (uint32_t)(warp & 3) * 32, 0);
     uint32_t item = 0;
     bool ok = true;
-    Words<D> k[kSubs];
-    while (wk.next()) {
+    KeyWords<D> k[kT];
+#pragma unroll
+    for (int kt = 0; kt < kT; ++kt) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) k[kt].w[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) k[kt].s[i] = 0u;
+    }
+    while (ok && wk.next()) {
       const Kv4Request& rq = wk.job.rq;
       const int32_t* table = p.block_table + (size_t)wk.r * p.table_stride;
-      const int tiles_mask = (1 << (p.cache.page_shift - 4)) - 1;
-      // lanes u < kSubs: page ids of this warp's cache tiles of a block
-      auto lane_page = [&](int blk) -> int {
-        const int t = blk * C::kKeys + 16 * (kSubs * dw + lane);
-        return lane < kSubs && t < rq.L ? table[t >> p.cache.page_shift] : -1;
+      // page of this thread's key of a block's key tile, and that key's words of one head; where there is
+      // none (no page of the cache, behind the last key) whatever was there: its sum is not used
+      auto page_of = [&](int kt, int blk) -> int {
+        const int t = blk * C::kKeys + 128 * kt + row;
+        return t < rq.L ? table[t >> p.cache.page_shift] : -1;
       };
-      auto fetch = [&](int blk, int head, int page) {
-#pragma unroll
-        for (int u = 0; u < kSubs; ++u) {
-          const int t = blk * C::kKeys + 16 * (kSubs * dw + u);
-          const int pg = __shfl_sync(0xffffffffu, page, u);
-          if ((uint32_t)pg < (uint64_t)p.cache.num_pages) {  // (else, and behind the last key: whatever was there; its sums are not used)
-            const size_t tile = ((size_t)head << (p.cache.page_shift - 4)) + ((t >> 4) & tiles_mask);
-            load_words<D>(k[u], p.cache.pages + (int64_t)pg * p.page_bytes + tile * L::kBytes, lane);
-          } else {
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) k[u].w[i] = make_uint4(0u, 0u, 0u, 0u);
-            k[u].s = k[u].s1 = 0;
-          }
-        }
+      auto fetch = [&](KeyWords<D>& w, int kt, int blk, int head, int page) {
+        const int t = (blk * C::kKeys + 128 * kt + row) & (P - 1);
+        if ((uint32_t)page < (uint64_t)p.cache.num_pages)
+          load_key<D>(w, p.cache.pages + kv4_tile_offset<D>(p.cache, page, head, t), t & 15);
       };
       int blk = (int)kv4_div(wk.x0, Hkv), head = (int)(wk.x0 - (long long)blk * Hkv);
-      int page = lane_page(blk), page_next = lane_page(blk + 1);
-      fetch(blk, head, page);
-      for (long long x = wk.x0; x < wk.x1; ++x, ++item) {
-        const uint32_t ks = item & 1;
-        if (ok) ok = mbar_wait(b_kempty + 8 * ks, ((item >> 1) & 1) ^ 1, ab, 167);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      int page[kT], page_next[kT];
 #pragma unroll
-        for (int u = 0; u < kSubs; ++u) {
-          const int ct = kSubs * dw + u;
-          expand_keys<D>(sK + ks * C::kKBytes + (ct >> 3) * C::kKTile + 2048 * (ct & 7), k[u], places);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_kfull + 8 * ks);
+      for (int kt = 0; kt < kT; ++kt) {
+        page[kt] = page_of(kt, blk);
+        page_next[kt] = page_of(kt, blk + 1);
+        fetch(k[kt], kt, blk, head, page[kt]);
+      }
+      for (long long x = wk.x0; x < wk.x1 && ok; ++x, ++item) {
         if (++head == Hkv) {
           head = 0;
           ++blk;
-          page = page_next;
-          page_next = lane_page(blk + 1);
+#pragma unroll
+          for (int kt = 0; kt < kT; ++kt) {
+            page[kt] = page_next[kt];
+            page_next[kt] = page_of(kt, blk + 1);
+          }
         }
-        if (x + 1 < wk.x1) fetch(blk, head, page);
+#pragma unroll
+        for (int kt = 0; kt < kT; ++kt) {
+          if (ok) ok = mbar_wait(b_kempty + 8 * kt, (item & 1) ^ 1, ab, 167);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+          expand_key<D>(tK + kt * C::kKCols, k[kt]);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_kfull + 8 * kt);
+          if (x + 1 < wk.x1) fetch(k[kt], kt, blk, head, page[kt]);
+        }
       }
-      if (!ok) break;
     }
   }
   __syncwarp();
