@@ -371,7 +371,8 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
   p.tickets = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) + l.tickets);
   p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + l.partials);
   const int32_t G = num_q_heads / Hkv;
-  const bool tiles = num_q_tokens > 0 && (int64_t)G * max_q_len >= kWeightsTileRows;
+  // (the tile kernel takes lse / scale in fp32)
+  const bool tiles = num_q_tokens > 0 && (int64_t)G * max_q_len >= kWeightsTileRows && p.scale >= 0x1p-60f && p.scale <= 0x1p60f;
   if (!tiles || num_requests > 1) {  // (a single long request is the tile kernel's, whatever its real length)
     p.split_rows = tiles ? kWeightsTileRows : 0;
     e = ra::launch_kv4_weights(D, sms, w, st);

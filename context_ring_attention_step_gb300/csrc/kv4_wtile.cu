@@ -11,12 +11,17 @@
 // would be read at 128 bytes a clock, all there is.  Both are bf16: codes times scales
 // have 6 significant bits.
 //
+// The rows' log-sum-exps come in by a product too: one more step of 16 along K adds 1 times
+// - lse / scale, in three bf16 pieces that add up to 24 bits.  Read from shared memory by the
+// threads, a value for every column, they would cost four passes a warp for four columns, as much of
+// the bandwidth as all else.
+//
 // Warp roles (512 threads):
-//   warp 0        UMMA issuer (owns tensor memory)
-//   warp 1        TMA loads of query tiles
-//   warps 2, 3    the tiles' log-sum-exps and key limits, tiles in turn
-//   warps 4-11    exponentials and sums: a thread is a key; at head_dim 256 warps
-//                 4-7 take the first half of a tile's rows and 8-11 the second
+//   warps 0, 1    UMMA issuers of the two key tiles (warp 0 owns tensor memory): a wait costs one
+//                 of them 100 to 200 clocks even where nothing is to be waited for
+//   warp 2        the query tiles' log-sum-exps and key limits
+//   warp 3        TMA loads of query tiles
+//   warps 4-11    exponentials and sums: a thread is a key, at head_dim 256 and half of a tile's rows
 //   warps 12-15   cache -> bf16 keys: a thread is a key here too
 // Tensor memory (512 columns): the keys (D / 2 columns for 128 of them), then a ring of S^T tiles.
 // Items (block of keys, head) lie on one line that the CTAs cut evenly; of a block
@@ -34,32 +39,38 @@
 namespace ra {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = 32 * (8 + kSumWarps);
 constexpr int kExpandCost = 1;  // expanding a unit's keys, in query tiles
-constexpr int kLseStages = 8;
+constexpr int kLseStages = 4;
 
 template <int D>
 struct WTile {
   static constexpr int kKeyTiles = D == 256 ? 1 : 2;  // 128 keys each
   static constexpr int kKeys = 128 * kKeyTiles;
   static constexpr int kN = D == 256 ? 64 : 128;      // query rows of a tile
-  static constexpr int kCols = kN * kKeyTiles / 2;    // columns of a thread
+  static constexpr int kShares = kSumWarps / 4 / kKeyTiles;  // threads that share a key
+  static constexpr int kCols = kN / kShares;                 // columns of a thread
   static constexpr int kKCols = D / 2;                // tensor memory columns of 128 keys
   static constexpr int kSRing = D == 256 ? 4 : 3;     // S^T tiles (128 keys x kN rows) in tensor memory
   static constexpr int kSOff = kKeyTiles * kKCols;
   static_assert(kSOff + kSRing * kN <= 512, "tensor memory");
   static constexpr int kQTile = kN * D * 2;
   static constexpr int kQStages = D == 64 ? 8 : 6;
-  static constexpr int kLseOff = kQStages * kQTile;
-  static constexpr int kLseStage = 8 * kN + 16;       // - lse (log2), limits, the smallest and the largest of them
-  static constexpr int kPartOff = kLseOff + kLseStages * kLseStage;
-  static constexpr int kBarOff = kPartOff + 512;      // (half sums of 128 keys: head_dim 256)
+  static constexpr int kOnesOff = kQStages * kQTile;  // the keys' side of the lse's step: 128 rows of 32 bytes
+  static constexpr int kLseOff = kOnesOff + 128 * 32;
+  static constexpr int kLseTile = 32 * kN;            // the rows' side
+  static constexpr int kLimOff = kLseOff + kLseStages * kLseTile;
+  static constexpr int kLimStage = 4 * kN + 16;       // limits, the smallest and the largest of them
+  static constexpr int kPartOff = kLimOff + kLseStages * kLimStage;
+  static constexpr int kBarOff = kPartOff + 4 * kKeys * (kShares - 1);  // (the other threads' sums)
   static constexpr int kSmem = kBarOff + 512 + 1024;  // barriers, alignment slack
   static constexpr uint32_t kIdesc = idesc_bf16_f32(128, kN, false, false);
+  static_assert(kLseOff == kOnesOff + 128 * 32 && kOnesOff % 1024 == 0, "descriptors");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void keys_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void keys_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSumWarps) : "memory"); }
 
 // One token's keys of one head: the codes in order (8 dims a word), and the scales' bytes.
 template <int D>
@@ -195,21 +206,22 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(smem);
-  auto lse_of = [&](int s) { return reinterpret_cast<float*>(smem + C::kLseOff + s * C::kLseStage); };
-  auto lim_of = [&](int s) { return reinterpret_cast<int*>(lse_of(s) + N); };  // [N], then the smallest and the largest
+  auto lim_of = [&](int s) { return reinterpret_cast<int*>(smem + C::kLimOff + s * C::kLimStage); };  // [N], then the smallest and the largest
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   const uint32_t b_kfull = smem_u32(bars);            // [2] a tile's keys expanded (4 warps)
   const uint32_t b_kempty = smem_u32(bars + 2);       // [2]
   const uint32_t b_qfull = smem_u32(bars + 4);        // [QS]
   const uint32_t b_qempty = smem_u32(bars + 12);      // [QS]
   const uint32_t b_lfull = smem_u32(bars + 20);       // [LS]
-  const uint32_t b_lempty = smem_u32(bars + 20 + LS); // [LS] (8 warps)
-  const uint32_t b_sfull = smem_u32(bars + 20 + 2 * LS);   // [kSRing] an S^T tile ready
-  const uint32_t b_sempty = smem_u32(bars + 24 + 2 * LS);  // [kSRing] (the warps that read it)
-  const uint32_t b_drain = smem_u32(bars + 28 + 2 * LS);
-  int* s_int = reinterpret_cast<int*>(bars + 29 + 2 * LS);  // abort, bad, last, where a wait was given up
+  const uint32_t b_lempty = smem_u32(bars + 20 + LS); // [LS] (the summing warps and the issuers)
+  // S^T tiles: the t-th tile of key tile kt lies in place (kKeyTiles t + kt) % kSRing.  Each key
+  // tile has barriers of its own for every place: neither may be two phases behind or ahead of a wait.
+  const uint32_t b_sfull = smem_u32(bars + 20 + 2 * LS);   // [2][4] ready
+  const uint32_t b_sempty = smem_u32(bars + 28 + 2 * LS);  // [2][4] read (by the warps that sum that key tile)
+  const uint32_t b_drain = smem_u32(bars + 36 + 2 * LS);   // [2]
+  int* s_int = reinterpret_cast<int*>(bars + 38 + 2 * LS);  // abort, bad, last, where a wait was given up
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_int + 4);
-  static_assert(QS <= 8 && (29 + 2 * LS) * 8 + 20 <= 512, "barriers");
+  static_assert(QS <= 8 && (38 + 2 * LS) * 8 + 20 <= 512, "barriers");
   __shared__ long long s_sum[kThreads / 32], s_found[2];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -220,19 +232,20 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       mbar_init(b_kfull + 8 * i, 4);
       mbar_init(b_kempty + 8 * i, 1);
     }
-    for (int i = 0; i < C::kSRing; ++i) {
+    for (int i = 0; i < 8; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
-      mbar_init(b_sempty + 8 * i, 8 / C::kKeyTiles);
+      mbar_init(b_sempty + 8 * i, kSumWarps / C::kKeyTiles);
     }
     for (int i = 0; i < QS; ++i) {
       mbar_init(b_qfull + 8 * i, 1);
-      mbar_init(b_qempty + 8 * i, 1);
+      mbar_init(b_qempty + 8 * i, C::kKeyTiles);
     }
     for (int i = 0; i < LS; ++i) {
       mbar_init(b_lfull + 8 * i, 1);
-      mbar_init(b_lempty + 8 * i, 8);
+      mbar_init(b_lempty + 8 * i, kSumWarps + C::kKeyTiles);
     }
     mbar_init(b_drain, 1);
+    mbar_init(b_drain + 8, 1);
     s_int[0] = s_int[1] = s_int[2] = s_int[3] = 0;
     fence_mbar_init();
   }
@@ -240,7 +253,16 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == 1 && lane == 0) tma_prefetch_desc(&tq);
+  if (warp == 3 && lane == 0) tma_prefetch_desc(&tq);
+  // 1, 1, 1, 0 ... in every row of the ones; zeros in the rows of the log-sum-exps, whose
+  // first three places are written tile by tile.  (Rows of 32 bytes, 16-byte halves swapped in
+  // rows 4 to 7 of every 8.)
+  for (int i = tid; i < (128 * 32 + LS * C::kLseTile) / 16; i += kThreads) {
+    const bool ones = i < 256 && ((i ^ (i >> 3)) & 1) == 0;
+    *reinterpret_cast<uint4*>(smem + C::kOnesOff + 16 * i) =
+        ones ? make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   int bad = 0;
   auto work = [&](int i) {
     const Job j = job_of<D>(wp, i);
@@ -275,41 +297,48 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
   // Register split: 512 threads x 128 at launch = 128 x 64 + 256 x 176 + 128 x 96.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
+    if (warp < C::kKeyTiles && lane == 0) {
+      // ---------------------------------------------------------- MMA issuers
+      const int kt = warp;
       const uint64_t d0 = sdesc_sw128(sQ, 0, 1024);
-      uint32_t qs = 0, qph = 0, sb = 0, sph = 0, item = 0;  // stages and their parities
+      const uint32_t tK = tmem + kt * C::kKCols;
+      const uint64_t d1 = sdesc_sw32(sQ + C::kOnesOff);
+      uint32_t g = 0, qs = 0, qph = 0, ls = 0, lph = 0, item = 0;
       bool ok = true;
       while (ok && wk.next()) {
         const int tiles = wk.job.tiles;
         for (long long x = wk.x0; x < wk.x1 && ok; ++x, ++item) {
-          for (int t = 0; t < tiles; ++t) {
+          if (!(ok = mbar_wait(b_kfull + 8 * kt, item & 1, ab, 160))) break;
+          for (int t = 0; t < tiles; ++t, ++g) {
             if (!(ok = mbar_wait(b_qfull + 8 * qs, qph, ab, 161))) break;
+            // the place's last tile: with two key tiles the other one's, one or two before this one
+            const uint32_t sb = (C::kKeyTiles * g + kt) % C::kSRing;
+            const uint32_t back = C::kKeyTiles == 1 ? C::kSRing : 2 - kt;
+            if (g >= back && !(ok = mbar_wait(b_sempty + 8 * (4 * (C::kKeyTiles - 1 - kt) + sb),
+                                              ((g - back) / C::kSRing) & 1, ab, 162)))
+              break;
+            if (!(ok = mbar_wait(b_lfull + 8 * ls, lph, ab, 168))) break;
+            tc_fence_after();
             const uint64_t dq = sdesc_at(opaque(d0), (uint32_t)(qs * C::kQTile), 0);
+            const uint32_t tS = tmem + C::kSOff + sb * N;
 #pragma unroll
-            for (int kt = 0; kt < C::kKeyTiles; ++kt) {
-              if (t == 0 && !(ok = mbar_wait(b_kfull + 8 * kt, item & 1, ab, 160))) break;
-              if (!(ok = mbar_wait(b_sempty + 8 * sb, sph ^ 1, ab, 162))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                umma_ts(tmem + C::kSOff + sb * N, tmem + kt * C::kKCols + kk * 8,
-                        sdesc_at(dq, (kk >> 2) * (N * 128) + (kk & 3) * 32, 16), C::kIdesc, kk > 0);
-              umma_commit(b_sfull + 8 * sb);
-              if (t + 1 == tiles) umma_commit(b_kempty + 8 * kt);
-              if (++sb == C::kSRing) { sb = 0; sph ^= 1; }
-            }
-            if (!ok) break;
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ts(tS, tK + kk * 8, sdesc_at(dq, (kk >> 2) * (N * 128) + (kk & 3) * 32, 16), C::kIdesc, kk > 0);
+            umma_ss(tS, d1, sdesc_at(d1, (uint32_t)(128 * 32 + ls * C::kLseTile), 0), C::kIdesc, 1);
+            umma_commit(b_sfull + 8 * (4 * kt + sb));
             umma_commit(b_qempty + 8 * qs);
+            umma_commit(b_lempty + 8 * ls);
             if (++qs == QS) { qs = 0; qph ^= 1; }
+            if (++ls == LS) { ls = 0; lph ^= 1; }
           }
+          if (ok) umma_commit(b_kempty + 8 * kt);
         }
       }
       if (!ok) {  // let issued MMAs finish before tensor memory is released
-        umma_commit(b_drain);
-        mbar_wait_drain(b_drain, 0);
+        umma_commit(b_drain + 8 * kt);
+        mbar_wait_drain(b_drain + 8 * kt, 0);
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 3 && lane == 0) {
       // ---------------------------------------------------------- query tiles
       const uint32_t bytes = (uint32_t)(tl.tokens * (tl.per_token > 1 ? N : G)) * D * 2;
       uint32_t g = 0;
@@ -336,10 +365,10 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       }
       if (!ok)  // copies under way land before the CTA's shared memory is given up
         for (uint32_t k = g > QS ? g - QS : 0; k < g; ++k) mbar_wait_drain(b_qfull + 8 * (k % QS), (k / QS) & 1);
-    } else if (warp >= 2) {
+    } else if (warp == 2) {
       // ---------------------------------------------------------- log-sum-exps and limits
-      // (values of the next tile are on their way while this one's wait for their place)
       constexpr int V = N / 32;
+      const float inv_scale = 1.f / p.scale;
       // where this lane's columns lie in a tile: token and head of the group (a tile of a part
       // of one token: head alone), past any of both for columns that are none
       int col_tok[V], col_head[V];
@@ -350,103 +379,110 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
         col_head[i] = tl.per_token > 1 ? c : c - col_tok[i] * G;
         if (tl.per_token == 1 && c >= tl.tokens * G) col_head[i] = 0x40000000;
       }
-      float v[V];
-      int lim[V];
-      uint32_t g = 0, held = 0;  // `held`: the tile in v and lim
-      bool ok = true, have = false;
-      auto put = [&]() {
-        const uint32_t ls = held % LS;
-        ok = mbar_wait(b_lempty + 8 * ls, ((held / LS) & 1) ^ 1, ab, 164);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
+      // the values of a tile; those of the next one are on their way while they wait for their place
+      struct Tile {
+        float v[V];
+        int lim[V];
+      } a, b;
+      long long x = 0;
+      int head = 0, t = 0, tok0 = 0, part = 0;
+      bool any = wk.next();
+      if (any) {
+        x = wk.x0;
+        head = (int)(wk.x0 % Hkv);
+      }
+      auto load = [&](Tile& o) -> bool {
+        if (!any) return false;
+        const Kv4Request& rq = wk.job.rq;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int gi = part * N + col_head[i], tok = tok0 + col_tok[i];
+          const bool valid = gi < G && tok < rq.n;
+          o.v[i] = valid ? __ldg(wp.lse + (size_t)(head * G + gi) * p.Tq + rq.b + tok) : neg_inf();
+          o.lim[i] = !valid ? 0 : p.causal ? max(0, min(rq.L, rq.L - rq.n + tok + 1)) : rq.L;
+        }
+        if (++part == tl.per_token) {
+          part = 0;
+          tok0 += tl.tokens;
+        }
+        if (++t == wk.job.tiles) {
+          t = part = tok0 = 0;
+          if (++head == Hkv) head = 0;
+          if (++x == wk.x1 && (any = wk.next())) {
+            x = wk.x0;
+            head = (int)(wk.x0 % Hkv);
+          }
+        }
+        return true;
+      };
+      uint32_t ls = 0, lph = 0;
+      auto put = [&](Tile& o) -> bool {
+        bool ok = mbar_wait(b_lempty + 8 * ls, lph ^ 1, ab, 164);
+        if (!(ok = __all_sync(0xffffffffu, ok))) return false;
         int least = 0x7fffffff, most = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           // rows that are none, or have no softmax (lse = -inf: they see no key), see no key here
-          const bool dead = v[i] == neg_inf();
-          if (dead) lim[i] = 0;
-          lse_of(ls)[lane + 32 * i] = dead ? neg_inf() : -v[i] * kLog2e;
-          lim_of(ls)[lane + 32 * i] = lim[i];
-          least = min(least, lim[i]);
-          most = max(most, lim[i]);
+          const bool dead = o.v[i] == neg_inf();
+          const int lim = dead ? 0 : o.lim[i];
+          const float f = dead ? neg_inf() : -o.v[i] * inv_scale;
+          float r1 = f - __bfloat162float(__float2bfloat16_rn(f));
+          if (!isfinite(f)) r1 = 0.f;
+          const float r2 = r1 - __bfloat162float(__float2bfloat16_rn(r1));
+          const int c = lane + 32 * i;
+          *reinterpret_cast<uint2*>(smem + C::kLseOff + ls * C::kLseTile + 32 * c + ((c & 4) << 2)) =
+              make_uint2(pack_bf16x2(f, r1), pack_bf16x2(r2, 0.f));
+          lim_of(ls)[c] = lim;
+          least = min(least, lim);
+          most = max(most, lim);
         }
         least = __reduce_min_sync(0xffffffffu, least);
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) *reinterpret_cast<int2*>(lim_of(ls) + N) = make_int2(least, most);
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_lfull + 8 * ls);
+        if (++ls == LS) { ls = 0; lph ^= 1; }
+        return true;
       };
-      while (ok && wk.next()) {
-        const Kv4Request& rq = wk.job.rq;
-        const int tiles = wk.job.tiles, n = rq.n, top = p.causal ? rq.L - n + 1 : rq.L;
-        const float* lse = wp.lse + rq.b;
-        int head = (int)(wk.x0 % Hkv);
-        for (long long x = wk.x0; x < wk.x1 && ok; ++x) {
-          int tok0 = 0, part = 0;  // the tile's first token, and which part of a token
-          for (int t = 0; t < tiles && ok; ++t, ++g) {
-            if ((g & 1) == (uint32_t)(warp - 2)) {
-              float nv[V];
-              int nl[V];
-#pragma unroll
-              for (int i = 0; i < V; ++i) {
-                const int gi = part * N + col_head[i], tok = tok0 + col_tok[i];
-                const bool valid = gi < G && tok < n;
-                nv[i] = valid ? __ldg(lse + (size_t)(head * G + gi) * p.Tq + tok) : neg_inf();
-                nl[i] = valid ? max(0, min(rq.L, p.causal ? top + tok : top)) : 0;
-              }
-              if (have) put();
-#pragma unroll
-              for (int i = 0; i < V; ++i) {
-                v[i] = nv[i];
-                lim[i] = nl[i];
-              }
-              held = g;
-              have = true;
-            }
-            if (++part == tl.per_token) {
-              part = 0;
-              tok0 += tl.tokens;
-            }
-          }
-          if (++head == Hkv) head = 0;
-        }
+      bool more = load(a);
+      while (more) {
+        more = load(b);
+        if (!put(a) || !more) break;
+        more = load(a);
+        if (!put(b)) break;
       }
-      if (have && ok) put();
     }
-  } else if (warp < 12) {
+  } else if (warp < 4 + kSumWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ------------------------------------------------------------ exponentials and sums
     constexpr int NC = C::kCols;
-    const int gp = (warp - 4) >> 2, row = tid - 128 * (1 + gp);
-    const int key_t = C::kKeyTiles == 2 ? 128 * gp + row : row;  // key of the block
-    const int col0 = C::kKeyTiles == 2 ? 0 : NC * gp;
+    const int gp = (warp - 4) >> 2, kt = gp % C::kKeyTiles, share = gp / C::kKeyTiles;
+    const int key_t = 128 * kt + 32 * (warp & 3) + lane;  // key of the block
+    const int col0 = NC * share;
     const uint32_t tS = tmem_addr(tmem, (uint32_t)(warp & 3) * 32, C::kSOff + col0);
     const float c1 = p.scale * kLog2e;
     const uint64_t c2 = f2_pack(c1, c1);
-    uint32_t g = 0, sb = C::kKeyTiles == 2 ? gp : 0, sph = 0;  // tiles so far; this thread's next S^T tile and its parity
+    uint32_t g = 0;  // tiles so far
     bool ok = true;
     float acc = 0.f;
     uint64_t sum_a, sum_b;
-    auto columns = [&](const uint32_t (&s)[32], const float4* nl) {
+    auto columns = [&](const uint32_t (&s)[32]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 m = nl[i];
+      for (int i = 0; i < 32; i += 4) {
         float e[4];
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2, f2_pack(m.x, m.y)), e[0], e[1]);
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), c2, f2_pack(m.z, m.w)), e[2], e[3]);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2), e[0], e[1]);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2), e[2], e[3]);
         sum_a = f2_add(sum_a, f2_pack(ex2_approx(e[0]), ex2_approx(e[1])));
         sum_b = f2_add(sum_b, f2_pack(ex2_approx(e[2]), ex2_approx(e[3])));
       }
     };
-    auto masked_columns = [&](const uint32_t (&s)[32], const float4* nl, const int4* lim, int key) {
+    auto masked_columns = [&](const uint32_t (&s)[32], const int4* lim, int key) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 m = nl[i];
-        const int4 l = lim[i];
-        const float e0 = ex2_approx(fmaf(__uint_as_float(s[4 * i]), c1, m.x));
-        const float e1 = ex2_approx(fmaf(__uint_as_float(s[4 * i + 1]), c1, m.y));
-        const float e2 = ex2_approx(fmaf(__uint_as_float(s[4 * i + 2]), c1, m.z));
-        const float e3 = ex2_approx(fmaf(__uint_as_float(s[4 * i + 3]), c1, m.w));
+      for (int i = 0; i < 32; i += 4) {
+        const int4 l = lim[i / 4];
+        const float e0 = ex2_approx(__uint_as_float(s[i]) * c1), e1 = ex2_approx(__uint_as_float(s[i + 1]) * c1);
+        const float e2 = ex2_approx(__uint_as_float(s[i + 2]) * c1), e3 = ex2_approx(__uint_as_float(s[i + 3]) * c1);
         sum_a = f2_add(sum_a, f2_pack(key < l.x ? e0 : 0.f, key < l.y ? e1 : 0.f));
         sum_b = f2_add(sum_b, f2_pack(key < l.z ? e2 : 0.f, key < l.w ? e3 : 0.f));
       }
@@ -460,60 +496,37 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
         for (int t = 0; t < job.tiles; ++t, ++g) {
           const uint32_t ls = g % LS;
           if (ok) ok = mbar_wait(b_lfull + 8 * ls, (g / LS) & 1, ab, 165);
-          if (ok) ok = mbar_wait(b_sfull + 8 * sb, sph, ab, 166);
+          const uint32_t sb = (C::kKeyTiles * g + kt) % C::kSRing;
+          if (ok) ok = mbar_wait(b_sfull + 8 * (4 * kt + sb), (g / C::kSRing) & 1, ab, 166);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          const float4* nl = reinterpret_cast<const float4*>(lse_of(ls) + col0);
           const int4* lim = reinterpret_cast<const int4*>(lim_of(ls) + col0);
           const int2 ends = *reinterpret_cast<const int2*>(lim_of(ls) + N);
           const bool whole = key_end <= ends.x, none = key_end - 128 >= ends.y;  // all rows see all keys; none does any
           auto release = [&]() {  // all columns are in registers: the S^T tile may be written again
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(b_sempty + 8 * sb);
+            if (lane == 0) mbar_arrive(b_sempty + 8 * (4 * kt + sb));
           };
           sum_a = sum_b = 0;
           if (none) {
             release();
-          } else if constexpr (NC == 32) {
-            uint32_t s[32];
-            tmem_ld32(tS + sb * N, s);
-            tmem_ld_wait();
-            reg_fence32(s);
-            release();
-            if (whole) columns(s, nl);
-            else masked_columns(s, nl, lim, key);
           } else {
-            // half of the columns are on their way while the other half is worked on
-            uint32_t s[2][32], u[2][32];
-            tmem_ld32(tS + sb * N, s[0]);
-            tmem_ld32(tS + sb * N + 32, s[1]);
+uint32_t s[NC / 32][32];
+#pragma unroll
+            for (int c = 0; c < NC / 32; ++c) tmem_ld32(tS + sb * N + 32 * c, s[c]);
             tmem_ld_wait();
-            reg_fence32(s[0]);
-            reg_fence32(s[1]);
-            tmem_ld32(tS + sb * N + 64, u[0]);
-            tmem_ld32(tS + sb * N + 96, u[1]);
-            if (whole) {
-              columns(s[0], nl);
-              columns(s[1], nl + 8);
-            } else {
-              masked_columns(s[0], nl, lim, key);
-              masked_columns(s[1], nl + 8, lim + 8, key);
-            }
-            tmem_ld_wait();
-            reg_fence32(u[0]);
-            reg_fence32(u[1]);
+#pragma unroll
+            for (int c = 0; c < NC / 32; ++c) reg_fence32(s[c]);
             release();
             if (whole) {
-              columns(u[0], nl + 16);
-              columns(u[1], nl + 24);
+#pragma unroll
+              for (int c = 0; c < NC / 32; ++c) columns(s[c]);
             } else {
-              masked_columns(u[0], nl + 16, lim + 16, key);
-              masked_columns(u[1], nl + 24, lim + 24, key);
+#pragma unroll
+              for (int c = 0; c < NC / 32; ++c) masked_columns(s[c], lim + 8 * c, key);
             }
           }
-          sb += C::kKeyTiles;
-          if (sb >= C::kSRing) { sb -= C::kSRing; sph ^= 1; }
           __syncwarp();
           if (lane == 0) mbar_arrive(b_lempty + 8 * ls);
           float a0, a1, a2, a3;
@@ -526,14 +539,15 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
         // ---- the block's sums (after a wait that was given up: not known)
         if (!ok) acc = quiet_nan();
         float total = acc;
-        if (C::kKeyTiles == 1) {
-          float* half = reinterpret_cast<float*>(smem + C::kPartOff);
-          keys_sync();  // (it was read)
-          if (gp == 1) half[row] = acc;
-          keys_sync();
-          if (gp == 0) total += half[row];
+        float* others = reinterpret_cast<float*>(smem + C::kPartOff);
+        keys_sync();  // (they were read)
+        if (share > 0) others[(share - 1) * C::kKeys + key_t] = acc;
+        keys_sync();
+        const bool owner = share == 0;
+        if (owner) {
+#pragma unroll
+          for (int i = 1; i < C::kShares; ++i) total += others[(i - 1) * C::kKeys + key_t];
         }
-        const bool owner = C::kKeyTiles == 2 || gp == 0;
         const long long first = (long long)blk * Hkv;  // the block's first item
         bool writes = true;
         if (x - head < wk.x0 || head + 1 < Hkv) {
