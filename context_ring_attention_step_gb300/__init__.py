@@ -19,10 +19,15 @@ from .ring_attn import (  # noqa: F401
 )
 from .kv_cache import (  # noqa: F401
     Kv4Cache,
+    Kv4Eviction,
     Kv4Tables,
     kv4_attention,
     kv4_attention_workspace,
+    kv4_evict,
+    kv4_evict_out,
+    kv4_evict_workspace,
     kv4_load,
+    kv4_move,
     kv4_status,
     kv4_store,
     kv4_tables,

@@ -22,7 +22,7 @@ constexpr int kKv4MaxLength = 1 << 30;     // cached tokens of a request (positi
 // Status of a kernel that gave up on a pipeline wait: this plus the wait's site.  Above the
 // codes of the public header, so that it wins where both occur: rows are missing then.
 constexpr int kKv4GaveUp = 2000;
-static_assert(kKv4GaveUp > RA_KV4_BAD_FREE_COUNT, "the largest status wins");
+static_assert(kKv4GaveUp > RA_KV4_TOO_MANY_MOVES, "the largest status wins");
 constexpr int kKv4MaxRequests = 4096;      // kv4_tables keeps per-request prefix sums in shared memory
 
 // One tile: K codes (8 D bytes), K scales (D), V codes (8 D), V scales (D).
@@ -173,6 +173,38 @@ cudaError_t launch_kv4_weights(int D, int sms, const Kv4WeightsParams& p, cudaSt
 // dims, `heads` heads and `tokens` tokens, as kv4_wtile_box says for groups of G heads.
 void kv4_wtile_box(int D, int G, int* heads, int* tokens);
 cudaError_t launch_kv4_wtile(int D, int ctas, const Kv4WeightsParams& p, const CUtensorMap& tq, cudaStream_t stream);
+
+// Eviction (kv4_evict.cu).
+struct Kv4EvictParams {
+  const float* weights;  // [num_pages, page size]
+  int64_t num_pages;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int32_t table_width, num_requests, page_shift;
+  const int32_t* kv_lens;
+  const int32_t* budgets;
+  int32_t slack, recent, sinks, max_moves;
+  int32_t* free_pages;  // null: pages are not given back
+  int32_t num_free;     // places of the free list
+  const int32_t* free_count;
+  int32_t* kv_lens_out;
+  int32_t* dropped;
+  int64_t* src;  // [num_requests, max_moves]
+  int64_t* dst;
+  int32_t* free_count_out;
+  int32_t* status;
+  // workspace: the requests' new lengths; zero between calls: what the CTAs found wrong, how many have ended
+  int32_t *after, *found, *ended;
+};
+struct Kv4MoveParams {
+  Kv4Cache cache;
+  const int64_t* src;
+  const int64_t* dst;
+  int64_t n;
+  float* weights;  // [num_pages, page size], or null
+};
+cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream);
+cudaError_t launch_kv4_move(int D, const Kv4MoveParams& p, cudaStream_t stream);
 
 cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_store(int D, const Kv4RowsParams& p, cudaStream_t stream);

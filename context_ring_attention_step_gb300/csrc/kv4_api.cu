@@ -391,6 +391,117 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
   return RA_OK;
 }
 
+ra_status ra_kv4_evict_workspace_bytes(int32_t num_requests, size_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "NULL output");
+  if (num_requests < 1 || num_requests > ra::kKv4MaxRequests)
+    return fail(RA_ERR_INVALID_ARG, "num_requests %d outside [1, %d]", num_requests, ra::kKv4MaxRequests);
+  *bytes = kHeader + align256((size_t)num_requests * sizeof(int32_t));
+  return RA_OK;
+}
+
+ra_status ra_kv4_evict(const float* weights, int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                       int32_t table_width, int64_t table_stride, const int32_t* kv_lens, int32_t num_requests,
+                       const int32_t* budgets, int32_t slack, int32_t recent, int32_t sinks, int32_t max_moves,
+                       int32_t* free_pages, int32_t num_free, const int32_t* free_count, int32_t* kv_lens_out,
+                       int32_t* dropped, int64_t* src_slots, int64_t* dst_slots, int32_t* free_count_out,
+                       int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  const ra_status rs = ra_kv4_evict_workspace_bytes(num_requests, &need);
+  if (rs != RA_OK) return rs;
+  if (page_shift(page_size) < 0) return fail(RA_ERR_UNSUPPORTED, "page_size %d: 16, 32, 64, 128 or 256", page_size);
+  if (num_pages < 1 || num_pages > (int64_t(1) << 30))
+    return fail(RA_ERR_INVALID_ARG, "num_pages %lld outside [1, 2^30]", (long long)num_pages);
+  if (table_width < 1 || table_stride < table_width)
+    return fail(RA_ERR_INVALID_ARG, "table_width %d, table_stride %lld: need 1 <= width <= stride", table_width,
+                (long long)table_stride);
+  if (slack < 0 || recent < 0 || sinks < 0 || (int64_t)recent > (int64_t)slack + 1 || slack > ra::kKv4MaxLength ||
+      sinks > ra::kKv4MaxLength)
+    return fail(RA_ERR_INVALID_ARG, "slack %d, recent %d, sinks %d: none negative or above 2^30, recent at most slack + 1",
+                slack, recent, sinks);
+  if (max_moves < 1 || max_moves > ra::kKv4MaxLength)
+    return fail(RA_ERR_INVALID_ARG, "max_moves %d outside [1, 2^30]", max_moves);
+  if (!weights || !block_table || !kv_lens || !budgets || !kv_lens_out || !dropped || !src_slots || !dst_slots || !status)
+    return fail(RA_ERR_INVALID_ARG, "NULL pointer");
+  if (free_pages && (!free_count || !free_count_out || num_free < 1 || num_free > (1 << 30)))
+    return fail(RA_ERR_INVALID_ARG, "a free list needs free_count, free_count_out and num_free in [1, 2^30]");
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes: need %zu, 256-byte aligned", workspace ? workspace_bytes : 0, need);
+  const void* words[] = {weights, block_table, kv_lens, budgets, free_pages, free_count, kv_lens_out, dropped, free_count_out, status};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return fail(RA_ERR_INVALID_ARG, "weights and int32 arrays must be 4-byte aligned");
+  if (!aligned(src_slots, 8) || !aligned(dst_slots, 8)) return fail(RA_ERR_INVALID_ARG, "src_slots, dst_slots must be 8-byte aligned");
+  // arrays that are written, then those that are only read
+  const size_t R4 = (size_t)num_requests * 4, list = (size_t)num_requests * max_moves * 8;
+  const struct { const void* at; size_t bytes; const char* name; } arrays[] = {
+      {kv_lens_out, R4, "kv_lens_out"}, {dropped, R4, "dropped"}, {src_slots, list, "src_slots"},
+      {dst_slots, list, "dst_slots"}, {free_count_out, 4, "free_count_out"}, {status, 4, "status"},
+      {free_pages, (size_t)num_free * 4, "free_pages"}, {workspace, need, "the workspace"},
+      {kv_lens, R4, "kv_lens"}, {budgets, R4, "budgets"}, {free_count, 4, "free_count"},
+      {weights, (size_t)num_pages * page_size * 4, "weights"},
+      {block_table, ((size_t)(num_requests - 1) * table_stride + table_width) * 4, "block_table"}};
+  for (int i = 0; i < 8; ++i)
+    for (int j = i + 1; j < 13; ++j) {
+      if (arrays[i].at == arrays[j].at && ((i == 0 && j == 8) || (i == 4 && j == 10))) continue;
+      if (overlap(arrays[i].at, arrays[i].bytes, arrays[j].at, arrays[j].bytes))
+        return fail(RA_ERR_INVALID_ARG, "%s lies over %s (only kv_lens_out may be kv_lens, and free_count_out free_count)",
+                    arrays[i].name, arrays[j].name);
+    }
+  ra::Kv4EvictParams p{};
+  p.weights = weights;
+  p.num_pages = num_pages;
+  p.block_table = block_table;
+  p.table_stride = table_stride;
+  p.table_width = table_width;
+  p.num_requests = num_requests;
+  p.page_shift = page_shift(page_size);
+  p.kv_lens = kv_lens;
+  p.budgets = budgets;
+  p.slack = slack;
+  p.recent = recent;
+  p.sinks = sinks;
+  p.max_moves = max_moves;
+  p.free_pages = free_pages;
+  p.num_free = num_free;
+  p.free_count = free_count;
+  p.kv_lens_out = kv_lens_out;
+  p.dropped = dropped;
+  p.src = src_slots;
+  p.dst = dst_slots;
+  p.free_count_out = free_count_out;
+  p.status = status;
+  p.found = reinterpret_cast<int32_t*>(workspace);
+  p.ended = p.found + 1;
+  p.after = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) + kHeader);
+  const cudaError_t e = ra::launch_kv4_evict(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache eviction launch");
+}
+
+ra_status ra_kv4_move(const ra_kv4_cache* cache, const int64_t* src_slots, const int64_t* dst_slots,
+                      int64_t num_moves, float* weights, void* stream) {
+  ra::Kv4MoveParams p{};
+  const ra_status rs = check_cache(cache, &p.cache);
+  if (rs != RA_OK) return rs;
+  if (num_moves < 0 || num_moves > (int64_t(1) << 31))
+    return fail(RA_ERR_INVALID_ARG, "num_moves %lld outside [0, 2^31]", (long long)num_moves);
+  if (num_moves == 0) return RA_OK;
+  if (!src_slots || !dst_slots) return fail(RA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(src_slots, 8) || !aligned(dst_slots, 8) || !aligned(weights, 4))
+    return fail(RA_ERR_INVALID_ARG, "slot lists must be 8-byte aligned, weights 4-byte aligned");
+  const size_t list = (size_t)num_moves * 8, slots4 = (size_t)cache->num_pages * cache->page_size * 4;
+  const size_t bytes = (size_t)cache->num_pages * page_bytes(cache->page_size, cache->num_kv_heads, cache->head_dim);
+  const struct { const void* at; size_t bytes; const char* name; } reads[] = {{src_slots, list, "src_slots"}, {dst_slots, list, "dst_slots"}};
+  for (const auto& x : reads)
+    if (overlap(cache->pages, bytes, x.at, x.bytes) || overlap(weights, slots4, x.at, x.bytes))
+      return fail(RA_ERR_INVALID_ARG, "%s lies over the cache or the weights", x.name);
+  if (overlap(cache->pages, bytes, weights, slots4)) return fail(RA_ERR_INVALID_ARG, "weights lie over the cache");
+  p.src = src_slots;
+  p.dst = dst_slots;
+  p.n = num_moves;
+  p.weights = weights;
+  const cudaError_t e = ra::launch_kv4_move(cache->head_dim, p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cache move launch");
+}
+
 ra_status ra_kv4_status(const void* status, void* stream_) {
   if (!status) return fail(RA_ERR_INVALID_ARG, "status is NULL");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream_);
@@ -405,6 +516,8 @@ ra_status ra_kv4_status(const void* status, void* stream_) {
     case RA_KV4_BAD_OFFSET: return fail(RA_ERR_INVALID_ARG, "query offsets fall or pass the number of query tokens");
     case RA_KV4_TOO_MANY_TOKENS: return fail(RA_ERR_INVALID_ARG, "more new tokens than slots");
     case RA_KV4_NO_PAGES: return fail(RA_ERR_WORKSPACE, "not enough free pages");
+    case RA_KV4_BAD_BUDGET: return fail(RA_ERR_INVALID_ARG, "a budget is below the number of protected tokens");
+    case RA_KV4_TOO_MANY_MOVES: return fail(RA_ERR_WORKSPACE, "more rows to move than max_moves");
     case RA_KV4_BAD_FREE_COUNT: return fail(RA_ERR_INVALID_ARG, "the free count is negative or passes the number of pages");
   }
   return fail(RA_ERR_TIMEOUT, "a kernel gave up on a pipeline wait (site %d)", word - ra::kKv4GaveUp);

@@ -1,0 +1,379 @@
+// kv4_evict.cu -- eviction from the 4-bit cache by accumulated attention weight:
+//   * evict: which tokens of every request over its budget go, which kept rows move
+//     into their places, and the pages given back;
+//   * move: rows copied from slots to slots, bit by bit.
+//
+// A request of L tokens with budget B keeps its first `sinks`, its last `recent`, and
+// of the others those with the largest sums.  A key orders them: the sum's bits (sums
+// are no negative numbers, so their bits order like they do), above all of them for the
+// protected ones; the B-th largest key is found digit by digit from histograms (11, 11 and 10 bits),
+// and of equal keys the lowest indices are taken.  Then kept tokens behind place B (the
+// m-th of them) move into the places of dropped ones before it (the m-th): sources and places
+// are disjoint, so the rows can move in any order, and no more of them than are dropped.
+//
+// What has to be read are 4 bytes a token; what takes time are the steps that wait for one another.  A
+// request is one cluster of CTAs: its tokens' keys lie in their shared memory, and counts
+// go between them by way of it.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
+#include "kv4.cuh"
+#include "kv4.h"
+#include "kv4_walk.cuh"
+
+namespace ra {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxKeys = 40960;  // keys of a CTA in shared memory; the others are made again where they are needed
+constexpr uint32_t kProtected = 0xffffffffu;
+
+// Block-wide exclusive prefix sum in thread order; `total` receives the sum.
+__device__ __forceinline__ int block_prefix(int x, int* s_sum, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, d);
+    if (lane >= d) y += z;
+  }
+  __syncthreads();  // (s_sum of the call before was read)
+  if (lane == 31) s_sum[warp] = y;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  return before + y - x;
+}
+
+// What a CTA of a cluster tells the others.
+struct Told {
+  int bad, equal, holes, movers;
+};
+
+__global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictParams p, int keys_held) {
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  __shared__ __align__(16) uint32_t s_hist[3][kBins];
+  __shared__ int s_sum[kWarps], s_digit[3];  // digit, keys still to take at it, keys with it
+  __shared__ Told s_told;
+  __shared__ int s_last;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int r = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = 1 << p.page_shift;
+  const int64_t pages = p.num_pages;
+
+  const int L = p.kv_lens[r], B = p.budgets[r];
+  int code = 0;
+  const bool sane = L >= 0 && (long long)L <= min((long long)p.table_width << p.page_shift, (long long)kKv4MaxLength);
+  if (!sane) code = RA_KV4_BAD_LENGTH;
+  bool cut = sane && B >= 0 && (long long)L > (long long)B + p.slack;
+  if (cut && B < p.sinks + p.recent) {
+    code = RA_KV4_BAD_BUDGET;
+    cut = false;
+  }
+  const int32_t* table = p.block_table + (size_t)r * p.table_stride;
+  int moves = 0;
+  int64_t* src = p.src + (size_t)r * p.max_moves;
+  int64_t* dst = p.dst + (size_t)r * p.max_moves;
+  if (cut) {
+    // this CTA's tokens [t0, t1), and each warp's share of them, in whole 32s
+    const int per_cta = (L + C - 1) / C, per_warp = ((per_cta + kWarps - 1) / kWarps + 31) & ~31;
+    const int t0 = min(rank * per_warp * kWarps, L), t1 = min(t0 + per_warp * kWarps, L);
+    const int w0 = min(t0 + warp * per_warp, t1), w1 = min(w0 + per_warp, t1);
+    int bad = 0;
+    auto slot_of = [&](int t) -> int64_t {
+      const int page = table[t >> p.page_shift];
+      return (uint32_t)page < (uint64_t)pages ? ((int64_t)page << p.page_shift) + (t & (P - 1)) : -1;
+    };
+    auto make_key = [&](int t) -> uint32_t {
+      const int64_t slot = slot_of(t);
+      if (slot < 0) {
+        bad = 1;
+        return 0u;
+      }
+      if (t < p.sinks || t >= L - p.recent) return kProtected;
+      const float w = __ldg(p.weights + slot);
+      return w > 0.f ? __float_as_uint(w) : 0u;
+    };
+    auto key_of = [&](int t) -> uint32_t { return t - t0 < keys_held ? s_keys[t - t0] : make_key(t); };
+    for (int i = tid; i < 3 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0u;
+    if (tid == 0) s_told = Told{0, 0, 0, 0};
+    __syncthreads();
+    // add one to a bin for every lane that asks; neighbours often ask for the same one
+    auto count = [&](uint32_t* hist, bool in, uint32_t bin) {
+      const uint32_t who = __ballot_sync(0xffffffffu, in);
+      if (who == 0) return;
+      const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(who) - 1);
+      if (__all_sync(0xffffffffu, !in || bin == first)) {
+        if (lane == 0) atomicAdd(hist + first, (uint32_t)__popc(who));
+      } else if (in) {
+        atomicAdd(hist + bin, 1u);
+      }
+    };
+#pragma unroll 4
+    for (int t = w0 + lane; t - lane < w1; t += 32) {
+      const bool in = t < w1;
+      const uint32_t k = in ? make_key(t) : 0u;
+      if (in && t - t0 < keys_held) s_keys[t - t0] = k;
+      count(s_hist[0], in, k >> 21);
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_told.bad, 1);
+
+    // ---- the B-th largest key, and how many of its equals are taken
+    uint32_t key = 0u;
+    int take = B, equal = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      if (pass > 0) {
+        const uint32_t top = shift + (pass == 1 ? 11 : 10);
+        for (int t = w0 + lane; t - lane < w1; t += 32) {
+          const bool in = t < w1;
+          const uint32_t k = in ? key_of(t) : 0u;
+          count(s_hist[pass], in && (k >> top) == (key >> top), (k >> shift) & (pass == 1 ? 2047u : 1023u));
+        }
+      }
+      cluster.sync();
+      // bins from the top: thread i has bins kBins - 4 - 4 i and the three behind it
+      const int b0 = kBins - 4 - 4 * tid;
+      int n[4] = {0, 0, 0, 0};
+      for (int c = 0; c < C; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s_hist[pass][b0], c));
+        n[0] += x.x; n[1] += x.y; n[2] += x.z; n[3] += x.w;
+      }
+      int total;
+      int above = block_prefix(n[0] + n[1] + n[2] + n[3], s_sum, total);
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        if (above < take && above + n[i] >= take) {
+          s_digit[0] = b0 + i;
+          s_digit[1] = take - above;
+          s_digit[2] = n[i];
+        }
+        above += n[i];
+      }
+      __syncthreads();
+      if (take > 0) {
+        key |= (uint32_t)s_digit[0] << shift;
+        take = s_digit[1];
+        equal = s_digit[2];
+      } else {
+        key = kProtected;  // none is kept
+        equal = 0;
+      }
+    }
+    for (int c = 0; c < C; ++c) bad |= cluster.map_shared_rank(&s_told, c)->bad;
+
+    // ---- of equal keys the lowest indices: this warp's first one's rank among them
+    int before_equal = 0;
+    if (equal != take) {
+      int mine = 0;
+      for (int t = w0 + lane; t < w1; t += 32) mine += key_of(t) == key;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+      int total;
+      before_equal = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? mine : 0, s_sum, total), 0);
+      if (tid == 0) s_told.equal = total;
+      cluster.sync();
+      for (int c = 0; c < rank; ++c) before_equal += cluster.map_shared_rank(&s_told, c)->equal;
+    }
+    // every token of this warp's share in turn: is it kept?  f(t, in, kept)
+    auto walk = [&](auto f) {
+      int seen = before_equal;
+      for (int t = w0 + lane; t - lane < w1; t += 32) {
+        const bool in = t < w1;
+        const uint32_t k = in ? key_of(t) : 0u;
+        bool kept = in && k > key;
+        const uint32_t same = __ballot_sync(0xffffffffu, in && k == key);
+        if (in && k == key) kept = equal == take || seen + __popc(same & ((1u << lane) - 1u)) < take;
+        seen += __popc(same);
+        f(t, in, kept);
+      }
+    };
+    int holes = 0, movers = 0;  // of this warp
+    walk([&](int t, bool in, bool kept) {
+      holes += __popc(__ballot_sync(0xffffffffu, in && !kept && t < B));
+      movers += __popc(__ballot_sync(0xffffffffu, kept && t >= B));
+    });
+    int cta_holes, cta_movers;
+    int h0 = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? holes : 0, s_sum, cta_holes), 0);
+    int m0 = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? movers : 0, s_sum, cta_movers), 0);
+    if (tid == 0) {
+      s_told.holes = cta_holes;
+      s_told.movers = cta_movers;
+    }
+    cluster.sync();
+    for (int c = 0; c < C; ++c) {
+      const Told* o = cluster.map_shared_rank(&s_told, c);
+      if (c < rank) {
+        h0 += o->holes;
+        m0 += o->movers;
+      }
+      moves += o->movers;
+    }
+    if (bad) code = RA_KV4_BAD_PAGE;
+    else if (moves > p.max_moves) code = RA_KV4_TOO_MANY_MOVES;
+    if (code) {
+      cut = false;
+      moves = 0;
+    } else {
+      walk([&](int t, bool in, bool kept) {
+        const uint32_t h = __ballot_sync(0xffffffffu, in && !kept && t < B), m = __ballot_sync(0xffffffffu, kept && t >= B);
+        const uint32_t below = (1u << lane) - 1u;
+        if ((h >> lane) & 1u) dst[h0 + __popc(h & below)] = slot_of(t);
+        if ((m >> lane) & 1u) src[m0 + __popc(m & below)] = slot_of(t);
+        h0 += __popc(h);
+        m0 += __popc(m);
+      });
+    }
+    cluster.sync();  // no CTA ends while another reads its shared memory
+  }
+  for (int i = moves + rank * kThreads + tid; i < p.max_moves; i += C * kThreads) src[i] = dst[i] = -1;
+
+  // ---- the call's last CTA: lengths, pages given back, status
+  __syncthreads();
+  if (tid == 0) {
+    if (rank == 0) {
+      p.after[r] = cut ? B : L;
+      if (code) atomicMax(p.found, code);
+    }
+    __threadfence();
+    s_last = atomicAdd(p.ended, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  const int R = p.num_requests;
+  const int count0 = p.free_count ? *p.free_count : 0;
+  // (the prefix sums of all requests' pages lie where the histograms were, or in the workspace)
+  int* s_back = reinterpret_cast<int*>(&s_hist[0][0]);  // [R + 1], R <= 4096
+  const int per = (R + kThreads - 1) / kThreads, r0 = min(tid * per, R), r1 = min(r0 + per, R);
+  auto held = [&](int n) { return n > 0 ? (int)(((long long)n + P - 1) >> p.page_shift) : 0; };
+  long long back = 0;
+  for (int i = r0; i < r1; ++i) {
+    const int l = p.kv_lens[i], a = __ldcg(p.after + i);
+    if (a < l) back += held(l) - held(a);
+  }
+  // the sum of all in 64 bits: tables that are not sound may hold more pages than there are
+  long long sum = back;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  __shared__ long long s_pages[kWarps];
+  if (lane == 0) s_pages[warp] = sum;
+  __syncthreads();
+  sum = 0;
+  for (int w = 0; w < kWarps; ++w) sum += s_pages[w];
+  const bool push = p.free_pages != nullptr;
+  const bool fits = !push || (count0 >= 0 && count0 + sum <= p.num_free);
+  if (!push || !fits) back = sum = 0;
+  int total;
+  int at = block_prefix((int)back, s_sum, total);
+  for (int i = r0; i < r1; ++i) {
+    const int l = p.kv_lens[i], a = fits ? __ldcg(p.after + i) : l;
+    s_back[i] = at;
+    if (push && a < l) at += held(l) - held(a);
+  }
+  if (tid == 0) s_back[R] = total;
+  __syncthreads();
+  for (int i = tid; i < total; i += kThreads) {
+    int lo = 0, hi = R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_back[mid] <= i) lo = mid; else hi = mid;
+    }
+    p.free_pages[count0 + i] = p.block_table[(size_t)lo * p.table_stride + held(__ldcg(p.after + lo)) + (i - s_back[lo])];
+  }
+  if (!fits)  // nothing is dropped
+    for (long long i = tid; i < (long long)R * p.max_moves; i += kThreads) p.src[i] = p.dst[i] = -1;
+  __syncthreads();
+  for (int i = r0; i < r1; ++i) {
+    const int l = p.kv_lens[i], a = fits ? __ldcg(p.after + i) : l;
+    p.dropped[i] = a < l ? l - a : 0;
+    p.kv_lens_out[i] = a;  // (may be kv_lens)
+  }
+  if (tid == 0) {
+    if (p.free_count_out) *p.free_count_out = count0 + total;
+    const int found = atomicExch(p.found, 0);
+    *p.status = !fits ? (int)RA_KV4_BAD_FREE_COUNT : found;
+    *p.ended = 0;
+  }
+}
+
+// A thread copies 16 dims of one row and head: K and V codes and scales.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_move_kernel(const Kv4MoveParams p) {
+  using L = Kv4Layout<D>;
+  const int64_t end = p.cache.num_pages << p.cache.page_shift;
+  const int64_t pmask = (int64_t(1) << p.cache.page_shift) - 1;
+  const int columns = p.cache.Hkv * L::kGroups;
+  const int64_t n = p.n * columns;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    const int64_t m = kv4_div(i, columns);
+    const int c = (int)(i - m * columns), head = c / L::kGroups, g = c % L::kGroups;
+    const int64_t from = __ldg(p.src + m), to = __ldg(p.dst + m);
+    if (from < 0 || to < 0 || from >= end || to >= end) continue;
+    const uint8_t* a = p.cache.pages + kv4_tile_offset<D>(p.cache, from >> p.cache.page_shift, head, (int)(from & pmask));
+    uint8_t* b = p.cache.pages + kv4_tile_offset<D>(p.cache, to >> p.cache.page_shift, head, (int)(to & pmask));
+    const int s = (int)(from & 15), t = (int)(to & 15);
+    const uint2 k = *reinterpret_cast<const uint2*>(a + L::k_code(s, g));
+    const uint32_t v0 = *reinterpret_cast<const uint32_t*>(a + L::v_code(s, g, 0));
+    const uint32_t v1 = *reinterpret_cast<const uint32_t*>(a + L::v_code(s, g, 1));
+    const uint8_t ks = a[L::k_scale(s, g)], vs = a[L::v_scale(s, g)];
+    *reinterpret_cast<uint2*>(b + L::k_code(t, g)) = k;
+    *reinterpret_cast<uint32_t*>(b + L::v_code(t, g, 0)) = v0;
+    *reinterpret_cast<uint32_t*>(b + L::v_code(t, g, 1)) = v1;
+    b[L::k_scale(t, g)] = ks;
+    b[L::v_scale(t, g)] = vs;
+    if (p.weights && c == 0) p.weights[to] = p.weights[from];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream) {
+  // CTAs of a request: enough that each has about 8192 tokens at most, where the
+  // requests alone do not fill the GPU
+  const int64_t most = std::min((int64_t)p.table_width << p.page_shift, (int64_t)kKv4MaxLength);
+  int ctas = 1;
+  while (ctas < 8 && most > 8192ll * ctas && (int64_t)p.num_requests * ctas < 152) ctas *= 2;
+  const int64_t share = ((most + ctas - 1) / ctas + kWarps - 1) / kWarps;
+  const int keys = (int)std::min<int64_t>((share + 31) / 32 * 32 * kWarps, kMaxKeys);
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(p.num_requests * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)keys * 4;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static Kv4SmemLimit limit;
+  return limit.launch(reinterpret_cast<const void*>(kv4_evict_kernel), kMaxKeys * 4,
+                      [&] { return cudaLaunchKernelEx(&cfg, kv4_evict_kernel, p, keys); });
+}
+
+cudaError_t launch_kv4_move(int D, const Kv4MoveParams& p, cudaStream_t stream) {
+  if (p.n == 0) return cudaSuccess;
+  const int64_t threads = p.n * p.cache.Hkv * (D / 16);
+  const unsigned blocks = (unsigned)std::min<int64_t>((threads + 255) / 256, 1 << 20);
+  if (D == 64) kv4_move_kernel<64><<<blocks, 256, 0, stream>>>(p);
+  else if (D == 128) kv4_move_kernel<128><<<blocks, 256, 0, stream>>>(p);
+  else if (D == 256) kv4_move_kernel<256><<<blocks, 256, 0, stream>>>(p);
+  else return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+}  // namespace ra

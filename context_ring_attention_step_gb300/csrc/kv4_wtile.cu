@@ -294,9 +294,9 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
   if (bad) atomicMax(s_int + 1, bad);
   Walk<D> wk(wp, line, r0, base0);
 
-  // Register split: 512 threads x 128 at launch = 128 x 64 + 256 x 176 + 128 x 96.
+  // Register split: 512 threads x 128 at launch = 128 x 72 + 256 x 168 + 128 x 104.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < C::kKeyTiles && lane == 0) {
       // ---------------------------------------------------------- MMA issuers
       const int kt = warp;
@@ -454,7 +454,7 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       }
     }
   } else if (warp < 4 + kSumWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ------------------------------------------------------------ exponentials and sums
     constexpr int NC = C::kCols;
     const int gp = (warp - 4) >> 2, kt = gp % C::kKeyTiles, share = gp / C::kKeyTiles;
@@ -593,7 +593,7 @@ uint32_t s[NC / 32][32];
     }
     if (bad) atomicMax(s_int + 1, bad);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ------------------------------------------------------------ expansion
     // Key tile by key tile: while one is expanded for the next head, the products of this
     // head's last query tile go on with the other.

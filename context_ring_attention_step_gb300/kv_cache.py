@@ -327,9 +327,104 @@ def kv4_weights(q, cache, block_table, kv_lens, cu_q, lse, weights, new_lens=Non
     return weights
 
 
+Kv4Eviction = collections.namedtuple("Kv4Eviction", "kv_lens dropped src_slots dst_slots free_count status")
+
+
+def kv4_evict_out(num_requests, max_moves, device="cuda"):
+    """Caller-owned outputs for ``kv4_evict(out=...)``."""
+    i32, i64 = dict(dtype=torch.int32, device=device), dict(dtype=torch.int64, device=device)
+    return Kv4Eviction(torch.empty(num_requests, **i32), torch.empty(num_requests, **i32),
+                       torch.empty(num_requests, max_moves, **i64), torch.empty(num_requests, max_moves, **i64),
+                       torch.empty(1, **i32), torch.empty(1, **i32))
+
+
+def kv4_evict_workspace(num_requests, device="cuda"):
+    """Workspace (zeroed, as its first use needs it) for ``kv4_evict``.  Calls that may overlap need one each."""
+    n = ctypes.c_size_t()
+    _ra._check(_library().ra_kv4_evict_workspace_bytes(int(num_requests), ctypes.byref(n)))
+    return torch.zeros(n.value, dtype=torch.uint8, device=device)
+
+
+def kv4_evict(weights, block_table, kv_lens, budgets, page_size, max_moves, slack=0, recent=0, sinks=0, free_pages=None,
+              free_count=None, workspace=None, out=None, check=False):
+    """Which cached tokens go, by the sums of ``kv4_weights`` (ra_kv4_evict): returns a ``Kv4Eviction``.
+
+    Request r with more than ``budgets[r]`` (int32 [R], negative: no budget) +
+    ``slack`` tokens is cut to its budget: the first ``sinks``, the last ``recent``
+    (at most ``slack`` + 1) and otherwise the tokens with the largest ``weights`` stay.
+    ``src_slots`` and ``dst_slots`` [R, max_moves] name the rows that move into the
+    places of dropped ones (-1 behind the last): hand them to ``kv4_move``, for every layer
+    that shares the block table, before the next tokens are stored.
+    ``dropped`` [R]: tokens that went (a position counts them: index + all dropped
+    so far).  Pages behind the new lengths go to ``free_pages``.  ``out`` may name ``kv_lens``
+    and ``free_count`` themselves as outputs.  A request that cannot be cut is left alone,
+    and ``status`` says why; ``check=True`` synchronises and raises.
+    """
+    lib = _library()
+    dev, R = kv_lens.device, kv_lens.shape[0]
+    _on_gpu("kv_lens", dev)
+    page_size, max_moves = int(page_size), int(max_moves)
+    if out is None:
+        out = kv4_evict_out(R, max_moves, dev)
+    slots = weights.shape[0]
+    w = _array("weights", weights, (slots,), _F32, dev)
+    if page_size < 1 or slots % page_size:
+        raise ValueError("weights has %d entries, not a multiple of page_size %d" % (slots, page_size))
+    per_r, one, lists = (R,), (1,), (R, max_moves)
+    table, width, stride = _table(block_table, R, dev)
+    free = count = None
+    num_free = 0
+    if free_pages is not None:
+        if free_count is None:
+            raise ValueError("free_pages needs free_count")
+        num_free = free_pages.shape[0]
+        free = _array("free_pages", free_pages, (num_free,), _I32, dev)
+    if free_count is not None:
+        count = _array("free_count", free_count, one, _I32, dev)
+    if workspace is None:
+        workspace = kv4_evict_workspace(R, dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    o_lens, o_dropped, o_src, o_dst, o_count, o_status = out
+    _launch(dev, lib.ra_kv4_evict, w, slots // page_size, page_size, table, width, stride,
+            _array("kv_lens", kv_lens, per_r, _I32, dev), R, _array("budgets", budgets, per_r, _I32, dev), int(slack),
+            int(recent), int(sinks), max_moves, free, num_free, count, _array("out.kv_lens", o_lens, per_r, _I32, dev),
+            _array("out.dropped", o_dropped, per_r, _I32, dev), _array("out.src_slots", o_src, lists, _I64, dev),
+            _array("out.dst_slots", o_dst, lists, _I64, dev), _array("out.free_count", o_count, one, _I32, dev),
+            _array("out.status", o_status, one, _I32, dev), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    if check:
+        kv4_status(out.status)
+    return out
+
+
+def kv4_move(cache, src_slots, dst_slots, weights=None, check=False):
+    """Copy cached rows, as they are, from ``src_slots`` to ``dst_slots`` (int64, of one shape).
+
+    Pairs with a slot that is negative or outside the cache are left out.
+    ``weights`` [num_pages * page_size] (fp32): the slots' sums go along.  A slot that is
+    written must occur only once among all of them; ``check=True`` synchronises and
+    raises if one occurs twice.
+    """
+    lib = _library()
+    dev, n = cache.device, src_slots.numel()
+    _on_gpu("cache", dev)
+    src = _array("src_slots", src_slots, src_slots.shape, _I64, dev)
+    dst = _array("dst_slots", dst_slots, src_slots.shape, _I64, dev)
+    end = cache.num_pages * cache.page_size
+    w = None if weights is None else _array("weights", weights, (end,), _F32, dev)
+    if check:
+        inside = lambda x: (x >= 0) & (x < end)  # noqa: E731
+        pairs = inside(src_slots) & inside(dst_slots)
+        written = dst_slots[pairs]
+        if torch.unique(written).numel() != written.numel() or bool(torch.isin(written, src_slots[pairs]).any()):
+            raise ValueError("a slot of dst_slots occurs twice, or in src_slots")
+    _launch(dev, lib.ra_kv4_move, cache._ref, src, dst, n, w)
+
+
 def kv4_status(status):
     """Synchronise and raise if the status word at the start of ``status`` (``Kv4Tables.status``,
-    or the workspace of ``kv4_attention``) reports a refusal."""
+    ``Kv4Eviction.status``, or the workspace of ``kv4_attention`` or ``kv4_weights``) reports a refusal."""
     lib = _library()
     _on_gpu("status", status.device)
     _launch(status.device, lib.ra_kv4_status, status.data_ptr())

@@ -108,6 +108,10 @@ def load_library(path: str | None = None):
     lib.ra_kv4_attention.argtypes = [P, P, i64, i32, i32, P, i32, i64, P, P, i32, i32, i32, c.c_float, P, i32, P, P,
                                      sz, P]
     lib.ra_kv4_status.argtypes = [P, P]
+    lib.ra_kv4_evict_workspace_bytes.argtypes = [i32, c.POINTER(sz)]
+    lib.ra_kv4_evict.argtypes = [P, i64, i32, P, i32, i64, P, i32, P, i32, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P,
+                                 sz, P]
+    lib.ra_kv4_move.argtypes = [P, P, P, i64, P, P]
     lib.ra_kv4_weights.argtypes = [P, P, i64, i32, i32, P, i32, i64, P, P, i32, i32, i32, c.c_float, P, P, P, P, sz, P]
     lib.ra_rope_turns.argtypes = [i32, c.c_double, c.POINTER(c.c_double), c.POINTER(c.c_uint64)]
     lib.ra_qk_norm_rope_fwd.argtypes = [P, P, i64, P, i64, P, i64, P, i64, P]
@@ -116,7 +120,8 @@ def load_library(path: str | None = None):
     for name in ("ra_rope_turns", "ra_qk_norm_rope_fwd", "ra_qk_norm_rope_workspace_bytes", "ra_qk_norm_rope_bwd"):
         getattr(lib, name).restype = i32
     for name in ("ra_kv4_cache_bytes", "ra_kv4_tables", "ra_kv4_store", "ra_kv4_load",
-                 "ra_kv4_attention_workspace_bytes", "ra_kv4_attention", "ra_kv4_status", "ra_kv4_weights"):
+                 "ra_kv4_attention_workspace_bytes", "ra_kv4_attention", "ra_kv4_status", "ra_kv4_weights",
+                 "ra_kv4_evict_workspace_bytes", "ra_kv4_evict", "ra_kv4_move"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib

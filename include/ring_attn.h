@@ -515,7 +515,9 @@ typedef enum {
   RA_KV4_BAD_OFFSET = 1003,      /* query offsets fall or pass the number of query tokens */
   RA_KV4_TOO_MANY_TOKENS = 1004, /* more new tokens than slots */
   RA_KV4_NO_PAGES = 1005,        /* not enough free pages */
-  RA_KV4_BAD_FREE_COUNT = 1006   /* free count negative or, with the released pages, above num_pages */
+  RA_KV4_BAD_FREE_COUNT = 1006,  /* free count negative or, with the released pages, above num_pages */
+  RA_KV4_BAD_BUDGET = 1007,      /* a budget does not hold the protected tokens */
+  RA_KV4_TOO_MANY_MOVES = 1008   /* more rows to move than max_moves */
 } ra_kv4_code;
 
 /* Bytes of a cache's pages. */
@@ -639,6 +641,54 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
                          const int32_t* kv_lens, const int32_t* cu_q, int32_t num_requests, int32_t max_q_len,
                          int32_t causal, float softmax_scale, const float* lse, const int32_t* new_lens,
                          float* weights, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Which cached tokens go, by the sums of ra_kv4_weights.  Request r with more than
+ * budgets[r] + slack tokens is cut to budgets[r]: it keeps its first `sinks` and
+ * its last `recent` tokens, and of the others those with the largest sums (of equal ones
+ * the lower indices; what is no positive number counts as 0).  The others, and requests with
+ * a negative budget, are left alone.  recent <= slack + 1: the protected last tokens
+ * then all lie behind the budget, and tokens that were protected before do not have to be known.
+ *   Kept tokens with an index of at least the budget move, in order, into the places of
+ * the dropped ones before it: token src_slots[r][m] into dst_slots[r][m].  No slot is in
+ * both lists.  The kept tokens' order changes by that; new tokens follow behind them
+ * (attention does not depend on the order of the tokens before the query's own).
+ *   weights fp32 [num_pages * page_size]; block_table, kv_lens as in ra_kv4_tables;
+ *     1 <= R <= 4096.
+ *   budgets int32 [R]; slack, recent, sinks >= 0.
+ *   kv_lens_out [R] (may be kv_lens): lengths afterwards.  dropped [R]: tokens that went.
+ *   src_slots, dst_slots int64 [R, max_moves]: the moves (ra_kv4_move makes them), -1
+ *     behind the last one.  A cut of n tokens makes at most min(n, budget) of them.
+ *   free_pages [num_free], free_count [1]: pages behind the new lengths are pushed
+ *     (in request order, then page order); free_count_out [1] (may be
+ *     free_count).  free_pages NULL: no page is given back (the count, 0 without free_count, is handed on).
+ *     The block table's entries stay as they are.
+ *   status int32 [1] (ra_kv4_status): 0, or why a request was left alone that is over its
+ *     budget (its length or a page is out of range, the budget is below sinks +
+ *     recent, or there are more moves than max_moves; the largest code).  RA_KV4_BAD_FREE_COUNT: the
+ *     pages do not fit the free list, and all requests were left alone.
+ *   workspace (ra_kv4_evict_workspace_bytes, 256-byte aligned): zero before its first use, not shared
+ *     by calls that may overlap.
+ * The moves have to be made before new tokens are stored: the pages given back hold their
+ * sources.  No output lies over another array, but kv_lens_out may be kv_lens and
+ * free_count_out free_count.
+ */
+ra_status ra_kv4_evict_workspace_bytes(int32_t num_requests, size_t* bytes);
+ra_status ra_kv4_evict(const float* weights, int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                       int32_t table_width, int64_t table_stride, const int32_t* kv_lens, int32_t num_requests,
+                       const int32_t* budgets, int32_t slack, int32_t recent, int32_t sinks, int32_t max_moves,
+                       int32_t* free_pages, int32_t num_free, const int32_t* free_count, int32_t* kv_lens_out,
+                       int32_t* dropped, int64_t* src_slots, int64_t* dst_slots, int32_t* free_count_out,
+                       int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Copy cached rows, as they are, from slot src_slots[i] to dst_slots[i], i <
+ * num_moves; pairs with a slot that is negative or outside the cache are left out.
+ * weights fp32 [num_pages * page_size], or NULL: the slots' sums go along.  A slot
+ * that is written must occur only once in the call.
+ */
+ra_status ra_kv4_move(const ra_kv4_cache* cache, const int64_t* src_slots, const int64_t* dst_slots,
+                      int64_t num_moves, float* weights, void* stream);
 
 /*
  * Synchronise `stream` and read a status word (ra_kv4_tables' status, or the
