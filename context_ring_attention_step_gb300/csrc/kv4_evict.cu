@@ -27,14 +27,15 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMaxCluster = 16;
 constexpr int kMaxKeys = 40960;  // keys of a CTA in shared memory; the others are made again where they are needed
 constexpr uint32_t kProtected = 0xffffffffu;
 
 // Block-wide exclusive prefix sum in thread order; `total` receives the sum.
+template <int T>
 __device__ __forceinline__ int block_prefix(int x, int* s_sum, int& total) {
+  constexpr int W = T / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int y = x;
 #pragma unroll
@@ -45,12 +46,12 @@ __device__ __forceinline__ int block_prefix(int x, int* s_sum, int& total) {
   __syncthreads();  // (s_sum of the call before was read)
   if (lane == 31) s_sum[warp] = y;
   __syncthreads();
-  int before = 0;
-  total = 0;
+  int before = lane < warp ? s_sum[lane % W] : 0;
+  total = lane < W ? s_sum[lane % W] : 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
+  for (int d = 16; d; d >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, d);
+    total += __shfl_xor_sync(0xffffffffu, total, d);
   }
   return before + y - x;
 }
@@ -60,12 +61,16 @@ struct Told {
   int bad, equal, holes, movers;
 };
 
-__global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictParams p, int keys_held) {
+// T threads: many where requests are few, few where many requests share an SM.
+template <int T>
+__global__ void __launch_bounds__(T, T == 1024 ? 1 : 4) kv4_evict_kernel(const Kv4EvictParams p, int keys_held) {
+  constexpr int kWarps = T / 32;
   extern __shared__ __align__(16) uint32_t s_keys[];
-  __shared__ __align__(16) uint32_t s_hist[3][kBins];
-  __shared__ int s_sum[kWarps], s_digit[3];  // digit, keys still to take at it, keys with it
+  __shared__ __align__(16) uint32_t s_hist[kBins];      // of this CTA
+  __shared__ __align__(16) uint32_t s_total[3][kBins];  // of the cluster, in its first CTA
+  __shared__ int s_sum[kWarps], s_digit[3];             // digit, keys still to take at it, keys with it
   __shared__ Told s_told;
-  __shared__ int s_last;
+  __shared__ int s_last, s_mine[4];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / C;
@@ -87,28 +92,37 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
   int64_t* src = p.src + (size_t)r * p.max_moves;
   int64_t* dst = p.dst + (size_t)r * p.max_moves;
   if (cut) {
-    // this CTA's tokens [t0, t1), and each warp's share of them, in whole 32s
-    const int per_cta = (L + C - 1) / C, per_warp = ((per_cta + kWarps - 1) / kWarps + 31) & ~31;
+    // this CTA's tokens [t0, t1), and each warp's share of them [w0, w1), in whole 128s: a lane
+    // takes four neighbours at a time, which lie on one page
+    const int per_cta = (L + C - 1) / C, per_warp = ((per_cta + kWarps - 1) / kWarps + 127) & ~127;
     const int t0 = min(rank * per_warp * kWarps, L), t1 = min(t0 + per_warp * kWarps, L);
     const int w0 = min(t0 + warp * per_warp, t1), w1 = min(w0 + per_warp, t1);
     int bad = 0;
     auto slot_of = [&](int t) -> int64_t {
+      return ((int64_t)table[t >> p.page_shift] << p.page_shift) + (t & (P - 1));
+    };
+    const bool wide = (reinterpret_cast<uintptr_t>(p.weights) & 15) == 0;
+    auto make_keys = [&](int t) -> uint4 {
       const int page = table[t >> p.page_shift];
-      return (uint32_t)page < (uint64_t)pages ? ((int64_t)page << p.page_shift) + (t & (P - 1)) : -1;
-    };
-    auto make_key = [&](int t) -> uint32_t {
-      const int64_t slot = slot_of(t);
-      if (slot < 0) {
+      if ((uint32_t)page >= (uint64_t)pages) {
         bad = 1;
-        return 0u;
+        return make_uint4(0u, 0u, 0u, 0u);
       }
-      if (t < p.sinks || t >= L - p.recent) return kProtected;
-      const float w = __ldg(p.weights + slot);
-      return w > 0.f ? __float_as_uint(w) : 0u;
+      const float* w = p.weights + ((int64_t)page << p.page_shift) + (t & (P - 1));
+      const float4 x = wide ? __ldg(reinterpret_cast<const float4*>(w))
+                            : make_float4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+      auto key = [&](int t, float w) -> uint32_t {
+        return t < p.sinks || t >= L - p.recent ? kProtected : w > 0.f ? __float_as_uint(w) : 0u;
+      };
+      return make_uint4(key(t, x.x), key(t + 1, x.y), key(t + 2, x.z), key(t + 3, x.w));
     };
-    auto key_of = [&](int t) -> uint32_t { return t - t0 < keys_held ? s_keys[t - t0] : make_key(t); };
-    for (int i = tid; i < 3 * kBins; i += kThreads) (&s_hist[0][0])[i] = 0u;
+    auto keys_of = [&](int t) -> uint4 {
+      return t - t0 + 3 < keys_held ? *reinterpret_cast<const uint4*>(s_keys + (t - t0)) : make_keys(t);
+    };
+    auto get = [](const uint4& k, int i) { return i == 0 ? k.x : i == 1 ? k.y : i == 2 ? k.z : k.w; };
+    for (int i = tid; i < kBins; i += T) s_hist[i] = s_total[0][i] = s_total[1][i] = s_total[2][i] = 0u;
     if (tid == 0) s_told = Told{0, 0, 0, 0};
+    if (C > 1) cluster.sync();  // (the others add to the first CTA's bins)
     __syncthreads();
     // add one to a bin for every lane that asks; neighbours often ask for the same one
     auto count = [&](uint32_t* hist, bool in, uint32_t bin) {
@@ -121,12 +135,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
         atomicAdd(hist + bin, 1u);
       }
     };
-#pragma unroll 4
-    for (int t = w0 + lane; t - lane < w1; t += 32) {
-      const bool in = t < w1;
-      const uint32_t k = in ? make_key(t) : 0u;
-      if (in && t - t0 < keys_held) s_keys[t - t0] = k;
-      count(s_hist[0], in, k >> 21);
+#pragma unroll 1
+    for (int t = w0 + 4 * lane; t - 4 * lane < w1; t += 256) {
+      uint4 k[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) k[h] = t + 128 * h < w1 ? make_keys(t + 128 * h) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int u = t + 128 * h;
+        if (u < w1 && u - t0 + 3 < keys_held) *reinterpret_cast<uint4*>(s_keys + (u - t0)) = k[h];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) count(s_hist, u + i < w1, get(k[h], i) >> 21);
+      }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_told.bad, 1);
 
@@ -138,24 +158,36 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       if (pass > 0) {
         const uint32_t top = shift + (pass == 1 ? 11 : 10);
-        for (int t = w0 + lane; t - lane < w1; t += 32) {
-          const bool in = t < w1;
-          const uint32_t k = in ? key_of(t) : 0u;
-          count(s_hist[pass], in && (k >> top) == (key >> top), (k >> shift) & (pass == 1 ? 2047u : 1023u));
+        for (int t = w0 + 4 * lane; t - 4 * lane < w1; t += 128) {
+          const uint4 k = t < w1 ? keys_of(t) : make_uint4(0u, 0u, 0u, 0u);
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m |= (t + i < w1 && (get(k, i) >> top) == (key >> top) ? 1u : 0u) << i;
+          if (!__any_sync(0xffffffffu, m != 0)) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) count(s_hist, (m >> i) & 1u, (get(k, i) >> shift) & (pass == 1 ? 2047u : 1023u));
         }
       }
-      cluster.sync();
-      // bins from the top: thread i has bins kBins - 4 - 4 i and the three behind it
-      const int b0 = kBins - 4 - 4 * tid;
-      int n[4] = {0, 0, 0, 0};
-      for (int c = 0; c < C; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s_hist[pass][b0], c));
-        n[0] += x.x; n[1] += x.y; n[2] += x.z; n[3] += x.w;
+      // this CTA's bins to the cluster's; most are empty
+      __syncthreads();
+      for (int i = tid; i < kBins; i += T) {
+        const uint32_t n = s_hist[i];
+        if (n) {
+          atomicAdd(cluster.map_shared_rank(&s_total[pass][i], 0), n);
+          s_hist[i] = 0u;
+        }
       }
-      int total;
-      int above = block_prefix(n[0] + n[1] + n[2] + n[3], s_sum, total);
+      if (C > 1) cluster.sync(); else __syncthreads();
+      // bins from the top: thread i has the kBins / T behind place kBins - (i + 1) kBins / T
+      constexpr int kEach = kBins / T;
+      const int b0 = kBins - kEach - kEach * tid;
+      int n[kEach], sum = 0;
 #pragma unroll
-      for (int i = 3; i >= 0; --i) {
+      for (int i = 0; i < kEach; ++i) sum += n[i] = (int)*cluster.map_shared_rank(&s_total[pass][b0 + i], 0);
+      int total;
+      int above = block_prefix<T>(sum, s_sum, total);
+#pragma unroll
+      for (int i = kEach - 1; i >= 0; --i) {
         if (above < take && above + n[i] >= take) {
           s_digit[0] = b0 + i;
           s_digit[1] = take - above;
@@ -173,73 +205,137 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
         equal = 0;
       }
     }
-    for (int c = 0; c < C; ++c) bad |= cluster.map_shared_rank(&s_told, c)->bad;
 
     // ---- of equal keys the lowest indices: this warp's first one's rank among them
     int before_equal = 0;
+    // sums over the cluster's CTAs of what they told: f(Told) of all of them, and of those before this one
+    auto gather = [&](auto f, int& before) {
+      int x = lane < C ? f(*cluster.map_shared_rank(&s_told, lane)) : 0;
+      before = lane < rank ? x : 0;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, d);
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+      }
+      return x;
+    };
     if (equal != take) {
       int mine = 0;
-      for (int t = w0 + lane; t < w1; t += 32) mine += key_of(t) == key;
+      for (int t = w0 + 4 * lane; t < w1; t += 128) {
+        const uint4 k = keys_of(t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += t + i < w1 && get(k, i) == key;
+      }
 #pragma unroll
       for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-      int total;
-      before_equal = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? mine : 0, s_sum, total), 0);
+      int total, others;
+      before_equal = __shfl_sync(0xffffffffu, block_prefix<T>(lane == 0 ? mine : 0, s_sum, total), 0);
       if (tid == 0) s_told.equal = total;
-      cluster.sync();
-      for (int c = 0; c < rank; ++c) before_equal += cluster.map_shared_rank(&s_told, c)->equal;
+      if (C > 1) cluster.sync(); else __syncthreads();
+      gather([](const Told& o) { return o.equal; }, others);
+      before_equal += others;
     }
-    // every token of this warp's share in turn: is it kept?  f(t, in, kept)
+    // The warp's tokens in order, 128 at a time: f(t, places, moves), a lane's four from t on:
+    // those that are dropped before place B, and those that are kept behind it.
+    const uint32_t below = (1u << lane) - 1u;
+    auto rank_of = [&](uint32_t m, int& all) {  // bits set in the lanes before; in all
+      int n = 0;
+      all = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __ballot_sync(0xffffffffu, (m >> i) & 1u);
+        n += __popc(b & below);
+        all += __popc(b);
+      }
+      return n;
+    };
     auto walk = [&](auto f) {
       int seen = before_equal;
-      for (int t = w0 + lane; t - lane < w1; t += 32) {
-        const bool in = t < w1;
-        const uint32_t k = in ? key_of(t) : 0u;
-        bool kept = in && k > key;
-        const uint32_t same = __ballot_sync(0xffffffffu, in && k == key);
-        if (in && k == key) kept = equal == take || seen + __popc(same & ((1u << lane) - 1u)) < take;
-        seen += __popc(same);
-        f(t, in, kept);
+      for (int t = w0 + 4 * lane; t - 4 * lane < w1; t += 128) {
+        const uint4 k = t < w1 ? keys_of(t) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t in = 0, kept = 0, same = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          in |= (t + i < w1 ? 1u : 0u) << i;
+          kept |= (get(k, i) > key ? 1u : 0u) << i;
+          same |= (get(k, i) == key ? 1u : 0u) << i;
+        }
+        kept &= in;
+        same &= in;
+        if (equal == take) {
+          kept |= same;
+        } else if (__any_sync(0xffffffffu, same != 0)) {
+          int all;
+          int n = seen + rank_of(same, all);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((same >> i) & 1u) kept |= (n++ < take ? 1u : 0u) << i;
+          seen += all;
+        }
+        const int inside = min(max(B - t, 0), 4);  // of the four, before place B
+        const uint32_t first = (1u << inside) - 1u;
+        f(t, in & ~kept & first, kept & ~first);
       }
     };
     int holes = 0, movers = 0;  // of this warp
-    walk([&](int t, bool in, bool kept) {
-      holes += __popc(__ballot_sync(0xffffffffu, in && !kept && t < B));
-      movers += __popc(__ballot_sync(0xffffffffu, kept && t >= B));
+    walk([&](int t, uint32_t h, uint32_t m) {
+      holes += __popc(h);
+      movers += __popc(m);
     });
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      holes += __shfl_xor_sync(0xffffffffu, holes, d);
+      movers += __shfl_xor_sync(0xffffffffu, movers, d);
+    }
     int cta_holes, cta_movers;
-    int h0 = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? holes : 0, s_sum, cta_holes), 0);
-    int m0 = __shfl_sync(0xffffffffu, block_prefix(lane == 0 ? movers : 0, s_sum, cta_movers), 0);
+    int h0 = __shfl_sync(0xffffffffu, block_prefix<T>(lane == 0 ? holes : 0, s_sum, cta_holes), 0);
+    int m0 = __shfl_sync(0xffffffffu, block_prefix<T>(lane == 0 ? movers : 0, s_sum, cta_movers), 0);
     if (tid == 0) {
       s_told.holes = cta_holes;
       s_told.movers = cta_movers;
     }
-    cluster.sync();
-    for (int c = 0; c < C; ++c) {
-      const Told* o = cluster.map_shared_rank(&s_told, c);
-      if (c < rank) {
-        h0 += o->holes;
-        m0 += o->movers;
+    if (C > 1) cluster.sync(); else __syncthreads();
+    if (warp == 0) {
+      int holes_before, movers_before, none;
+      gather([](const Told& o) { return o.holes; }, holes_before);
+      const int all = gather([](const Told& o) { return o.movers; }, movers_before);
+      const int wrong = gather([](const Told& o) { return o.bad; }, none);
+      if (lane == 0) {
+        s_mine[0] = holes_before;
+        s_mine[1] = movers_before;
+        s_mine[2] = all;
+        s_mine[3] = wrong;
       }
-      moves += o->movers;
     }
+    __syncthreads();
+    h0 += s_mine[0];
+    m0 += s_mine[1];
+    moves = s_mine[2];
+    bad = s_mine[3];
     if (bad) code = RA_KV4_BAD_PAGE;
     else if (moves > p.max_moves) code = RA_KV4_TOO_MANY_MOVES;
     if (code) {
       cut = false;
       moves = 0;
     } else {
-      walk([&](int t, bool in, bool kept) {
-        const uint32_t h = __ballot_sync(0xffffffffu, in && !kept && t < B), m = __ballot_sync(0xffffffffu, kept && t >= B);
-        const uint32_t below = (1u << lane) - 1u;
-        if ((h >> lane) & 1u) dst[h0 + __popc(h & below)] = slot_of(t);
-        if ((m >> lane) & 1u) src[m0 + __popc(m & below)] = slot_of(t);
-        h0 += __popc(h);
-        m0 += __popc(m);
+      walk([&](int t, uint32_t h, uint32_t m) {
+        if (!__any_sync(0xffffffffu, (h | m) != 0)) return;
+        int all_h, all_m;
+        int nh = h0 + rank_of(h, all_h), nm = m0 + rank_of(m, all_m);
+        h0 += all_h;
+        m0 += all_m;
+        if (!(h | m)) return;
+        const int64_t slot = slot_of(t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if ((h >> i) & 1u) dst[nh++] = slot + i;
+          if ((m >> i) & 1u) src[nm++] = slot + i;
+        }
       });
     }
-    cluster.sync();  // no CTA ends while another reads its shared memory
+    if (C > 1) cluster.sync();  // no CTA ends while another reads its shared memory
   }
-  for (int i = moves + rank * kThreads + tid; i < p.max_moves; i += C * kThreads) src[i] = dst[i] = -1;
+  for (int i = moves + rank * T + tid; i < p.max_moves; i += C * T) src[i] = dst[i] = -1;
 
   // ---- the call's last CTA: lengths, pages given back, status
   __syncthreads();
@@ -256,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
   __threadfence();
   const int R = p.num_requests;
   const int count0 = p.free_count ? *p.free_count : 0;
-  // (the prefix sums of all requests' pages lie where the histograms were, or in the workspace)
-  int* s_back = reinterpret_cast<int*>(&s_hist[0][0]);  // [R + 1], R <= 4096
-  const int per = (R + kThreads - 1) / kThreads, r0 = min(tid * per, R), r1 = min(r0 + per, R);
+  // (the prefix sums of all requests' pages lie where the histograms were)
+  int* s_back = reinterpret_cast<int*>(&s_total[0][0]);  // [R + 1], R <= 4096
+  const int per = (R + T - 1) / T, r0 = min(tid * per, R), r1 = min(r0 + per, R);
   auto held = [&](int n) { return n > 0 ? (int)(((long long)n + P - 1) >> p.page_shift) : 0; };
   long long back = 0;
   for (int i = r0; i < r1; ++i) {
@@ -278,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
   const bool fits = !push || (count0 >= 0 && count0 + sum <= p.num_free);
   if (!push || !fits) back = sum = 0;
   int total;
-  int at = block_prefix((int)back, s_sum, total);
+  int at = block_prefix<T>((int)back, s_sum, total);
   for (int i = r0; i < r1; ++i) {
     const int l = p.kv_lens[i], a = fits ? __ldcg(p.after + i) : l;
     s_back[i] = at;
@@ -286,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
   }
   if (tid == 0) s_back[R] = total;
   __syncthreads();
-  for (int i = tid; i < total; i += kThreads) {
+  for (int i = tid; i < total; i += T) {
     int lo = 0, hi = R;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -295,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_evict_kernel(const Kv4EvictPa
     p.free_pages[count0 + i] = p.block_table[(size_t)lo * p.table_stride + held(__ldcg(p.after + lo)) + (i - s_back[lo])];
   }
   if (!fits)  // nothing is dropped
-    for (long long i = tid; i < (long long)R * p.max_moves; i += kThreads) p.src[i] = p.dst[i] = -1;
+    for (long long i = tid; i < (long long)R * p.max_moves; i += T) p.src[i] = p.dst[i] = -1;
   __syncthreads();
   for (int i = r0; i < r1; ++i) {
     const int l = p.kv_lens[i], a = fits ? __ldcg(p.after + i) : l;
@@ -341,28 +437,44 @@ __global__ void __launch_bounds__(256) kv4_move_kernel(const Kv4MoveParams p) {
 
 }  // namespace
 
-cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream) {
-  // CTAs of a request: enough that each has about 8192 tokens at most, where the
-  // requests alone do not fill the GPU
-  const int64_t most = std::min((int64_t)p.table_width << p.page_shift, (int64_t)kKv4MaxLength);
-  int ctas = 1;
-  while (ctas < 8 && most > 8192ll * ctas && (int64_t)p.num_requests * ctas < 152) ctas *= 2;
-  const int64_t share = ((most + ctas - 1) / ctas + kWarps - 1) / kWarps;
-  const int keys = (int)std::min<int64_t>((share + 31) / 32 * 32 * kWarps, kMaxKeys);
+template <int T>
+static cudaError_t launch_evict(const Kv4EvictParams& p, int ctas, int64_t most, cudaStream_t stream) {
+  auto kern = kv4_evict_kernel<T>;
+  const int64_t share = ((most + ctas - 1) / ctas + T / 32 - 1) / (T / 32);
+  const int keys = (int)std::min<int64_t>((share + 127) / 128 * 4 * T, kMaxKeys);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(p.num_requests * ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(T);
   cfg.dynamicSmemBytes = (size_t)keys * 4;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static Kv4SmemLimit limit;
-  return limit.launch(reinterpret_cast<const void*>(kv4_evict_kernel), kMaxKeys * 4,
-                      [&] { return cudaLaunchKernelEx(&cfg, kv4_evict_kernel, p, keys); });
+  return limit.launch(reinterpret_cast<const void*>(kern), kMaxKeys * 4, [&] {
+    cudaError_t e = ctas > 8 ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
+                             : cudaSuccess;
+    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, p, keys) : e;
+  });
+}
+
+cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t stream) {
+  // CTAs of a request: as many as have 2048 tokens each at least, where the requests alone do not
+  // fill the GPU
+  const int64_t most = std::min((int64_t)p.table_width << p.page_shift, (int64_t)kKv4MaxLength);
+  int ctas = 1;
+  while (ctas < kMaxCluster && most > 2048ll * ctas && (int64_t)p.num_requests * ctas * 2 <= 128) ctas *= 2;
+  if (p.num_requests > 128) return launch_evict<256>(p, ctas, most, stream);
+  cudaError_t e = launch_evict<1024>(p, ctas, most, stream);
+  if (e != cudaSuccess && ctas > 8) {  // (a GPU, or a part of one, without 16 free SMs side by side)
+    (void)cudaGetLastError();
+    e = launch_evict<1024>(p, 8, most, stream);
+  }
+  return e;
 }
 
 cudaError_t launch_kv4_move(int D, const Kv4MoveParams& p, cudaStream_t stream) {
