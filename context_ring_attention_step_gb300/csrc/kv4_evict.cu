@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : 4) kv4_evict_kernel(const K
         atomicAdd(hist + bin, 1u);
       }
     };
+    uint32_t* hist = C > 1 ? s_hist : s_total[0];
 #pragma unroll 1
     for (int t = w0 + 4 * lane; t - 4 * lane < w1; t += 256) {
       uint4 k[2];
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : 4) kv4_evict_kernel(const K
         const int u = t + 128 * h;
         if (u < w1 && u - t0 + 3 < keys_held) *reinterpret_cast<uint4*>(s_keys + (u - t0)) = k[h];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) count(s_hist, u + i < w1, get(k[h], i) >> 21);
+        for (int i = 0; i < 4; ++i) count(hist, u + i < w1, get(k[h], i) >> 21);
       }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_told.bad, 1);
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : 4) kv4_evict_kernel(const K
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       if (pass > 0) {
         const uint32_t top = shift + (pass == 1 ? 11 : 10);
+        if (C == 1) hist = s_total[pass];
         for (int t = w0 + 4 * lane; t - 4 * lane < w1; t += 128) {
           const uint4 k = t < w1 ? keys_of(t) : make_uint4(0u, 0u, 0u, 0u);
           uint32_t m = 0;
@@ -165,45 +167,50 @@ __global__ void __launch_bounds__(T, T == 1024 ? 1 : 4) kv4_evict_kernel(const K
           for (int i = 0; i < 4; ++i) m |= (t + i < w1 && (get(k, i) >> top) == (key >> top) ? 1u : 0u) << i;
           if (!__any_sync(0xffffffffu, m != 0)) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) count(s_hist, (m >> i) & 1u, (get(k, i) >> shift) & (pass == 1 ? 2047u : 1023u));
+          for (int i = 0; i < 4; ++i) count(hist, (m >> i) & 1u, (get(k, i) >> shift) & (pass == 1 ? 2047u : 1023u));
         }
       }
-      // this CTA's bins to the cluster's; most are empty
       __syncthreads();
-      for (int i = tid; i < kBins; i += T) {
-        const uint32_t n = s_hist[i];
-        if (n) {
-          atomicAdd(cluster.map_shared_rank(&s_total[pass][i], 0), n);
-          s_hist[i] = 0u;
+      if (C > 1) {  // this CTA's bins to the cluster's; most are empty
+        for (int i = tid; i < kBins; i += T) {
+          const uint32_t n = s_hist[i];
+          if (n) {
+            atomicAdd(cluster.map_shared_rank(&s_total[pass][i], 0), n);
+            s_hist[i] = 0u;
+          }
+        }
+        cluster.sync();
+      }
+      // The first CTA finds the digit for all: 16 that each read its 8 KB of bins took 6 us a pass.
+      // Bins from the top: thread i has the kBins / T behind place kBins - (i + 1) kBins / T.
+      if (rank == 0) {
+        constexpr int kEach = kBins / T;
+        const int b0 = kBins - kEach - kEach * tid;
+        int n[kEach], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) sum += n[i] = (int)s_total[pass][b0 + i];
+        int total;
+        int above = block_prefix<T>(sum, s_sum, total);
+#pragma unroll
+        for (int i = kEach - 1; i >= 0; --i) {
+          if (above < take && above + n[i] >= take) {
+            s_digit[0] = b0 + i;
+            s_digit[1] = take - above;
+            s_digit[2] = n[i];
+          }
+          above += n[i];
         }
       }
       if (C > 1) cluster.sync(); else __syncthreads();
-      // bins from the top: thread i has the kBins / T behind place kBins - (i + 1) kBins / T
-      constexpr int kEach = kBins / T;
-      const int b0 = kBins - kEach - kEach * tid;
-      int n[kEach], sum = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) sum += n[i] = (int)*cluster.map_shared_rank(&s_total[pass][b0 + i], 0);
-      int total;
-      int above = block_prefix<T>(sum, s_sum, total);
-#pragma unroll
-      for (int i = kEach - 1; i >= 0; --i) {
-        if (above < take && above + n[i] >= take) {
-          s_digit[0] = b0 + i;
-          s_digit[1] = take - above;
-          s_digit[2] = n[i];
-        }
-        above += n[i];
+      if (take <= 0) {  // none is kept
+        key = kProtected;
+        break;
       }
-      __syncthreads();
-      if (take > 0) {
-        key |= (uint32_t)s_digit[0] << shift;
-        take = s_digit[1];
-        equal = s_digit[2];
-      } else {
-        key = kProtected;  // none is kept
-        equal = 0;
-      }
+      const int* digit = cluster.map_shared_rank(s_digit, 0);
+      key |= (uint32_t)digit[0] << shift;
+      take = digit[1];
+      equal = digit[2];
+      if (equal == take) break;  // all keys that begin with these digits are taken: those from `key` on
     }
 
     // ---- of equal keys the lowest indices: this warp's first one's rank among them
