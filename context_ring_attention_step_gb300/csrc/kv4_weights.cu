@@ -9,13 +9,15 @@
 // additions is fixed.
 //
 // What has to be read are the codes of the keys: 0.5625 D bytes a token and head
-// for 2 D flops and one exponential a row.  As in kv4_attn.cu keys are the M side
+// for 2 D flops and one exponential a row: 128 requests of 500 to 16000 tokens, 4 rows a head at
+// head_dim 128, take 73 us, 4.0 TB/s; a tile and head costs 190 instructions of a warp (a third of them
+// the expansion), and the schedulers issue 64 % of the time.  As in kv4_attn.cu keys are the M side
 // of the product (16 tokens x 8 rows), a lane's codes are whole words that it
 // copies through a ring of its own, and a code expands with one conversion and one
-// multiplication.  A tile is expanded once for all row tiles; those lie in shared
+// multiplication; asked for early in registers instead of the ring, the same call took 103 us,
+// and with three CTAs on an SM in place of four 78.  A tile is expanded once for all row tiles; those lie in shared
 // memory in the order of the operand registers.
 #include <algorithm>
-#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,10 +31,6 @@
 namespace ra {
 namespace {
 
-#ifndef WP
-#define WP 4
-#define WH 1
-#endif
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int KB = 16 * kWarps;  // keys of one block: a tile a warp
@@ -40,12 +38,11 @@ constexpr int kExpandCost = 3;   // expanding a tile, in row tiles
 
 template <int D>
 struct WeightsCfg {
-  static constexpr int kPerSm = D == 64 ? 4 : D == 128 ? WP : 2;
+  static constexpr int kPerSm = D == 256 ? 2 : 4;      // CTAs on an SM
   static constexpr int kTile = 9 * D;                  // bytes of a tile's keys: codes, then scales
   static constexpr int kSlots = D == 256 ? 6 : 8;      // ring of each warp
-  static constexpr int kHeads = D == 256 ? 1 : WH;     // heads whose products are mixed
   static constexpr int kQTile = 16 * D;                // bytes of eight rows in fp16
-  static constexpr int kCap = D == 64 ? 28 : D == 128 ? (WP == 3 ? 16 : 8) : 12;  // row tiles in shared memory at once
+  static constexpr int kCap = D == 64 ? 28 : D == 128 ? 8 : 12;  // row tiles in shared memory at once
   static constexpr int kRing = kWarps * kSlots * kTile;
   static constexpr int kSmem = kRing + kCap * (kQTile + 8 * 12);
   static_assert(kSmem <= (220 / kPerSm - 1) * 1024, "CTAs on an SM");
@@ -270,57 +267,42 @@ __global__ void __launch_bounds__(kThreads, (WeightsCfg<D>::kPerSm)) kv4_weights
           sum1 += __shfl_xor_sync(0xffffffffu, sum1, 2);
           if (dst) *dst = old + (c4 == 0 ? sum0 : sum1);
         };
-        // a tile's keys of N neighbouring heads against all rows of those
+        // a tile's keys of one head against all rows of it
         int slot = 0;
-        auto products = [&](auto heads, int hh) {
-          constexpr int N = decltype(heads)::value;
+        auto products = [&](int hh) {
           const int tok = i * KB + 16 * warp;
           const bool masked = tok + 16 > lim_min;
-          copy_wait<S - 1 - N>();
-          uint32_t a[N][D / 16][4];
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            KeyRegs<D> keys;
-            load_keys<D>(keys, ring + slot, lane);
-            slot = slot == (S - 1) * C::kTile ? 0 : slot + C::kTile;
-            expand_keys<D>(keys, a[n]);
-          }
-#pragma unroll
-          for (int n = 0; n < N; ++n) ask();
+          copy_wait<S - 2>();
+          uint32_t a[D / 16][4];
+          KeyRegs<D> keys;
+          load_keys<D>(keys, ring + slot, lane);
+          slot = slot == (S - 1) * C::kTile ? 0 : slot + C::kTile;
+          expand_keys<D>(keys, a);
+          ask();
           const uint4* q = s_q + hh * nt * D + lane;
           const float2* rows = s_row + hh * nt * 8 + 2 * c4;
 #pragma unroll 1
           for (int t = 0; t < nt; ++t, q += D, rows += 8) {
-            float e[N][4];
+            float c[2][4] = {}, e[4];
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-              float c[2][4] = {};
+            for (int j = 0; j < D / 32; ++j) {
+              const uint4 w = q[32 * j];
+              const uint32_t x[2] = {w.x, w.y}, y[2] = {w.z, w.w};
+              mma16816(c[0], a[2 * j], x);
+              mma16816(c[1], a[2 * j + 1], y);
+            }
+            const float4 row = *reinterpret_cast<const float4*>(rows);
 #pragma unroll
-              for (int j = 0; j < D / 32; ++j) {
-                const uint4 w = q[n * nt * D + 32 * j];
-                const uint32_t x[2] = {w.x, w.y}, y[2] = {w.z, w.w};
-                mma16816(c[0], a[n][2 * j], x);
-                mma16816(c[1], a[n][2 * j + 1], y);
-              }
-              const float4 row = *reinterpret_cast<const float4*>(rows + n * nt * 8);
+            for (int v = 0; v < 4; ++v)
+              e[v] = ex2_approx(fmaf(c[0][v] + c[1][v], v & 1 ? row.z : row.x, v & 1 ? row.w : row.y));
+            if (masked) {
+              const int2 lim = *reinterpret_cast<const int2*>(s_lim + (hh * nt + t) * 8 + 2 * c4);
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                e[n][v] = ex2_approx(fmaf(c[0][v] + c[1][v], v & 1 ? row.z : row.x, v & 1 ? row.w : row.y));
+                if (tok + r8 + 8 * (v >> 1) >= (v & 1 ? lim.y : lim.x)) e[v] = 0.f;
             }
-            if (masked) {
-#pragma unroll
-              for (int n = 0; n < N; ++n) {
-                const int2 lim = *reinterpret_cast<const int2*>(s_lim + ((hh + n) * nt + t) * 8 + 2 * c4);
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  if (tok + r8 + 8 * (v >> 1) >= (v & 1 ? lim.y : lim.x)) e[n][v] = 0.f;
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-              sum0 += e[n][0] + e[n][1];
-              sum1 += e[n][2] + e[n][3];
-            }
+            sum0 += e[0] + e[1];
+            sum1 += e[2] + e[3];
           }
         };
         if (nh > 0 && i < e1) {
@@ -330,10 +312,8 @@ __global__ void __launch_bounds__(kThreads, (WeightsCfg<D>::kPerSm)) kv4_weights
 #pragma unroll 1
         for (; i < e1; ++i) {
           begin();
-          int hh = 0;
 #pragma unroll 1
-          for (; hh + C::kHeads <= nh; hh += C::kHeads) products(std::integral_constant<int, C::kHeads>{}, hh);
-          if (C::kHeads > 1 && hh < nh) products(std::integral_constant<int, 1>{}, hh);
+          for (int hh = 0; hh < nh; ++hh) products(hh);
           end();
         }
         copy_wait<0>();

@@ -23,7 +23,16 @@
 //   warp 3        TMA loads of query tiles
 //   warps 4-11    exponentials and sums: a thread is a key, at head_dim 256 and half of a tile's rows
 //   warps 12-15   cache -> bf16 keys: a thread is a key here too
-// Tensor memory (512 columns): the keys (D / 2 columns for 128 of them), then a ring of S^T tiles.
+// Tensor memory (512 columns): the keys (D / 2 columns for 128 of them; at head_dim 256 those of two
+// units, 4 to 10 % faster), then a ring of S^T tiles.
+//
+// 1024 tokens x 32 query heads over 33792 cached, 8 key heads of 128: 257 us, 1088 TFLOP/s; tensor
+// cores are at work half of that and exponentials 46 %.  128 rows of queries against 256 keys cost 1154
+// clocks of the one, 1024 of the other, and about 2100 in all: a summing warp's 512 clocks of
+// exponentials begin when a tile is ready and wait for its 128 columns to come, and two warps a
+// scheduler do not cover that.  (Single issuer: 290 us; log-sum-exps from shared memory: 294; tiles of 192
+// rows: 364.)  64 tokens over 32768: 44 us, of which 13 are start, first keys and the merge of blocks whose
+// heads lie in two CTAs.
 // Items (block of keys, head) lie on one line that the CTAs cut evenly; of a block
 // whose heads went to several CTAs the one that brings the last sum adds them, in
 // the CTAs' order.
@@ -53,8 +62,9 @@ struct WTile {
   static constexpr int kCols = kN / kShares;                 // columns of a thread
   static constexpr int kKCols = D / 2;                // tensor memory columns of 128 keys
   static constexpr int kSRing = D == 256 ? 4 : 3;     // S^T tiles (128 keys x kN rows) in tensor memory
-  static constexpr int kSOff = kKeyTiles * kKCols;
-  static_assert(kSOff + kSRing * kN <= 512, "tensor memory");
+  static constexpr int kSets = D == 256 ? 2 : 1;      // units whose keys lie there (two at 128 or 64: no faster)
+  static constexpr int kSOff = kSets * kKeyTiles * kKCols;
+  static_assert(kSOff + kSRing * kN <= 512 && (kSets == 1 || kKeyTiles == 1), "tensor memory");
   static constexpr int kQTile = kN * D * 2;
   static constexpr int kQStages = D == 64 ? 8 : 6;
   static constexpr int kOnesOff = kQStages * kQTile;  // the keys' side of the lse's step: 128 rows of 32 bytes
@@ -208,7 +218,7 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
   const uint32_t sQ = smem_u32(smem);
   auto lim_of = [&](int s) { return reinterpret_cast<int*>(smem + C::kLimOff + s * C::kLimStage); };  // [N], then the smallest and the largest
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  const uint32_t b_kfull = smem_u32(bars);            // [2] a tile's keys expanded (4 warps)
+  const uint32_t b_kfull = smem_u32(bars);            // [2] a tile's keys expanded (4 warps): of a key tile, or of a set
   const uint32_t b_kempty = smem_u32(bars + 2);       // [2]
   const uint32_t b_qfull = smem_u32(bars + 4);        // [QS]
   const uint32_t b_qempty = smem_u32(bars + 12);      // [QS]
@@ -308,7 +318,8 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       while (ok && wk.next()) {
         const int tiles = wk.job.tiles;
         for (long long x = wk.x0; x < wk.x1 && ok; ++x, ++item) {
-          if (!(ok = mbar_wait(b_kfull + 8 * kt, item & 1, ab, 160))) break;
+          const uint32_t set = item % C::kSets;
+          if (!(ok = mbar_wait(b_kfull + 8 * (kt + set), (item / C::kSets) & 1, ab, 160))) break;
           for (int t = 0; t < tiles; ++t, ++g) {
             if (!(ok = mbar_wait(b_qfull + 8 * qs, qph, ab, 161))) break;
             // the place's last tile: with two key tiles the other one's, one or two before this one
@@ -323,7 +334,7 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
             const uint32_t tS = tmem + C::kSOff + sb * N;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_ts(tS, tK + kk * 8, sdesc_at(dq, (kk >> 2) * (N * 128) + (kk & 3) * 32, 16), C::kIdesc, kk > 0);
+              umma_ts(tS, tK + set * C::kKCols + kk * 8, sdesc_at(dq, (kk >> 2) * (N * 128) + (kk & 3) * 32, 16), C::kIdesc, kk > 0);
             umma_ss(tS, d1, sdesc_at(d1, (uint32_t)(128 * 32 + ls * C::kLseTile), 0), C::kIdesc, 1);
             umma_commit(b_sfull + 8 * (4 * kt + sb));
             umma_commit(b_qempty + 8 * qs);
@@ -331,7 +342,7 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
             if (++qs == QS) { qs = 0; qph ^= 1; }
             if (++ls == LS) { ls = 0; lph ^= 1; }
           }
-          if (ok) umma_commit(b_kempty + 8 * kt);
+          if (ok) umma_commit(b_kempty + 8 * (kt + set));
         }
       }
       if (!ok) {  // let issued MMAs finish before tensor memory is released
@@ -512,7 +523,7 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
           if (none) {
             release();
           } else {
-uint32_t s[NC / 32][32];
+            uint32_t s[NC / 32][32];
 #pragma unroll
             for (int c = 0; c < NC / 32; ++c) tmem_ld32(tS + sb * N + 32 * c, s[c]);
             tmem_ld_wait();
@@ -539,14 +550,15 @@ uint32_t s[NC / 32][32];
         // ---- the block's sums (after a wait that was given up: not known)
         if (!ok) acc = quiet_nan();
         float total = acc;
-        float* others = reinterpret_cast<float*>(smem + C::kPartOff);
-        keys_sync();  // (they were read)
-        if (share > 0) others[(share - 1) * C::kKeys + key_t] = acc;
-        keys_sync();
         const bool owner = share == 0;
-        if (owner) {
+        if (C::kShares > 1) {
+          float* others = reinterpret_cast<float*>(smem + C::kPartOff);
+          keys_sync();  // (they were read)
+          if (!owner) others[(share - 1) * C::kKeys + key_t] = acc;
+          keys_sync();
 #pragma unroll
-          for (int i = 1; i < C::kShares; ++i) total += others[(i - 1) * C::kKeys + key_t];
+          for (int i = 1; i < C::kShares; ++i)
+            if (owner) total += others[(i - 1) * C::kKeys + key_t];
         }
         const long long first = (long long)blk * Hkv;  // the block's first item
         bool writes = true;
@@ -644,14 +656,15 @@ uint32_t s[NC / 32][32];
         }
 #pragma unroll
         for (int kt = 0; kt < kT; ++kt) {
-          if (ok) ok = mbar_wait(b_kempty + 8 * kt, (item & 1) ^ 1, ab, 167);
+          const uint32_t set = item % C::kSets;
+          if (ok) ok = mbar_wait(b_kempty + 8 * (kt + set), ((item / C::kSets) & 1) ^ 1, ab, 167);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          expand_key<D>(tK + kt * C::kKCols, k[kt]);
+          expand_key<D>(tK + (kt + set) * C::kKCols, k[kt]);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_kfull + 8 * kt);
+          if (lane == 0) mbar_arrive(b_kfull + 8 * (kt + set));
           if (x + 1 < wk.x1) fetch(k[kt], kt, blk, head, page[kt]);
         }
       }
