@@ -81,11 +81,11 @@ int64_t few_rows(int32_t G, int32_t max_q_len) {
 // The same for the weights of cached tokens: there the tile kernel's time hardly depends on the
 // rows up to 128 a request either.  8 key heads of head_dim 128 / 64 / 256, 8 requests of 8192 cached
 // tokens, us:
-//    32 rows   74 /  60 /  75 (tiles),  47 /  36 /  69 (few rows)
-//    48 rows   74 /  60 /  75 (tiles),  75 /  46 /  93 (few rows)
-//    64 rows   74 /  60 /  75 (tiles),  86 /  61 / 128 (few rows)
-//    96 rows   74 /  59 /  95 (tiles), 136 /  87 / 181 (few rows).
-// One request of 32768 crosses at 48 / 64 / 48 rows, 32 of 4096 at 72 / 88 / 56.
+//    32 rows   74 /  60 /  80 (tiles),  47 /  36 /  69 (few rows)
+//    48 rows   74 /  60 /  81 (tiles),  75 /  46 /  93 (few rows)
+//    64 rows   74 /  60 /  77 (tiles),  86 /  61 / 128 (few rows)
+//    96 rows   74 /  59 / 101 (tiles), 136 /  87 / 181 (few rows).
+// One request of 32768 crosses at 44 / 62 / 38 rows, 32 of 4096 at 70 / 86 / 52.
 constexpr int kWeightsTileRows = 64;
 static_assert(2 * 256 * ra::kKv4MaxSms <= 2 * ra::kKv4MaxSms * 8 * (64 + 16), "attention's workspace holds the tile kernel's sums");
 

@@ -9,7 +9,7 @@
 // additions is fixed.
 //
 // What has to be read are the codes of the keys: 0.5625 D bytes a token and head
-// for 2 D flops and one exponential a row: 128 requests of 500 to 16000 tokens, 4 rows a head at
+// for 2 D flops and one exponential a row: 128 requests of 4000 tokens on average, 4 rows a head at
 // head_dim 128, take 73 us, 4.0 TB/s; a tile and head costs 190 instructions of a warp (a third of them
 // the expansion), and the schedulers issue 64 % of the time.  As in kv4_attn.cu keys are the M side
 // of the product (16 tokens x 8 rows), a lane's codes are whole words that it
