@@ -99,7 +99,7 @@ def test_small_batches(ra, kind, page, in_place):
                                       (131072, 0, 256), (70001, 64, 32)])
 @pytest.mark.parametrize("kind", ["spread", "ties", "zeros"])
 def test_one_long_request(ra, L, B, page, kind):
-    """A cluster of up to eight CTAs; equal sums are told apart across them."""
+    """A cluster of up to 16 CTAs; equal sums are told apart across them."""
     table, w, free, count, N = draw(L, [L], page, kind=kind)
     check(ra, table, w, [L], [B], page, max(1, min(B, L - B)), 0 if B == 0 else 40, 0 if B == 0 else 41, min(B, 4), free, count)
 
@@ -113,6 +113,26 @@ def test_more_tokens_than_shared_memory_holds(ra):
     lens += [11] * 90
     table, w, free, count, N = draw(4, lens, 256, kind="ties")
     check(ra, table, w, lens, [3000] * len(lens), 256, 3000, 0, 0, 1, free, count)
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+def test_more_tokens_than_a_cluster_holds(ra, kind):
+    L, B = 16 * 40960 + 30000, 5000
+    table, w, free, count, N = draw(5, [L], 256, kind=kind)
+    check(ra, table, w, [L], [B], 256, B, 10, 11, 3, free, count)
+
+
+@pytest.mark.parametrize("L,B", [(40, 20), (9000, 700)])
+def test_sums_at_any_address(ra, L, B):
+    """Sums begin at any multiple of four bytes."""
+    table, w, free, count, N = draw(L, [L, 33], 16)
+    want = E.evict(w, table.tolist(), [L, 33], [B, 16], 16, B, 0, 1, 2)
+    for shift in (1, 2, 3):
+        buf = torch.full((len(w) + 4,), float("nan")).cuda()
+        buf[shift:shift + len(w)] = torch.tensor(w).cuda()
+        e = ra.kv4_evict(buf[shift:shift + len(w)], torch.tensor(table).cuda(), i32([L, 33]), i32([B, 16]), 16, B, 0, 1, 2,
+                         check=True)
+        assert (e.kv_lens.tolist(), e.dropped.tolist(), e.src_slots.tolist(), e.dst_slots.tolist()) == tuple(want[:4])
 
 
 @pytest.mark.parametrize("R", [127, 600, 4096])
