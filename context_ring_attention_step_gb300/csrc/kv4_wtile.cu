@@ -26,13 +26,14 @@
 // Tensor memory (512 columns): the keys (D / 2 columns for 128 of them; at head_dim 256 those of two
 // units, 4 to 10 % faster), then a ring of S^T tiles.
 //
-// 1024 tokens x 32 query heads over 33792 cached, 8 key heads of 128: 257 us, 1088 TFLOP/s; tensor
+// 1024 tokens x 32 query heads over 33792 cached, 8 key heads of 128: 254 us, 1100 TFLOP/s; tensor
 // cores are at work half of that and exponentials 46 %.  128 rows of queries against 256 keys cost 1154
 // clocks of the one, 1024 of the other, and about 2100 in all: a summing warp's 512 clocks of
-// exponentials begin when a tile is ready and wait for its 128 columns to come, and two warps a
-// scheduler do not cover that.  (Single issuer: 290 us; log-sum-exps from shared memory: 294; tiles of 192
-// rows: 364.)  64 tokens over 32768: 44 us, of which 13 are start, first keys and the merge of blocks whose
-// heads lie in two CTAs.
+// exponentials begin when a tile is ready and its 128 columns have come, and two warps a scheduler,
+// whose tiles are ready at the same time, do not cover that.  (One issuer: 290 us; the issuers in
+// strict turns: 269, one behind the other's tile: 257; log-sum-exps from shared memory: 294; a tile in pieces
+// of 32 columns, each summed while the next comes: 298; tiles of 192 rows: 364.)  64 tokens over 32768:
+// 44 us, of which 13 are start, first keys and the merge of blocks whose heads lie in two CTAs.
 // Items (block of keys, head) lie on one line that the CTAs cut evenly; of a block
 // whose heads went to several CTAs the one that brings the last sum adds them, in
 // the CTAs' order.
@@ -322,13 +323,13 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
           if (!(ok = mbar_wait(b_kfull + 8 * (kt + set), (item / C::kSets) & 1, ab, 160))) break;
           for (int t = 0; t < tiles; ++t, ++g) {
             if (!(ok = mbar_wait(b_qfull + 8 * qs, qph, ab, 161))) break;
+            if (!(ok = mbar_wait(b_lfull + 8 * ls, lph, ab, 168))) break;
             // the place's last tile: with two key tiles the other one's, one or two before this one
             const uint32_t sb = (C::kKeyTiles * g + kt) % C::kSRing;
             const uint32_t back = C::kKeyTiles == 1 ? C::kSRing : 2 - kt;
             if (g >= back && !(ok = mbar_wait(b_sempty + 8 * (4 * (C::kKeyTiles - 1 - kt) + sb),
                                               ((g - back) / C::kSRing) & 1, ab, 162)))
               break;
-            if (!(ok = mbar_wait(b_lfull + 8 * ls, lph, ab, 168))) break;
             tc_fence_after();
             const uint64_t dq = sdesc_at(opaque(d0), (uint32_t)(qs * C::kQTile), 0);
             const uint32_t tS = tmem + C::kSOff + sb * N;
@@ -507,13 +508,13 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
         for (int t = 0; t < job.tiles; ++t, ++g) {
           const uint32_t ls = g % LS;
           if (ok) ok = mbar_wait(b_lfull + 8 * ls, (g / LS) & 1, ab, 165);
+          const int4* lim = reinterpret_cast<const int4*>(lim_of(ls) + col0);
+          const int2 ends = *reinterpret_cast<const int2*>(lim_of(ls) + N);
+          const bool whole = key_end <= ends.x, none = key_end - 128 >= ends.y;  // all rows see all keys; none does any
           const uint32_t sb = (C::kKeyTiles * g + kt) % C::kSRing;
           if (ok) ok = mbar_wait(b_sfull + 8 * (4 * kt + sb), (g / C::kSRing) & 1, ab, 166);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          const int4* lim = reinterpret_cast<const int4*>(lim_of(ls) + col0);
-          const int2 ends = *reinterpret_cast<const int2*>(lim_of(ls) + N);
-          const bool whole = key_end <= ends.x, none = key_end - 128 >= ends.y;  // all rows see all keys; none does any
           auto release = [&]() {  // all columns are in registers: the S^T tile may be written again
             tc_fence_before();
             __syncwarp();
