@@ -13,6 +13,14 @@ ring attention uses them like this::
     kv4_store(cache, k1, v1, step.slot_map)
     o, lse = kv4_attention(q1, cache, table, step.kv_lens, step.cu_new, max_q_len=1)
 
+and, to keep every request within a budget, the attention weight that its
+tokens receive in the step, and once in a while the lightest ones' removal::
+
+    kv4_weights(q1, cache, table, step.kv_lens, step.cu_new, lse, sums, new_lens=ones, max_q_len=1)
+    cut = kv4_evict(sums, table, step.kv_lens, budgets, 64, max_moves, slack, recent, sinks, free_pages, step.free_count)
+    kv4_move(cache, cut.src_slots, cut.dst_slots, weights=sums)      # before the next kv4_store
+    # cut.kv_lens and cut.free_count go into the next kv4_tables; positions: its own + all cut.dropped so far
+
 No call synchronises unless ``check=True``, and with caller-owned outputs
 (``out=``) and ``workspace=`` none allocates, so a step can be captured into a
 CUDA graph.  Calls run on the current stream of the tensors' device.
