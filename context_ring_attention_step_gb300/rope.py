@@ -123,13 +123,20 @@ def _shape_of(q, k, positions, rotary, q_weight, k_weight, eps):
     return c, T, Hq, Hkv, dev
 
 
+def _trained(w):
+    return w is not None and w.requires_grad
+
+
 def qk_norm_rope_fwd(q, k, positions, rotary, q_weight=None, k_weight=None, eps=1e-6, out=None):
     """Normed and rotated (q, k) of q [T, Hq, d] and k [T, Hkv, d] (bf16; rows may be strided).
 
     ``positions`` int32 [T]; a negative one makes the token's rows zero.
     ``eps=None`` leaves the norm out.  ``out=(q_out, k_out)`` writes into
     caller-owned tensors (rows may be strided); they may be q and k themselves.
+    No gradient flows through it: ``qk_norm_rope`` does that.
     """
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or _trained(q_weight) or _trained(k_weight)):
+        raise ValueError("qk_norm_rope_fwd has no gradient: call qk_norm_rope, or this under torch.no_grad()")
     c, T, Hq, Hkv, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
     D = rotary.head_dim
     qp, qs = _strided("q", q, T, Hq, D, _BF16, dev)
@@ -214,5 +221,10 @@ class QkNormRope(torch.autograd.Function):
 
 
 def qk_norm_rope(q, k, positions, rotary, q_weight=None, k_weight=None, eps=1e-6):
-    """Differentiable ``qk_norm_rope_fwd``: gradients flow to q, k and the weights."""
+    """Differentiable ``qk_norm_rope_fwd``: gradients flow to q, k and the weights.
+
+    A backward pass that is captured into a CUDA graph needs leaves of its own, or that
+    every graph that was recorded eagerly from the same leaves is gone by then: PyTorch adds a
+    leaf's gradients up on the stream of its first graph, and a capture must not wait for that one.
+    """
     return QkNormRope.apply(q, k, q_weight, k_weight, positions, rotary, eps)

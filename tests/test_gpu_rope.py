@@ -10,11 +10,13 @@ Tolerances, from the arithmetic (u = 2^-24, an fp32 half step):
     then 8 warps, then 80 CTAs and 8): 2^-16 of the sum of magnitudes.
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
 
-from oracle import rope as O
+from oracle import attention as A, rope as O
 
 pytestmark = pytest.mark.gpu
 
@@ -308,6 +310,63 @@ def test_streams_graphs_and_two_calls_at_once(ra):
         b = ra.qk_norm_rope_bwd(qs, ks, gq, gk, ps, rotary, wq, wk)
         for x, y in zip(out + dout + (dwq, dwk), f + b):
             assert torch.equal(x, y)
+
+
+def test_before_ring_attention(ra):
+    """Norm and rotation, ring attention and both backward passes, as a training step runs them.
+
+    Ring attention's gradients differ from the oracle's by roundings of P, dS and the
+    results to bf16 (2^-9 of each, of either sign): together less than 2^-6 of their norm, and the
+    gradients of rows before the norm are linear in them."""
+    d, Hq, Hkv, cu = 64, 4, 2, [0, 96, 256]
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(cu[-1], Hq + 2 * Hkv, d, generator=g).to(torch.bfloat16)
+    do = torch.randn(cu[-1], Hq, d, generator=g).to(torch.bfloat16)
+    w = [(1 + 0.3 * torch.randn(d, generator=g)) for _ in range(2)]
+    qkv, wq, wk = x.cuda().requires_grad_(), w[0].cuda().requires_grad_(), w[1].cuda().requires_grad_()
+    rotary, freq = ra.Rotary(d, base=500.0), O.frequencies(d, 500.0)
+    pos = ra.rope_positions(cu)
+    q, k = ra.qk_norm_rope(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], pos, rotary, wq, wk)
+    o, _ = ra.ring_attention(q, k, qkv[:, Hq + Hkv:].contiguous(), cu, 2)
+    o.backward(do.cuda())
+    scale = 1 / math.sqrt(d)
+    rq, rk, rv, ro, _ = A.attention_bwd(q.detach().cpu(), k.detach().cpu(), x[:, Hq + Hkv:], do, cu, True, scale)
+    p = pos.cpu().numpy()
+    dq, dwq = O.backward(x[:, :Hq].double().numpy(), rq, p, freq, False, w[0].double().numpy(), 1e-6)
+    dk, dwk = O.backward(x[:, Hq:Hq + Hkv].double().numpy(), rk, p, freq, False, w[1].double().numpy(), 1e-6)
+    for got, want in ((qkv.grad[:, :Hq], dq), (qkv.grad[:, Hq:Hq + Hkv], dk), (qkv.grad[:, Hq + Hkv:], rv), (wq.grad, dwq),
+                      (wk.grad, dwk), (o, ro)):
+        assert np.linalg.norm(f64(got) - want) <= 2.0 ** -6 * np.linalg.norm(want)
+
+
+def test_captured_training_step(ra):
+    T, Hq, Hkv, d = 130, 4, 2, 128
+    q, k, pos, wq, wk = case(T, Hq, Hkv, d, fused=False)
+    rotary = ra.Rotary(d)
+    leaves = [t.clone().requires_grad_() for t in (q, k, wq, wk)]
+    gq, gk = torch.randn_like(q), torch.randn_like(k)
+
+    def step():
+        torch.autograd.backward(ra.qk_norm_rope(leaves[0], leaves[1], pos, rotary, leaves[2], leaves[3]), (gq, gk))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    for t in leaves:
+        t.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(2):
+        with torch.no_grad():
+            leaves[0].mul_(1.5)
+            gk.neg_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ra.qk_norm_rope_bwd(*(t.detach() for t in leaves[:2]), gq, gk, pos, rotary, *(t.detach() for t in leaves[2:]))
+        for t, x in zip(leaves, want):
+            assert torch.equal(t.grad, x)
 
 
 def test_offsets_beyond_32_bits(ra):

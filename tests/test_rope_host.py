@@ -191,3 +191,15 @@ def test_slices_of_one_tensor_lie_beside_one_another(ra):
     assert "lies over" in lib.ra_last_error().decode()
     if not torch.cuda.is_available():                            # past every check: the device is missing
         assert lib.ra_qk_norm_rope_fwd(ctypes.addressof(c), *ok, None) == 3
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_a_lost_gradient_is_refused(ra, which):
+    rotary = ra.Rotary(64, device="cpu")
+    t = [torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.ones(64), torch.ones(64)]
+    t[which].requires_grad_()
+    pos = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="gradient"):
+        ra.qk_norm_rope_fwd(t[0], t[1], pos, rotary, t[2], t[3])
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+        ra.qk_norm_rope_fwd(t[0], t[1], pos, rotary, t[2], t[3])
