@@ -499,14 +499,16 @@ __global__ void __launch_bounds__(256) rope_dw_kernel(const float* partials, int
   }
 }
 
-// CTAs for this many tokens: a token's heads go to one warp (parts 0) where the tokens alone
-// fill the GPU, else each side's are shared out over some.
+// CTAs for this many tokens: a token's heads go to one warp (parts 0), or, of fewer tokens than a
+// quarter of the warps that run at once (912 forward, 608 backward), to several warps, each with the
+// token's angles to make.  Shared out / not, 40 heads of 128, us: forward 256 tokens 4.1 / 7.4, 760 6.4 / 7.6,
+// 1024 7.9 / 7.6, 3600 14.2 / 10.7; backward 256 tokens 7.8 / 11.0, 600 11.2 / 11.3, 1024 13.5 / 11.4.
 unsigned share_out(RopeParams& p, int D, int sms, int per_sm) {
   const int rows_at_once = 256 / D;
   const int64_t want = (int64_t)sms * per_sm * kWarps;  // warps that run at once
   int64_t items = p.T;
   p.parts[0] = p.parts[1] = 0;
-  if (p.T < want) {
+  if (4 * p.T < want) {
     const int g0 = (p.H[0] + rows_at_once - 1) / rows_at_once, g1 = (p.H[1] + rows_at_once - 1) / rows_at_once;
     const int64_t warps = std::max<int64_t>(2, want / std::max<int64_t>(1, p.T));
     const int per = (int)std::max<int64_t>(1, (g0 + g1 + warps - 1) / warps);  // rows (of 32 lanes) of a warp
