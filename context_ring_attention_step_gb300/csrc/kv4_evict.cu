@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(T, T == 512 ? 2 : 4) kv4_evict_kernel(const Kv
   const bool sane = L >= 0 && (long long)L <= min((long long)p.table_width << p.page_shift, (long long)kKv4MaxLength);
   if (!sane) code = RA_KV4_BAD_LENGTH;
   bool cut = sane && B >= 0 && (long long)L > (long long)B + p.slack;
-  if (cut && B < p.sinks + p.recent) {
+  if (cut && B < (long long)p.sinks + p.recent) {
     code = RA_KV4_BAD_BUDGET;
     cut = false;
   }
