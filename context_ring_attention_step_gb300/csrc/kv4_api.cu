@@ -79,14 +79,14 @@ int64_t few_rows(int32_t G, int32_t max_q_len) {
 }
 
 // The same for the weights of cached tokens: there the tile kernel's time hardly depends on the
-// rows up to 128 a request either.  8 key heads of head_dim 128 / 64 / 256, 8 requests of 8192 cached
+// rows up to 96 a request either.  8 key heads of head_dim 128 / 64 / 256, 8 requests of 8192 cached
 // tokens, us:
-//    32 rows   74 /  60 /  80 (tiles),  47 /  36 /  69 (few rows)
-//    48 rows   74 /  60 /  81 (tiles),  75 /  46 /  93 (few rows)
-//    64 rows   74 /  60 /  77 (tiles),  86 /  61 / 128 (few rows)
-//    96 rows   74 /  59 / 101 (tiles), 136 /  87 / 181 (few rows).
-// One request of 32768 crosses at 44 / 62 / 38 rows, 32 of 4096 at 70 / 86 / 52.
-constexpr int kWeightsTileRows = 64;
+//    32 rows   61 /  53 /  81 (tiles),  47 /  35 /  69 (few rows)
+//    40 rows   61 /  53 /  81 (tiles),  71 /  42 /  87 (few rows)
+//    48 rows   60 /  53 /  80 (tiles),  75 /  46 /  94 (few rows)
+//    64 rows   61 /  53 /  77 (tiles),  86 /  61 / 128 (few rows).
+// One request of 32768 crosses at 36 / 62 / 36 rows, 32 of 4096 at 41 / 66 / 52.
+constexpr int weights_tile_rows(int32_t D) { return D == 64 ? 64 : 40; }
 static_assert(2 * 256 * ra::kKv4MaxSms <= 2 * ra::kKv4MaxSms * 8 * (64 + 16), "attention's workspace holds the tile kernel's sums");
 
 struct AttnLayout {
@@ -379,9 +379,9 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
   p.partials = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + l.partials);
   const int32_t G = num_q_heads / Hkv;
   // (the tile kernel takes lse / scale in fp32)
-  const bool tiles = num_q_tokens > 0 && (int64_t)G * max_q_len >= kWeightsTileRows && p.scale >= 0x1p-60f && p.scale <= 0x1p60f;
+  const bool tiles = num_q_tokens > 0 && (int64_t)G * max_q_len >= weights_tile_rows(D) && p.scale >= 0x1p-60f && p.scale <= 0x1p60f;
   if (!tiles || num_requests > 1) {  // (a single long request is the tile kernel's, whatever its real length)
-    p.split_rows = tiles ? kWeightsTileRows : 0;
+    p.split_rows = tiles ? weights_tile_rows(D) : 0;
     e = ra::launch_kv4_weights(D, sms, w, st);
     if (e != cudaSuccess) return cuda_fail(e, "cache weights launch");
     p.status_kept = 1;

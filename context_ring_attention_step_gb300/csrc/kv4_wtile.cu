@@ -16,24 +16,26 @@
 // threads, a value for every column, they would cost four passes a warp for four columns, as much of
 // the bandwidth as all else.
 //
-// Warp roles (512 threads):
+// Warp roles (896 threads; at head_dim 256 512, with 8 warps for the sums and 4 for the keys):
 //   warps 0, 1    UMMA issuers of the two key tiles (warp 0 owns tensor memory): a wait costs one
 //                 of them 100 to 200 clocks even where nothing is to be waited for
 //   warp 2        the query tiles' log-sum-exps and key limits
 //   warp 3        TMA loads of query tiles
-//   warps 4-11    exponentials and sums: a thread is a key, at head_dim 256 and half of a tile's rows
-//   warps 12-15   cache -> bf16 keys: a thread is a key here too
+//   warps 4-19    exponentials and sums: a thread is a key and half of a tile's rows
+//   warps 20-27   cache -> bf16 keys: a thread is a key here too
 // Tensor memory (512 columns): the keys (D / 2 columns for 128 of them; at head_dim 256 those of two
 // units, 4 to 10 % faster), then a ring of S^T tiles.
 //
-// 1024 tokens x 32 query heads over 33792 cached, 8 key heads of 128: 254 us, 1100 TFLOP/s; tensor
-// cores are at work half of that and exponentials 46 %.  128 rows of queries against 256 keys cost 1154
-// clocks of the one, 1024 of the other, and about 2100 in all: a summing warp's 512 clocks of
-// exponentials begin when a tile is ready and its 128 columns have come, and two warps a scheduler,
-// whose tiles are ready at the same time, do not cover that.  (One issuer: 290 us; the issuers in
-// strict turns: 269, one behind the other's tile: 257; log-sum-exps from shared memory: 294; a tile in pieces
-// of 32 columns, each summed while the next comes: 298; tiles of 192 rows: 364.)  64 tokens over 32768:
-// 44 us, of which 13 are start, first keys and the merge of blocks whose heads lie in two CTAs.
+// 1024 tokens x 32 query heads over 33792 cached, 8 key heads of 128: 246 us, 1135 TFLOP/s; tensor
+// cores and exponentials are at work half of that.  128 rows of queries against 256 keys cost 1154
+// clocks of the one, 1024 of the other, and about 2050 in all: a summing warp waits for its tile and its
+// columns about as long as it sums them, and four warps a scheduler, whose tiles are ready at the same
+// time, do not cover that.  64 tokens over 32768: 41 us, of which 13 are start, first keys and the
+// merge of blocks whose heads lie in two CTAs; 32 requests of 4096, 512 rows a head: 193 us.
+// Measured on the way, the first call: one issuer 290 us, two 257; issuers in strict turns 269; log-sum-exps
+// from shared memory 294; tiles of 192 rows 364; a tile in pieces of 32 columns, each summed while the next
+// comes, 298.  With 8 summing and 4 expanding warps (168 and 104 registers) it took 254, the other two 44 and
+// 232; with 16 and 4 (72, 104; spills) 246, 47 and 215; other splits of the registers of 28 warps 250 to 343.
 // Items (block of keys, head) lie on one line that the CTAs cut evenly; of a block
 // whose heads went to several CTAs the one that brings the last sum adds them, in
 // the CTAs' order.
@@ -49,13 +51,14 @@
 namespace ra {
 namespace {
 
-constexpr int kSumWarps = 8;
-constexpr int kThreads = 32 * (8 + kSumWarps);
 constexpr int kExpandCost = 1;  // expanding a unit's keys, in query tiles
 constexpr int kLseStages = 4;
 
 template <int D>
 struct WTile {
+  static constexpr int kSumWarps = D == 256 ? 8 : 16;
+  static constexpr int kExpandWarps = D == 256 ? 4 : 8;
+  static constexpr int kThreads = 32 * (4 + kSumWarps + kExpandWarps);
   static constexpr int kKeyTiles = D == 256 ? 1 : 2;  // 128 keys each
   static constexpr int kKeys = 128 * kKeyTiles;
   static constexpr int kN = D == 256 ? 64 : 128;      // query rows of a tile
@@ -81,7 +84,8 @@ struct WTile {
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void keys_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSumWarps) : "memory"); }
+template <int kWarps>
+__device__ __forceinline__ void keys_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 // One token's keys of one head: the codes in order (8 dims a word), and the scales' bytes.
 template <int D>
@@ -209,10 +213,10 @@ struct Walk {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((WTile<D>::kThreads), 1)
 kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap tq) {
   using C = WTile<D>;
-  constexpr int N = C::kN, QS = C::kQStages, LS = kLseStages;
+  constexpr int N = C::kN, QS = C::kQStages, LS = kLseStages, kThreads = C::kThreads, kSumWarps = C::kSumWarps;
   const Kv4AttnParams& p = wp.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -305,9 +309,11 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
   if (bad) atomicMax(s_int + 1, bad);
   Walk<D> wk(wp, line, r0, base0);
 
-  // Register split: 512 threads x 128 at launch = 128 x 72 + 256 x 168 + 128 x 104.
+  // Register split: 896 threads x 72 at launch = 128 x 56 + 512 x 80 + 256 x 64; head_dim 256: 512 x 128 =
+  // 128 x 72 + 256 x 168 + 128 x 104.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp < C::kKeyTiles && lane == 0) {
       // ---------------------------------------------------------- MMA issuers
       const int kt = warp;
@@ -466,7 +472,8 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       }
     }
   } else if (warp < 4 + kSumWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
     // ------------------------------------------------------------ exponentials and sums
     constexpr int NC = C::kCols;
     const int gp = (warp - 4) >> 2, kt = gp % C::kKeyTiles, share = gp / C::kKeyTiles;
@@ -524,19 +531,15 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
           if (none) {
             release();
           } else {
-            uint32_t s[NC / 32][32];
+            uint32_t s[32];
 #pragma unroll
-            for (int c = 0; c < NC / 32; ++c) tmem_ld32(tS + sb * N + 32 * c, s[c]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < NC / 32; ++c) reg_fence32(s[c]);
-            release();
-            if (whole) {
-#pragma unroll
-              for (int c = 0; c < NC / 32; ++c) columns(s[c]);
-            } else {
-#pragma unroll
-              for (int c = 0; c < NC / 32; ++c) masked_columns(s[c], lim + 8 * c, key);
+            for (int c = 0; c < NC / 32; ++c) {
+              tmem_ld32(tS + sb * N + 32 * c, s);
+              tmem_ld_wait();
+              reg_fence32(s);
+              if (c == NC / 32 - 1) release();
+              if (whole) columns(s);
+              else masked_columns(s, lim + 8 * c, key);
             }
           }
           __syncwarp();
@@ -554,9 +557,9 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
         const bool owner = share == 0;
         if (C::kShares > 1) {
           float* others = reinterpret_cast<float*>(smem + C::kPartOff);
-          keys_sync();  // (they were read)
+          keys_sync<kSumWarps>();  // (they were read)
           if (!owner) others[(share - 1) * C::kKeys + key_t] = acc;
-          keys_sync();
+          keys_sync<kSumWarps>();
 #pragma unroll
           for (int i = 1; i < C::kShares; ++i)
             if (owner) total += others[(i - 1) * C::kKeys + key_t];
@@ -577,15 +580,15 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
           const int me = blockIdx.x;
           if (owner) p.partials[(size_t)(2 * me + (me == c0 ? 1 : 0)) * C::kKeys + key_t] = total;
           __threadfence();
-          keys_sync();
+          keys_sync<kSumWarps>();
           if (tid == 128) {
             int* ticket = p.tickets + 2 * c0 + 1;
             s_int[2] = atomicAdd(ticket, 1) == parts - 1;
             if (s_int[2]) *ticket = 0;  // as the next call expects it
           }
-          keys_sync();
+          keys_sync<kSumWarps>();
           writes = s_int[2];
-          keys_sync();
+          keys_sync<kSumWarps>();
           if (writes) {
             __threadfence();
             total = 0.f;
@@ -606,11 +609,13 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
     }
     if (bad) atomicMax(s_int + 1, bad);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ------------------------------------------------------------ expansion
     // Key tile by key tile: while one is expanded for the next head, the products of this
     // head's last query tile go on with the other.
-    constexpr int kT = C::kKeyTiles;
+    constexpr int kGroups = C::kExpandWarps / 4, kT = C::kKeyTiles / kGroups;
+    const int kt0 = kGroups == 1 ? 0 : (warp - 4 - kSumWarps) >> 2;
     const int row = 32 * (warp & 3) + lane;  // key of a key tile
     const uint32_t tK = tmem_addr(tmem, (uint32_t)(warp & 3) * 32, 0);
     uint32_t item = 0;
@@ -629,11 +634,11 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
       // page of this thread's key of a block's key tile, and that key's words of one head; where there is
       // none (no page of the cache, behind the last key) whatever was there: its sum is not used
       auto page_of = [&](int kt, int blk) -> int {
-        const int t = blk * C::kKeys + 128 * kt + row;
+        const int t = blk * C::kKeys + 128 * (kt0 + kt) + row;
         return t < rq.L ? table[t >> p.cache.page_shift] : -1;
       };
       auto fetch = [&](KeyWords<D>& w, int kt, int blk, int head, int page) {
-        const int t = (blk * C::kKeys + 128 * kt + row) & (P - 1);
+        const int t = (blk * C::kKeys + 128 * (kt0 + kt) + row) & (P - 1);
         if ((uint32_t)page < (uint64_t)p.cache.num_pages)
           load_key<D>(w, p.cache.pages + kv4_tile_offset<D>(p.cache, page, head, t), t & 15);
       };
@@ -658,14 +663,14 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
 #pragma unroll
         for (int kt = 0; kt < kT; ++kt) {
           const uint32_t set = item % C::kSets;
-          if (ok) ok = mbar_wait(b_kempty + 8 * (kt + set), ((item / C::kSets) & 1) ^ 1, ab, 167);
+          if (ok) ok = mbar_wait(b_kempty + 8 * (kt0 + kt + set), ((item / C::kSets) & 1) ^ 1, ab, 167);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
-          expand_key<D>(tK + (kt + set) * C::kKCols, k[kt]);
+          expand_key<D>(tK + (kt0 + kt + set) * C::kKCols, k[kt]);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(b_kfull + 8 * (kt + set));
+          if (lane == 0) mbar_arrive(b_kfull + 8 * (kt0 + kt + set));
           if (x + 1 < wk.x1) fetch(k[kt], kt, blk, head, page[kt]);
         }
       }
@@ -686,7 +691,7 @@ cudaError_t launch(int ctas, const Kv4WeightsParams& p, const CUtensorMap& tq, c
   auto kern = kv4_wtile_kernel<D>;
   static Kv4SmemLimit limit;
   return limit.launch(reinterpret_cast<const void*>(kern), WTile<D>::kSmem, [&] {
-    kern<<<ctas, kThreads, WTile<D>::kSmem, stream>>>(p, tq);
+    kern<<<ctas, WTile<D>::kThreads, WTile<D>::kSmem, stream>>>(p, tq);
     return cudaGetLastError();
   });
 }
