@@ -334,12 +334,16 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
 #pragma unroll
         for (int u = 0; u < U; ++u) fwd_row<D, kInter>(p, ln, v[u], ca, sa, y + u * RPW * D, true);
       }
-#pragma unroll 1
-      for (; h < n; h += RPW, x += RPW * D, y += RPW * D) {
-        Vec<false> v;
-        v.clear();
-        if (h + row < n) v.load(x, db);
-        fwd_row<D, kInter>(p, ln, v, ca, sa, y, h + row < n);
+      if (h < n) {  // the last ones, on the way together too (one after the other, 7 + 1 heads took 101 us for 75)
+        Vec<false> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          v[u].clear();
+          if (h + u * RPW + row < n) v[u].load(x + u * RPW * D, db);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (h + u * RPW < n) fwd_row<D, kInter>(p, ln, v[u], ca, sa, y + u * RPW * D, h + u * RPW + row < n);
       }
     }
   }
@@ -451,16 +455,22 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) rope_bwd_kernel(const Rope
         for (int u = 0; u < U; ++u)
           bwd_row<D, kInter, kFp32, kNorm>(p, ln, v[u], gv[u], cs, sn, w, dw, y + u * RPW * D, true);
       }
-#pragma unroll 1
-      for (; h < n; h += RPW, x += RPW * D, g += RPW * D, y += RPW * D) {
-        const bool in = h + row < n;
-        Vec<false> v;
-        Vec<kFp32> gv;
-        v.clear();
-        gv.clear();
-        if (in && kNorm) v.load(x, db);
-        if (in) gv.load(g, db);
-        bwd_row<D, kInter, kFp32, kNorm>(p, ln, v, gv, cs, sn, w, dw, y, in);
+      if (h < n) {  // the last ones
+        Vec<false> v[U];
+        Vec<kFp32> gv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          v[u].clear();
+          gv[u].clear();
+          if (h + u * RPW + row < n) {
+            if (kNorm) v[u].load(x + u * RPW * D, db);
+            gv[u].load(g + u * RPW * D, db);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (h + u * RPW < n)
+            bwd_row<D, kInter, kFp32, kNorm>(p, ln, v[u], gv[u], cs, sn, w, dw, y + u * RPW * D, h + u * RPW + row < n);
       }
       if (kNorm) {
 #pragma unroll
