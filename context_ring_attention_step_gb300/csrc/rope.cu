@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) rope_fwd_kernel(const Rope
 #pragma unroll
         for (int u = 0; u < U; ++u) fwd_row<D, kInter>(p, ln, v[u], ca, sa, y + u * RPW * D, true);
       }
-      if (h < n) {  // the last ones, on the way together too (one after the other, 7 + 1 heads took 101 us for 75)
+      if (h < n) {  // the last ones, on the way together too (one after the other, 7 + 1 heads took 101 us for 77)
         Vec<false> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
