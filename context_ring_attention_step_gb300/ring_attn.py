@@ -351,6 +351,30 @@ def ring_attn_bwd(q, k, v, o, do, lse, cu_seqlens, cp_size, layout="zigzag", cau
     return dq, dk, dv
 
 
+class _FirstOrder(torch.autograd.Function):
+    """Gradients that a kernel computed, as results of the tensors they depend on; their own derivative is an error."""
+
+    @staticmethod
+    def forward(ctx, name, grads, *inputs):
+        ctx.name = name
+        return grads
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("%s has no second derivative" % ctx.name)
+
+
+def first_order(name, grads, *inputs):
+    """What a backward pass returns: ``grads``, computed from ``inputs`` by a kernel.
+
+    To autograd they would be constants.  Where it records the backward pass (create_graph)
+    they are marked, so that a second derivative raises in place of losing a term.  (PyTorch's
+    once_differentiable looks at the incoming gradients alone: behind a loss that is linear in the
+    results, whose gradients are constants, it marks nothing.)
+    """
+    return _FirstOrder.apply(name, grads, *inputs) if torch.is_grad_enabled() else grads
+
+
 class RingAttention(torch.autograd.Function):
     """Autograd wrapper: the forward runs ring_attn_fwd and saves (q, k, v, o,
     lse); the backward runs ring_attn_bwd from the saved LSE.  Gradients flow

@@ -201,7 +201,9 @@ def qk_norm_rope_bwd(q, k, gq, gk, positions, rotary, q_weight=None, k_weight=No
 
 
 class QkNormRope(torch.autograd.Function):
-    """Autograd wrapper: saves the inputs and runs qk_norm_rope_bwd.  Use ``qk_norm_rope(...)``."""
+    """Autograd wrapper: saves the inputs and runs qk_norm_rope_bwd.  Use ``qk_norm_rope(...)``.
+
+    The kernels' gradients are constants to autograd, so a second derivative is an error."""
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, positions, rotary, eps):
@@ -213,11 +215,13 @@ class QkNormRope(torch.autograd.Function):
     def backward(ctx, gq, gk):
         q, k, q_weight, k_weight, positions = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dq, dk, dqw, dkw = qk_norm_rope_bwd(q, k, gq.contiguous(), gk.contiguous(), positions, ctx.rotary, q_weight,
-                                            k_weight, ctx.eps, weight_grads=need[2] or need[3])
-        cast = lambda g, w, n: g.to(w.dtype) if n and g is not None else None  # noqa: E731
-        return (dq if need[0] else None, dk if need[1] else None, cast(dqw, q_weight, need[2]),
-                cast(dkw, k_weight, need[3]), None, None, None)
+        with torch.no_grad():
+            dq, dk, dqw, dkw = qk_norm_rope_bwd(q, k, gq.contiguous(), gk.contiguous(), positions, ctx.rotary, q_weight,
+                                                k_weight, ctx.eps, weight_grads=need[2] or need[3])
+            cast = lambda g, w, n: g.to(w.dtype) if n and g is not None else None  # noqa: E731
+            grads = (dq if need[0] else None, dk if need[1] else None, cast(dqw, q_weight, need[2]),
+                     cast(dkw, k_weight, need[3]))
+        return _ra.first_order("qk_norm_rope", grads, gq, gk, q, k, q_weight, k_weight) + (None, None, None)
 
 
 def qk_norm_rope(q, k, positions, rotary, q_weight=None, k_weight=None, eps=1e-6):

@@ -1,6 +1,7 @@
 """Norms with rotation without a GPU: the oracle's own pins, the frequencies' table, and what the calls refuse."""
 
 import ctypes
+import sys
 
 import numpy as np
 import pytest
@@ -203,3 +204,39 @@ def test_a_lost_gradient_is_refused(ra, which):
         ra.qk_norm_rope_fwd(t[0], t[1], pos, rotary, t[2], t[3])
     with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
         ra.qk_norm_rope_fwd(t[0], t[1], pos, rotary, t[2], t[3])
+
+
+# ------------------------------------------------------------------ second derivatives
+
+def _stand_ins(ra, monkeypatch):
+    """y = x^2 on the CPU in place of the two kernels; the weights count for nothing."""
+    mod = sys.modules[ra.QkNormRope.__module__]
+    monkeypatch.setattr(mod, "qk_norm_rope_fwd", lambda q, k, *a, **kw: (q * q, k * k))
+    monkeypatch.setattr(mod, "qk_norm_rope_bwd",
+                        lambda q, k, gq, gk, *a, **kw: ((2 * q * gq).detach(), (2 * k * gk).detach(), None, None))
+
+
+@pytest.mark.parametrize("linear", [False, True])
+def test_a_second_derivative_is_an_error(ra, monkeypatch, linear):
+    """Kernels' gradients are constants to autograd: what would lose the rest of a second derivative raises,
+    behind a loss that is linear in the results (their gradients are constants) too."""
+    _stand_ins(ra, monkeypatch)
+    q, k = (torch.full((2, 1, 64), v, requires_grad=True) for v in (1.5, 2.0))
+    y, z = ra.qk_norm_rope(q, k, torch.zeros(2, dtype=torch.int32), None)
+    loss = y.sum() + z.sum() if linear else (y * q).sum() + (z * k).sum()
+    grads = torch.autograd.grad(loss, (q, k), create_graph=True)
+    for g, x in zip(grads, (q, k)):
+        assert torch.equal(g, (2 if linear else 3 * x) * x)
+        with pytest.raises(RuntimeError, match="qk_norm_rope has no second derivative"):
+            torch.autograd.grad((g * g).sum() + (x * x).sum(), x, retain_graph=True)
+
+
+def test_gradients_of_frozen_inputs(ra, monkeypatch):
+    """With create_graph and without: the first derivative is the same, beside inputs that need none."""
+    _stand_ins(ra, monkeypatch)
+    for create in (False, True):
+        q, k = torch.full((2, 1, 64), 1.5, requires_grad=True), torch.full((2, 1, 64), 2.0)
+        w = torch.ones(64, requires_grad=True)
+        y, z = ra.qk_norm_rope(q, k, torch.zeros(2, dtype=torch.int32), None, w, None)
+        dq, = torch.autograd.grad(y.sum(), q, create_graph=create)
+        assert torch.equal(dq, 2 * q) and dq.requires_grad is create
