@@ -378,7 +378,8 @@ def first_order(name, grads, *inputs):
 class RingAttention(torch.autograd.Function):
     """Autograd wrapper: the forward runs ring_attn_fwd and saves (q, k, v, o,
     lse); the backward runs ring_attn_bwd from the saved LSE.  Gradients flow
-    to q, k and v only.  Use ``ring_attention(...)``."""
+    to q, k and v only, and have no derivative of their own (an error under
+    create_graph).  Use ``ring_attention(...)``."""
 
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, cp_size, layout, causal, scale, plan):
@@ -392,9 +393,10 @@ class RingAttention(torch.autograd.Function):
     def backward(ctx, do, _dlse):
         q, k, v, o, lse = ctx.saved_tensors
         cu_seqlens, cp_size, layout, causal, scale, plan = ctx.args
-        dq, dk, dv = ring_attn_bwd(q, k, v, o, do.contiguous().to(torch.bfloat16), lse, cu_seqlens, cp_size,
-                                   layout, causal, scale, plan=plan)
-        return dq, dk, dv, None, None, None, None, None, None
+        with torch.no_grad():
+            grads = ring_attn_bwd(q, k, v, o, do.contiguous().to(torch.bfloat16), lse, cu_seqlens, cp_size,
+                                  layout, causal, scale, plan=plan)
+        return first_order("ring_attention", grads, do, q, k, v) + (None,) * 6
 
 
 def ring_attention(q, k, v, cu_seqlens, cp_size, layout="zigzag", causal=True, scale=None, plan=None):

@@ -348,3 +348,25 @@ def test_kernel_source_hash_ignores_comments_only():
     assert bench.strip_comments(a) == bench.strip_comments(b)
     assert bench.strip_comments(a) != bench.strip_comments(c)
     assert len(bench.kernel_source_hash("ring_bwd_step_kernel")) == 16
+
+
+@pytest.mark.parametrize("linear", [False, True])
+def test_a_second_derivative_is_an_error(ra, monkeypatch, linear):
+    """ring_attention's gradients are constants to autograd: a second derivative raises in place of losing a term."""
+    import sys
+
+    import torch
+    mod = sys.modules[ra.RingAttention.__module__]
+    monkeypatch.setattr(mod, "ring_attn_fwd", lambda q, k, v, *a, **kw: (q * k * v, q[..., 0].float().t().contiguous()))
+    monkeypatch.setattr(mod, "ring_attn_bwd",
+                        lambda q, k, v, o, do, *a, **kw: tuple(x.detach() for x in (do * k * v, do * q * v, do * q * k)))
+    leaves = [torch.full((4, 2, 64), x, dtype=torch.bfloat16).requires_grad_() for x in (1.0, 2.0, 4.0)]
+    plan = ra.Plan([0, 4], 1, "zigzag", True, 2, 2, 64)
+    o, lse = ra.ring_attention(*leaves, [0, 4], 1, plan=plan)
+    assert not lse.requires_grad
+    grads = torch.autograd.grad(o.sum() if linear else (o * o).sum(), leaves, create_graph=True)
+    scale = 1.0 if linear else 16.0
+    for g, x, want in zip(grads, leaves, (8.0, 4.0, 2.0)):
+        assert torch.all(g == scale * want)
+        with pytest.raises(RuntimeError, match="ring_attention has no second derivative"):
+            torch.autograd.grad((g * g).sum() + (x * x).sum(), x, retain_graph=True)
