@@ -165,8 +165,11 @@ def qk_norm_rope_bwd(q, k, gq, gk, positions, rotary, q_weight=None, k_weight=No
     ``gq``, ``gk``: both bf16 or both fp32, rows may be strided.  dq, dk are bf16
     (``out=(dq, dk)``: caller-owned, rows may be strided, e.g. slices of a fused
     projection's gradient); the weights' are fp32 [d], None where there is no
-    weight or ``weight_grads`` is false.
+    weight or ``weight_grads`` is false.  No gradient flows through it, and q, k, gq and
+    gk that would need one are refused (the weights may be parameters).
     """
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or gq.requires_grad or gk.requires_grad):
+        raise ValueError("qk_norm_rope_bwd has no gradient: call it under torch.no_grad()")
     c, T, Hq, Hkv, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
     D = rotary.head_dim
     qp, qs = _strided("q", q, T, Hq, D, _BF16, dev)

@@ -240,3 +240,18 @@ def test_gradients_of_frozen_inputs(ra, monkeypatch):
         y, z = ra.qk_norm_rope(q, k, torch.zeros(2, dtype=torch.int32), None, w, None)
         dq, = torch.autograd.grad(y.sum(), q, create_graph=create)
         assert torch.equal(dq, 2 * q) and dq.requires_grad is create
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_a_lost_gradient_of_the_gradients_is_refused(ra, which):
+    rotary, pos = ra.Rotary(64, device="cpu"), torch.zeros(2, dtype=torch.int32)
+    t = [torch.zeros(2, 1, 64, dtype=torch.bfloat16) for _ in range(4)]
+    w = torch.ones(64, requires_grad=True)                       # (a parameter as it is)
+    t[which].requires_grad_()
+    with pytest.raises(ValueError, match="no gradient"):
+        ra.qk_norm_rope_bwd(*t, pos, rotary, w, w)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
+        ra.qk_norm_rope_bwd(*t, pos, rotary, w, w)
+    t[which] = t[which].detach()
+    with pytest.raises(ValueError, match="GPU"):
+        ra.qk_norm_rope_bwd(*t, pos, rotary, w, w)
