@@ -265,6 +265,8 @@ def kv4_attention(q, cache, block_table, kv_lens, cu_q, causal=True, scale=None,
     lib = _library()
     if q.requires_grad and torch.is_grad_enabled():
         raise ValueError("kv4_attention has no gradient: call it under torch.no_grad()")
+    if _ra.has_tangent(q):
+        raise ValueError("kv4_attention has no forward-mode derivative: call it on tensors without tangents")
     dev, R = cache.device, kv_lens.shape[0]
     if q.dim() != 3:
         raise ValueError("q has shape %s, expected [T, heads, %d]" % (tuple(q.shape), cache.head_dim))
@@ -310,6 +312,8 @@ def kv4_weights(q, cache, block_table, kv_lens, cu_q, lse, weights, new_lens=Non
     lib = _library()
     if q.requires_grad and torch.is_grad_enabled():
         raise ValueError("kv4_weights has no gradient: call it under torch.no_grad()")
+    if _ra.has_tangent(q, lse, weights):
+        raise ValueError("kv4_weights has no forward-mode derivative: call it on tensors without tangents")
     dev, R = cache.device, kv_lens.shape[0]
     if q.dim() != 3:
         raise ValueError("q has shape %s, expected [T, heads, %d]" % (tuple(q.shape), cache.head_dim))

@@ -12,6 +12,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import build as _build
 
@@ -373,6 +374,12 @@ def first_order(name, grads, *inputs):
     results, whose gradients are constants, it marks nothing.)
     """
     return _FirstOrder.apply(name, grads, *inputs) if torch.is_grad_enabled() else grads
+
+
+def has_tangent(*tensors):
+    """Does one of them (or None) carry a tangent of forward-mode differentiation?  A kernel would drop it."""
+    return _forward_ad._current_level >= 0 and any(t is not None and _forward_ad.unpack_dual(t).tangent is not None
+                                                   for t in tensors)
 
 
 class RingAttention(torch.autograd.Function):

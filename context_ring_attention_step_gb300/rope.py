@@ -137,6 +137,8 @@ def qk_norm_rope_fwd(q, k, positions, rotary, q_weight=None, k_weight=None, eps=
     """
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or _trained(q_weight) or _trained(k_weight)):
         raise ValueError("qk_norm_rope_fwd has no gradient: call qk_norm_rope, or this under torch.no_grad()")
+    if _ra.has_tangent(q, k, q_weight, k_weight):
+        raise ValueError("qk_norm_rope_fwd has no forward-mode derivative: call it on tensors without tangents")
     c, T, Hq, Hkv, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
     D = rotary.head_dim
     qp, qs = _strided("q", q, T, Hq, D, _BF16, dev)
@@ -170,6 +172,8 @@ def qk_norm_rope_bwd(q, k, gq, gk, positions, rotary, q_weight=None, k_weight=No
     """
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or gq.requires_grad or gk.requires_grad):
         raise ValueError("qk_norm_rope_bwd has no gradient: call it under torch.no_grad()")
+    if _ra.has_tangent(q, k, gq, gk, q_weight, k_weight):
+        raise ValueError("qk_norm_rope_bwd has no forward-mode derivative: call it on tensors without tangents")
     c, T, Hq, Hkv, dev = _shape_of(q, k, positions, rotary, q_weight, k_weight, eps)
     D = rotary.head_dim
     qp, qs = _strided("q", q, T, Hq, D, _BF16, dev)

@@ -255,3 +255,26 @@ def test_a_lost_gradient_of_the_gradients_is_refused(ra, which):
     t[which] = t[which].detach()
     with pytest.raises(ValueError, match="GPU"):
         ra.qk_norm_rope_bwd(*t, pos, rotary, w, w)
+
+
+def test_a_lost_tangent_is_refused(ra, monkeypatch):
+    """Forward-mode differentiation: tensors with a tangent need no gradient, and the kernels would drop it."""
+    from torch.autograd import forward_ad
+    rotary, pos = ra.Rotary(64, device="cpu"), torch.zeros(2, dtype=torch.int32)
+    x, w = torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.ones(64)
+    cache, i32 = ra.Kv4Cache(4, 64, 1, 64, device="cpu"), lambda n: torch.zeros(n, dtype=torch.int32)
+    tables, lse, sums = (torch.zeros(1, 4, dtype=torch.int32), i32(1), i32(2)), torch.zeros(1, 2), torch.zeros(256)
+    with forward_ad.dual_level():
+        with pytest.raises(ValueError, match="GPU"):             # no tangent: on to the other checks
+            ra.qk_norm_rope_fwd(x, x, pos, rotary, w, w)
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call, args, at in ((ra.qk_norm_rope_fwd, (x, x, pos, rotary, w, w), (0, 1, 4, 5)),
+                               (ra.qk_norm_rope_bwd, (x, x, x, x, pos, rotary, w, w), (0, 1, 2, 3, 6, 7)),
+                               (ra.kv4_attention, (x, cache) + tables, (0,)),
+                               (ra.kv4_weights, (x, cache) + tables + (lse, sums), (0, 5, 6))):
+            for i in at:
+                with pytest.raises(ValueError, match="forward-mode"):
+                    call(*[dual(a) if j == i else a for j, a in enumerate(args)])
+        _stand_ins(ra, monkeypatch)
+        with pytest.raises(RuntimeError):                        # the differentiable call has no rule for it
+            ra.qk_norm_rope(dual(x), x, pos, None)
