@@ -110,6 +110,11 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 // squares comes near its ends (the lower one matters only beside an eps that small) are
 // scaled by a power of two first.
 __device__ __forceinline__ bool far_out(float ss, float eps) { return !(ss <= 0x1p120f) || (ss < 0x1p-80f && eps < 0x1p-60f); }
+// Likewise the sum of h w x (backward): above, products leave the range; below, what was lost of them shows
+// beside h w, where the eps is small enough for the row to count at all.
+__device__ __forceinline__ bool products_far_out(float dot, float eps) {
+  return !(fabsf(dot) <= 0x1p120f) || (fabsf(dot) < 0x1p-90f && eps < 0x1p-30f);
+}
 // The inverse of the power of two that brings the row's largest magnitude (fp32 bits) to
 // [1, 2); 1 for a row that is zero or not finite.  At most 2^60 beside an eps, which is far
 // above the squares then and must not overflow when it is scaled along.
@@ -371,21 +376,28 @@ __device__ __forceinline__ void bwd_row(const RopeParams& p, const Lane<D, kInte
       for (int i = 1; i < 4; ++i) s = f2_fma(hw[i], x[i], s);
       return f2_sum(s);
     };
-    float ss = row_sum<D>(square_sum(x)), dot = row_sum<D>(product()), e = p.eps, down = 1.f;
-    const bool far = in && far_out(ss, p.eps);
+    float ss = row_sum<D>(square_sum(x)), dot = row_sum<D>(product()), e = p.eps, up = 1.f;
+    const bool far = in && (far_out(ss, p.eps) || products_far_out(dot, p.eps));
     if (__any_sync(0xffffffffu, far)) {
-      // as forward: r is the scaled row's then, and r x that of the row itself
-      down = scale_row<D>(x, p.eps, far);
+      // as forward: r is the scaled row's then, and r times the power of two that of the row itself.  h w takes
+      // the power, of one above 2^63 that much, and at most 2^-16 where the sum was large; r takes the rest
+      const float down = scale_row<D>(x, p.eps, far);
+      if (far) {
+        const float take = fminf(down, fabsf(dot) <= 0x1p100f ? 0x1p63f : 0x1p-16f);
+        e = p.eps * down * down;
+        up = down / take;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hw[i] = f2_mul(hw[i], f2_both(take));
+      }
       const float s2 = row_sum<D>(square_sum(x)), d2 = row_sum<D>(product());
       if (far) {
         ss = s2;
         dot = d2;
-        e = p.eps * down * down;
       }
     }
     const float r = rsqrtf(fmaf(ss, 1.f / D, e));
     const float mean = dot * r * (1.f / D);  // of h w r x
-    const uint64_t r2 = f2_both(r), m2 = f2_both(-mean), rd = f2_both(r * down);
+    const uint64_t r2 = f2_both(r), m2 = f2_both(-mean), rd = f2_both(r * up);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint64_t n = f2_mul(x[i], r2);

@@ -208,6 +208,36 @@ def test_rows_at_the_ends_of_the_number_range(ra):
     assert torch.isinf(y[0, 0, 100]) and torch.isfinite(y[0, 0, :100]).all()
 
 
+@pytest.mark.parametrize("gt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_gradients_at_the_ends_of_the_number_range(ra, d, gt):
+    """Rows and gradients whose products leave fp32's range although the results are inside it.
+
+    The tolerance is the one above.  Products of h w and x that fall below 2^-126 are off by at most
+    2^-150 each, d of them together by r 2^-150 in the mean: less than 2^-18 of h w = 2^-112 where r <= 2^20
+    (eps 1e-6, 1e-22 with its rows scaled), and rows whose sum is below 2^-90 beside a smaller eps are scaled."""
+    powers = [(56, 75), (56, 118), (0, 118), (0, -112), (-39, -112), (-39, 100), (-60, -112), (-120, -100), (-130, -100),
+              (100, 118), (120, 118), (120, -10), (30, 60), (-20, -112)]
+    n, rotary, freq = len(powers), ra.Rotary(d), O.frequencies(d, 10000.0)
+    g = torch.Generator().manual_seed(d)
+    scale = [torch.tensor([2.0 ** p[i] for p in powers], dtype=torch.float64).view(n, 1, 1) for i in range(2)]
+    x = (torch.randn(n, 1, d, generator=g) * scale[0]).to(torch.bfloat16).cuda()
+    gy = (torch.randn(n, 1, d, generator=g) * scale[1]).to(gt).cuda()
+    pos = torch.arange(n, dtype=torch.int32).cuda()
+    w = (1 + 0.1 * torch.randn(d, generator=g)).cuda()
+    for eps, fit in ((1e-6, 14), (1e-22, 13), (0.0, 13)):
+        want, _ = O.backward(f64(x), f64(gy), pos.cpu().numpy(), freq, False, f64(w), eps)
+        rows = (np.abs(want) < 2.0 ** 126).all(axis=(1, 2))      # (the others have no bf16 number, or the last few)
+        assert rows.sum() == fit
+        dx, _, _, _ = ra.qk_norm_rope_bwd(x, x.clone(), gy, gy.clone(), pos, rotary, w, w, eps=eps)
+        check_bwd(dx[rows], None, x[rows], gy[rows], pos[rows], freq, False, w, eps)
+        for i in rows.nonzero()[0]:                              # the weights' gradients of each row alone
+            one = slice(i, i + 1)
+            dx1, _, dw, _ = ra.qk_norm_rope_bwd(x[one], x[one].clone(), gy[one], gy[one].clone(), pos[one], rotary, w, w, eps=eps)
+            assert torch.equal(dx1, dx[one])
+            check_bwd(dx1, dw, x[one], gy[one], pos[one], freq, False, w, eps)
+
+
 def test_negative_positions_are_no_tokens(ra):
     q, k, pos, wq, wk = case(60, 4, 2, 128, far=False)
     q[3] = float("nan")
