@@ -167,7 +167,8 @@ def qk_norm_rope_bwd(q, k, gq, gk, positions, rotary, q_weight=None, k_weight=No
     ``gq``, ``gk``: both bf16 or both fp32, rows may be strided.  dq, dk are bf16
     (``out=(dq, dk)``: caller-owned, rows may be strided, e.g. slices of a fused
     projection's gradient); the weights' are fp32 [d], None where there is no
-    weight or ``weight_grads`` is false.  No gradient flows through it, and q, k, gq and
+    weight or ``weight_grads`` is false (``out=(dq, dk, dq_weight, dk_weight)``:
+    caller-owned too, None for those that are not).  No gradient flows through it, and q, k, gq and
     gk that would need one are refused (the weights may be parameters).
     """
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or gq.requires_grad or gk.requires_grad):
@@ -185,18 +186,22 @@ def qk_norm_rope_bwd(q, k, gq, gk, positions, rotary, q_weight=None, k_weight=No
     gkp, gks = _strided("gk", gk, T, Hkv, D, gt, dev)
     if out is None:
         out = torch.empty((T, Hq, D), dtype=_BF16, device=dev), torch.empty((T, Hkv, D), dtype=_BF16, device=dev)
-    dq, dk = out
+    dq, dk, dqw, dkw = out if len(out) == 4 else (*out, None, None)
     dqp, dqs = _strided("dq", dq, T, Hq, D, _BF16, dev)
     dkp, dks = _strided("dk", dk, T, Hkv, D, _BF16, dev)
-    dqw = dkw = None
+    if (dqw is not None and (q_weight is None or not weight_grads)) or (
+            dkw is not None and (k_weight is None or not weight_grads)):
+        raise ValueError("out holds the gradient of a weight that is not there or not asked for")
     dqwp = dkwp = ws = ws_bytes = 0
     if weight_grads and not (q_weight is None and k_weight is None):
         if q_weight is not None:
-            dqw = torch.empty(D, dtype=_F32, device=dev)
-            dqwp = dqw.data_ptr()
+            if dqw is None:
+                dqw = torch.empty(D, dtype=_F32, device=dev)
+            dqwp = _array("dq_weight", dqw, (D,), _F32, dev)
         if k_weight is not None:
-            dkw = torch.empty(D, dtype=_F32, device=dev)
-            dkwp = dkw.data_ptr()
+            if dkw is None:
+                dkw = torch.empty(D, dtype=_F32, device=dev)
+            dkwp = _array("dk_weight", dkw, (D,), _F32, dev)
         if workspace is None:
             workspace = qk_norm_rope_workspace(D, dev)
         elif workspace.device != dev or not workspace.is_contiguous():

@@ -289,6 +289,33 @@ def test_in_place_and_into_slices(ra):
     assert torch.all(dqkv[:, Hq + Hkv:] == 7.0)
 
 
+def test_caller_owned_outputs_allocate_nothing(ra):
+    T, Hq, Hkv, d = 91, 6, 2, 128
+    q, k, pos, wq, wk = case(T, Hq, Hkv, d)
+    rotary, ws = ra.Rotary(d), ra.qk_norm_rope_workspace(d)
+    y = ra.qk_norm_rope_fwd(q, k, pos, rotary, wq, wk)
+    want = ra.qk_norm_rope_bwd(q, k, *y, pos, rotary, wq, wk)
+    fwd, bwd = tuple(map(torch.empty_like, y)), tuple(map(torch.empty_like, want))
+    count = lambda: torch.cuda.memory_stats()["allocation.all.allocated"]  # noqa: E731
+    before = count()
+    ra.qk_norm_rope_fwd(q, k, pos, rotary, wq, wk, out=fwd)
+    got = ra.qk_norm_rope_bwd(q, k, *y, pos, rotary, wq, wk, workspace=ws, out=bwd)
+    assert count() == before
+    assert all(a is b for a, b in zip(got, bwd)) and all(map(torch.equal, got + fwd, want + y))
+    some = ra.qk_norm_rope_bwd(q, k, *y, pos, rotary, wq, wk, out=bwd[:2] + (None, bwd[3].zero_()))
+    assert some[3] is bwd[3] and all(map(torch.equal, some, want))
+    for kw, word in ((dict(out=bwd[:2] + (bwd[2].bfloat16(), None)), "dq_weight has dtype"),
+                     (dict(out=bwd[:3] + (torch.empty(2 * d).cuda()[::2],)), "dk_weight must be contiguous"),
+                     (dict(out=bwd, weight_grads=False), "not asked for"),
+                     (dict(out=bwd[:2] + (torch.empty(64).cuda(), None)), "dq_weight has shape")):
+        with pytest.raises(ValueError, match=word):
+            ra.qk_norm_rope_bwd(q, k, *y, pos, rotary, wq, wk, workspace=ws, **kw)
+    with pytest.raises(ValueError, match="not there"):
+        ra.qk_norm_rope_bwd(q, k, *y, pos, rotary, wq, None, workspace=ws, out=bwd)
+    with pytest.raises(ra.RingAttnError, match="lies over"):
+        ra.qk_norm_rope_bwd(q, k, *y, pos, rotary, wq, wk, workspace=ws, out=bwd[:3] + (bwd[2],))
+
+
 def test_autograd(ra):
     T, Hq, Hkv, d = 70, 4, 2, 64
     q, k, pos, wq, wk = case(T, Hq, Hkv, d, w=torch.bfloat16, far=False)
