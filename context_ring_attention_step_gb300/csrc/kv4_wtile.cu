@@ -352,10 +352,10 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
           if (ok) umma_commit(b_kempty + 8 * (kt + set));
         }
       }
-      if (!ok) {  // let issued MMAs finish before tensor memory is released
-        umma_commit(b_drain + 8 * kt);
-        mbar_wait_drain(b_drain + 8 * kt, 0);
-      }
+      // Issued MMAs finish before tensor memory is released, and copies land before the CTA's shared memory is
+      // given up (below), also where only another role gave a wait up; without that they have by now.
+      umma_commit(b_drain + 8 * kt);
+      mbar_wait_drain(b_drain + 8 * kt, 0);
     } else if (warp == 3 && lane == 0) {
       // ---------------------------------------------------------- query tiles
       const uint32_t bytes = (uint32_t)(tl.tokens * (tl.per_token > 1 ? N : G)) * D * 2;
@@ -381,8 +381,7 @@ kv4_wtile_kernel(const Kv4WeightsParams wp, const __grid_constant__ CUtensorMap 
           if (++head == Hkv) head = 0;
         }
       }
-      if (!ok)  // copies under way land before the CTA's shared memory is given up
-        for (uint32_t k = g > QS ? g - QS : 0; k < g; ++k) mbar_wait_drain(b_qfull + 8 * (k % QS), (k / QS) & 1);
+      for (uint32_t k = g > QS ? g - QS : 0; k < g; ++k) mbar_wait_drain(b_qfull + 8 * (k % QS), (k / QS) & 1);
     } else if (warp == 2) {
       // ---------------------------------------------------------- log-sum-exps and limits
       constexpr int V = N / 32;

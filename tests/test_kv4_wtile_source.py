@@ -221,3 +221,17 @@ def test_the_model_sees_a_changed_wait(monkeypatch, site, part, was, now):
             except (AssertionError, KeyError):
                 off += 1
     assert off > 0
+
+
+def test_nothing_is_under_way_when_the_block_ends():
+    """Where some role gives a wait up, another may have issued its last product or copy and left its loop
+    without a failed wait: products are awaited before tensor memory is given back, and copies before the block's
+    shared memory is, whether that role's own waits held or not."""
+    for text, loop, drain in ((ISSUE, "while (ok && wk.next()) {", "umma_commit(b_drain + 8 * kt);"),
+                              (QUERY, "while (ok && wk.next()) {", "mbar_wait_drain(b_qfull")):
+        i, depth = text.index(loop) + len(loop), 1
+        while depth:                                             # behind the loop
+            depth += (text[i] == "{") - (text[i] == "}")
+            i += 1
+        between = text[i:text.index(drain)]
+        assert "ok" not in between, between
