@@ -481,3 +481,31 @@ def test_both_kernels_agree(ra):
     c.compare(a, lse)
     c.compare(b, lse)
     assert torch.allclose(a, b, rtol=2e-5, atol=1e-7)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,lens,qlens", [
+    (64, 2, 2, [40000], [1]), (128, 32, 8, [20011, 300], [1, 2]), (128, 24, 2, [6000, 900], [7, 7]), (256, 16, 2, [9001], [2]),
+    (64, 4, 2, [9000, 800, 1], [130, 1, 1]), (128, 8, 2, [9000], [70]), (128, 7, 1, [3000, 700], [40, 50]),
+    (256, 4, 1, [5000, 70], [40, 40])])
+def test_what_is_added_to_old_sums(ra, d, Hq, Hkv, lens, qlens):
+    """A step adds its weights, once, to slots that may hold far more than it adds.
+
+    The tolerance above belongs to the added sums alone; what a slot held is only added to:
+    half a step (2^-24) of the result for each of at most Hkv (rows / 64 + 1) + 1 additions."""
+    c = Case(ra, 13 * d + lens[0], lens, qlens, Hq, Hkv, d, 64)
+    c.new = [0] * len(lens)
+    lse = c.lse(ra)
+    z, q, before = f64(lse), f64(c.q), f64(c.before)
+    sums = E.weights(q, c.keys, c.lens, c.cu, z, True, 1 / math.sqrt(d))
+    got = f64(c.run(ra, lse, max_q_len=max(qlens), check=True))
+    for r, n in enumerate(qlens):
+        rows = n * Hq
+        x = np.abs(q[c.cu[r]:c.cu[r + 1]]).max() * np.abs(c.keys[r]).sum(-1).max() / math.sqrt(d)
+        rel = d * 2.0 ** -23 * x + (min(x, 200) + np.abs(z[np.isfinite(z)]).max()) * 2.0 ** -22 + 2.0 ** -20 + (rows + 2) * 2.0 ** -23
+        old = before[c.slots[r]]
+        adds = Hkv * (rows // Hkv // 64 + 1) + 1
+        tol = rel * sums[r] + adds * 2.0 ** -24 * (old + sums[r]) + rows * 2.0 ** -126
+        assert np.all(np.abs(got[c.slots[r]] - (old + sums[r])) <= tol)
+        assert np.median(tol) < np.median(sums[r]) / 4           # (one that is left out, or added twice, shows)
+    rest = np.setdiff1d(np.arange(len(before)), np.concatenate([np.array(s) for s in c.slots]))
+    assert np.array_equal(got[rest], before[rest])
