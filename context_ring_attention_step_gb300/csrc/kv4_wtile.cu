@@ -36,6 +36,11 @@
 // from shared memory 294; tiles of 192 rows 364; a tile in pieces of 32 columns, each summed while the next
 // comes, 298.  With 8 summing and 4 expanding warps (168 and 104 registers) it took 254, the other two 44 and
 // 232; with 16 and 4 (72, 104; spills) 246, 47 and 215; other splits of the registers of 28 warps 250 to 343.
+// (Its 56, 80 and 64 registers are not without spills either: 208 bytes of the 72 at launch at head_dim
+// 128, 192 at 64, 84 at 256.)
+// A tile with columns that are no rows takes the masked sums, with a limit read for every column: where the
+// heads of a group do not divide the tile that is every tile.  The same call at 28 query and 4 key heads takes
+// 360 us (679 TFLOP/s), at 40 and 8 451 us (774), at 24 and 8 288 us (728).
 // Items (block of keys, head) lie on one line that the CTAs cut evenly; of a block
 // whose heads went to several CTAs the one that brings the last sum adds them, in
 // the CTAs' order.

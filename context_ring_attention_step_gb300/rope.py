@@ -8,7 +8,8 @@ ring attention, or a cache step::
     # training: differentiable in q, k and both weights
     q, k = qk_norm_rope(q, k, rope_positions(cu_seqlens), rotary, q_weight, k_weight)
     o, lse = ring_attention(q, k, v, cu_seqlens, cp_size)
-    # generating: positions from the cache's tables
+    # generating: positions from the cache's tables (which count cached tokens: once kv4_evict has cut a
+    # request, add all that it has dropped of it so far)
     q, k = qk_norm_rope_fwd(q, k, step.positions, rotary, q_weight, k_weight, out=(q, k))
     kv4_store(cache, k, v, step.slot_map)
 

@@ -409,7 +409,8 @@ ra_status ra_noalloc_status(void* stream);
  * interleaved, i < rotary_dim / 2; elements from rotary_dim on are y = u.
  * The weights w [head_dim] are the heads' in common (fp32, or bf16 when
  * weights_bf16; NULL: ones).  f_i is held as the turns per position in 2^-64
- * (ra_rope_turns), so that p f_i loses nothing at any position.
+ * (ra_rope_turns), so that whole turns fall out of p f_i exactly; what is left is off by
+ * at most 2^-53 p turns (f_i comes from a double) and an fp32 rounding of its half turns.
  *
  * positions int32 [num_tokens], device: every token's place in its document
  * (or, while generating, in its request: ra_kv4_tables writes them).  Rows at a
@@ -456,7 +457,8 @@ ra_status ra_qk_norm_rope_workspace_bytes(int32_t head_dim, size_t* bytes);
  * Gradients.  q, k: the forward's inputs; gq, gk: gradients of its results
  * (bf16, or fp32 when g_is_fp32; strides multiples of 8 or 4); dq, dk: bf16.
  * dq_weight, dk_weight fp32 [head_dim], or NULL where they are not wanted: sums
- * over all tokens and heads, in an order that depends on the shape alone.  The
+ * over all tokens and heads, in an order that the shape and the device's number of SMs
+ * fix.  The
  * workspace (256-byte aligned; its content does not matter) is only needed for
  * those.  Outputs lie over nothing else.
  */
@@ -656,7 +658,8 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
  *   weights fp32 [num_pages * page_size]; block_table, kv_lens as in ra_kv4_tables;
  *     1 <= R <= 4096.
  *   budgets int32 [R]; slack, recent, sinks >= 0.
- *   kv_lens_out [R] (may be kv_lens): lengths afterwards.  dropped [R]: tokens that went.
+ *   kv_lens_out [R] (may be kv_lens): lengths afterwards.  dropped [R]: tokens that went
+ *     (ra_kv4_tables' positions count cached tokens: after a cut, all dropped so far are added to them).
  *   src_slots, dst_slots int64 [R, max_moves]: the moves (ra_kv4_move makes them), -1
  *     behind the last one.  A cut of n tokens makes at most min(n, budget) of them.
  *   free_pages [num_free], free_count [1]: pages behind the new lengths are pushed
@@ -669,8 +672,8 @@ ra_status ra_kv4_weights(const ra_kv4_cache* cache, const void* q, int64_t q_str
  *     pages do not fit the free list, and all requests were left alone.
  *   workspace (ra_kv4_evict_workspace_bytes, 256-byte aligned): zero before its first use, not shared
  *     by calls that may overlap.
- * The moves have to be made before new tokens are stored: the pages given back hold their
- * sources.  No output lies over another array, but kv_lens_out may be kv_lens and
+ * A page must not belong to two requests (or twice to one).  The moves have to be made before
+ * new tokens are stored: the pages given back hold their sources.  No output lies over another array, but kv_lens_out may be kv_lens and
  * free_count_out free_count.
  */
 ra_status ra_kv4_evict_workspace_bytes(int32_t num_requests, size_t* bytes);
