@@ -195,14 +195,16 @@ def qk_norm_rope_bwd(q, k, gq, gk, positions, rotary, q_weight=None, k_weight=No
         raise ValueError("out holds the gradient of a weight that is not there or not asked for")
     dqwp = dkwp = ws = ws_bytes = 0
     if weight_grads and not (q_weight is None and k_weight is None):
-        if q_weight is not None:
-            if dqw is None:
-                dqw = torch.empty(D, dtype=_F32, device=dev)
+        if dqw is not None:
             dqwp = _array("dq_weight", dqw, (D,), _F32, dev)
-        if k_weight is not None:
-            if dkw is None:
-                dkw = torch.empty(D, dtype=_F32, device=dev)
+        elif q_weight is not None:
+            dqw = torch.empty(D, dtype=_F32, device=dev)
+            dqwp = dqw.data_ptr()
+        if dkw is not None:
             dkwp = _array("dk_weight", dkw, (D,), _F32, dev)
+        elif k_weight is not None:
+            dkw = torch.empty(D, dtype=_F32, device=dev)
+            dkwp = dkw.data_ptr()
         if workspace is None:
             workspace = qk_norm_rope_workspace(D, dev)
         elif workspace.device != dev or not workspace.is_contiguous():
